@@ -46,12 +46,14 @@ typedef enum {
   PD_ERR_BAD_PAGE = 4,      /* device: a page id or sequence offset was out of range */
   PD_ERR_BAD_LENGTH = 5,    /* device: length_info inconsistent, or more KV chunks than planned */
   PD_ERR_BAD_SLOT = 6,      /* device: an append slot lay beyond max_pages*page_size */
-  PD_ERR_TIMEOUT = 7,       /* device: reserved (the current kernels have no waits) */
+  PD_ERR_TIMEOUT = 7,       /* device: a kernel's bounded wait for its own copies ran out; the
+                               outputs of that call are not valid */
   PD_ERR_WORKSPACE = 8      /* caller workspace too small or misaligned */
 } pd_status;
 
-/* Element types.  PD_E4M3 = OCP float8 e4m3fn (bias 7, max 448, no inf); KV only. */
-typedef enum { PD_F32 = 0, PD_F16 = 1, PD_BF16 = 2, PD_E4M3 = 3 } pd_dtype;
+/* Element types.  PD_E4M3 = OCP float8 e4m3fn (bias 7, max 448, no inf); KV only.
+ * PD_I8 = 8-bit integer codes; block-scaled KV only (pd_..._bs). */
+typedef enum { PD_F32 = 0, PD_F16 = 1, PD_BF16 = 2, PD_E4M3 = 3, PD_I8 = 4 } pd_dtype;
 
 /*
  * What [TVM] fixes when it builds a decode kernel (head counts, head dim, page
@@ -68,7 +70,7 @@ typedef struct {
                                 E4M3 KV (D 128, 16-bit Q); every other accepted shape
                                 runs on the SIMT kernel (pd_last_decode_variant) */
   int32_t q_dtype;           /* pd_dtype of Q: F32, F16 or BF16 */
-  int32_t kv_dtype;          /* pd_dtype of pages: F32, F16, BF16 or E4M3 */
+  int32_t kv_dtype;          /* pd_dtype of pages: F32, F16, BF16 or E4M3 (block-scaled: E4M3 or I8) */
   int32_t out_dtype;         /* pd_dtype of output: F32, F16 or BF16 */
   int32_t sliding_window;    /* 0: length_info is [B] = last_page_len.
                                 1: length_info is [3,B] = (last_page_len,
@@ -270,6 +272,129 @@ pd_status pd_batch_decode_paged_kv_mq(const void* Q, const void* pages,
                                       const pd_decode_desc* desc, pd_stream_t stream);
 
 /*
+ * Block-scaled 8-bit cache — an addition of this library to the per-tensor E4M3 cache.
+ *   pages  [max_pages, 2, H_kv, P, D] of 8-bit codes, PD_E4M3 or PD_I8;
+ *   scales [max_pages, 2, H_kv, P / scale_rows] float32: row `slot` of a page's K (0) or
+ *          V (1) block of a head stands for code * scales[page, K | V, head, slot / scale_rows].
+ * scale_rows divides P; with scale_rows = P a page's head has one scale for K, one for V.
+ * Scales are finite and >= 0; a NaN or infinite one makes the outputs that attend its block
+ * non-finite, and nothing else.  The cache holds K as the decode uses it: rotate (and norm)
+ * the new K rows before the append, and Q before the decode, with pd_qk_norm_rope.
+ *
+ * pd_append_paged_kv_bs — quantises new tokens' K/V into such a cache.
+ * Sequence b brings the tokens append_indptr[b] .. append_indptr[b+1] - 1 of k_new / v_new;
+ * they are the last rows of the sequence that the page table and length_info (as they stand
+ * AFTER the append, the ones the decode then reads) describe.  For each block of scale_rows
+ * rows that receives rows, with amax the largest magnitude of its new rows (per head, K and V
+ * apart) and M = 448 (E4M3) or 127 (I8):
+ *   need  = the smallest power of two 2^k, k >= -126, with amax <= M 2^k;
+ *   scale = need if the block's first row is among the new ones, else max(scale, need), the
+ *           block's earlier codes c becoming RN(c * old_scale / scale);
+ *   code  = RN(x / scale), ties to even.
+ * A power of two makes both quotients exact.  A non-finite new value makes its block's scale
+ * NaN and its new codes 0, until the block is filled again from its first row.  Rows behind the
+ * sequence's last one, and blocks that receive nothing, are left as they were.
+ * Arguments (device pointers): k_new, v_new [T, H_kv, D] of in_dtype (F32, F16, BF16), token t
+ * at element t * k_stride (v_stride), heads contiguous (slices of a fused projection's output
+ * need no copy); append_indptr [B+1] int32, append_indptr[0] = 0, append_indptr[B] = T;
+ * page_table_indptr, page_table_values, length_info as for the decode (of a sliding-window
+ * length_info [3,B] only the first row is read).  D is 64, 128 or 256; pages 16-byte aligned.
+ * A sequence whose table does not hold its new rows is skipped (PD_ERR_BAD_LENGTH on the
+ * device), as is a block whose page id is out of range (PD_ERR_BAD_PAGE).  Pages that receive
+ * rows must belong to one sequence (a shared prefix is full and receives none).  k_stride,
+ * v_stride >= H_kv * D.  The decode may follow with PD_DECODE_EARLY_INPUTS.
+ */
+pd_status pd_append_paged_kv_bs(void* pages, float* scales, const void* k_new, const void* v_new,
+                                const int32_t* append_indptr, const int32_t* page_table_indptr,
+                                const int32_t* page_table_values, const int32_t* length_info,
+                                int32_t T, int32_t B, int32_t H_kv, int32_t D, int32_t page_size,
+                                int32_t scale_rows, int64_t max_pages, int64_t nnz_pages,
+                                int64_t k_stride, int64_t v_stride, int32_t in_dtype,
+                                int32_t kv_dtype, pd_stream_t stream);
+
+/*
+ * pd_batch_decode_paged_kv_bs — pd_batch_decode_paged_kv (q_len = 1) and
+ * pd_batch_decode_paged_kv_mq (q_len > 1) over a block-scaled cache:
+ *   s_r = sm_scale * log2(e) * ks q.c_r,  out = sum_r 2^(s_r) vs e_r / sum_r 2^(s_r),
+ * c_r, e_r row r's codes and ks, vs its block's scales.  Shapes, page table, windows and
+ * sinks, desc->sink, the host copies, splits, workspaces and capture are those of the two
+ * entry points; there are no RoPE arguments (see above), desc->kv_dtype is PD_E4M3 or PD_I8,
+ * desc->k_scale and v_scale are not read, and a caller workspace holds
+ * pd_workspace_size_bs(desc, q_len, scale_rows) bytes.  Q may be F32, F16 or BF16 whatever the
+ * codes.  With PD_DECODE_EARLY_INPUTS the scales, like the pages, are read only after the
+ * previous kernel.
+ * Arithmetic: F16 and BF16 Q with D 64 or 128 and page_size and scale_rows multiples of 16 run
+ * on tensor cores (Q and the codes enter exactly, the weights 2^(s - n) vs are rounded once to
+ * f16 against their own running maximum n, sums in fp32); every other shape runs an fp32 kernel
+ * without tensor cores, for q_len = 1 (q_len > 1: PD_ERR_UNSUPPORTED).
+ */
+pd_status pd_batch_decode_paged_kv_bs(const void* Q, const void* pages, const float* scales,
+                                      const int32_t* page_table_indptr,
+                                      const int32_t* page_table_values, const int32_t* length_info,
+                                      void* output, float* lse, int32_t q_len, int32_t scale_rows,
+                                      float sm_scale, const pd_decode_desc* desc,
+                                      pd_stream_t stream);
+
+/*
+ * pd_qk_norm_rope — the per-head RMS norm of queries and keys and the position rotation, in one
+ * pass (the order norm, rotation, cache update).  For token t, head h, x the head's D values:
+ *   y_d = x_d / sqrt(mean(x^2) + eps) * (w_d + weight_offset); without weights y = x (no norm;
+ *   Q's and K's are independent);
+ *   the first rotary_dim dims are rotated by angle_i = positions[t] * inv_freq[i], in the pairs
+ *   (i, i + rotary_dim / 2) (rotary_mode 1) or (2i, 2i + 1) (rotary_mode 2), and multiplied by
+ *   attention_factor: (a, b) <- (a cos - b sin, b cos + a sin) * attention_factor; the others
+ *   pass.  rotary_mode 0 or rotary_dim 0: no rotation.
+ * Arithmetic in fp32 (positions times frequencies in 64-bit fixed point, exact modulo a turn),
+ * one rounding at the end.
+ */
+typedef struct {
+  int32_t T;                  /* tokens */
+  int32_t H_q, H_k;           /* query and key heads; either may be 0 */
+  int32_t D;                  /* head dim, 1 to 512 */
+  int32_t dtype;              /* F32, F16 or BF16, of q, k, q_out and k_out */
+  int32_t weight_dtype;       /* F32, F16 or BF16, of q_weight and k_weight */
+  int32_t rotary_mode;        /* 0 none, 1 rotate-half, 2 interleaved pairs */
+  int32_t rotary_dim;         /* dims rotated: even, at most D */
+  float eps;                  /* >= 0 */
+  float weight_offset;        /* 0, or 1 for weights stored around zero */
+  float attention_factor;     /* 1, or the factor of a context extension */
+  int64_t q_stride, k_stride;                    /* elements from token to token */
+  int64_t q_head_stride, k_head_stride;          /* elements from head to head; the last dim is contiguous */
+  int64_t q_out_stride, k_out_stride;
+  int64_t q_out_head_stride, k_out_head_stride;
+} pd_qk_desc;
+
+/*
+ * Arguments (device pointers): q [T, H_q, D], k [T, H_k, D], q_out, k_out alike, by the
+ * strides of desc; q_weight, k_weight [D] or NULL; positions [T] int32; inv_freq
+ * [rotary_dim / 2] float64, radians per position (pd_rope_frequencies, copied to the device).
+ * q_out may be q and k_out may be k (same strides); outputs must not overlap otherwise.
+ * Heads whose rows are 16-byte aligned, D a multiple of 8 up to 256 and a rotated part that is
+ * a multiple of 16 (mode 1) or 8 (mode 2) run with 16-byte accesses; the rest element by element.
+ */
+pd_status pd_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                          const int32_t* positions, const double* inv_freq, void* q_out, void* k_out,
+                          const pd_qk_desc* desc, pd_stream_t stream);
+
+/*
+ * pd_rope_frequencies — host-only: inv_freq[i], i < n = rotary_dim / 2 (HOST pointer), from
+ * f_i = rope_theta^(-i / n):
+ *   PD_ROPE_PLAIN   f_i
+ *   PD_ROPE_LINEAR  f_i / factor                                  (positions interpolated)
+ *   PD_ROPE_THETA   rope_theta replaced by rope_theta * factor^(n / (n - 1)): the highest
+ *                   frequency kept, the lowest divided by factor
+ *   PD_ROPE_PARTS   (1 - g) f_i / factor + g f_i, g = clamp((original_context f_i / 2 pi -
+ *                   low_turns) / (high_turns - low_turns), 0, 1): frequencies that turn more than
+ *                   high_turns times over the original context kept, those below low_turns
+ *                   divided by factor, a ramp between
+ * Arguments a form does not use are ignored.
+ */
+enum { PD_ROPE_PLAIN = 0, PD_ROPE_LINEAR = 1, PD_ROPE_THETA = 2, PD_ROPE_PARTS = 3 };
+pd_status pd_rope_frequencies(int32_t rotary_dim, double rope_theta, int32_t scaling, double factor,
+                              double original_context, double low_turns, double high_turns,
+                              double* inv_freq);
+
+/*
  * merge_state_inplace — [TVM] `merge_state_inplace`.
  * For every (n, h):  m = max(S, S_o);  w = 2^(S - m);  w_o = 2^(S_o - m);
  *   V[n,h,:] <- V * w/(w+w_o) + V_other * w_o/(w+w_o);  S[n,h] <- log2(w + w_o) + m.
@@ -380,6 +505,9 @@ size_t pd_workspace_size(const pd_decode_desc* desc);
 
 /* The same for pd_batch_decode_paged_kv_mq with q_len query tokens per sequence. */
 size_t pd_workspace_size_mq(const pd_decode_desc* desc, int32_t q_len);
+
+/* The same for pd_batch_decode_paged_kv_bs. */
+size_t pd_workspace_size_bs(const pd_decode_desc* desc, int32_t q_len, int32_t scale_rows);
 
 /* Zero-fill a caller-provided workspace before its first use (enqueued on stream). */
 pd_status pd_workspace_init(void* workspace, size_t bytes, pd_stream_t stream);

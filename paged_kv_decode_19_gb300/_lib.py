@@ -37,6 +37,8 @@ DTYPE_CODES = {
     torch.bfloat16: 2,
     torch.float8_e4m3fn: 3,
 }
+# codes of a block-scaled cache (the _bs entry points)
+BS_DTYPE_CODES = {torch.float8_e4m3fn: 3, torch.int8: 4}
 DTYPE_NAMES = {"f32": 0, "f16": 1, "bf16": 2, "e4m3": 3}
 
 # Every entry point declared in include/pageddecode.h.
@@ -54,6 +56,11 @@ EXPORTS = (
     "pd_workspace_init",
     "pd_release_stream_workspace",
     "pd_plan",
+    "pd_append_paged_kv_bs",
+    "pd_batch_decode_paged_kv_bs",
+    "pd_workspace_size_bs",
+    "pd_qk_norm_rope",
+    "pd_rope_frequencies",
     "pd_check_device_errors",
     "pd_last_decode_variant",
     "pd_get_last_error_string",
@@ -94,6 +101,30 @@ class DecodeDesc(ctypes.Structure):
     ]
 
 
+class QkDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int32),
+        ("H_q", ctypes.c_int32),
+        ("H_k", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("rotary_mode", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+        ("attention_factor", ctypes.c_float),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64),
+        ("k_out_stride", ctypes.c_int64),
+        ("q_out_head_stride", ctypes.c_int64),
+        ("k_out_head_stride", ctypes.c_int64),
+    ]
+
+
 def lib():
     """Load libpageddecode.so (raises if it has not been built)."""
     global _lib
@@ -127,6 +158,18 @@ def lib():
             L.pd_append_paged_kv_rope.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i64, i32,
                                                   i32, f32, f32, i32, f32, f32, P]
             L.pd_append_paged_kv_rope.restype = i32
+            L.pd_append_paged_kv_bs.argtypes = [P] * 8 + [i32] * 6 + [i64] * 4 + [i32, i32, P]
+            L.pd_append_paged_kv_bs.restype = i32
+            L.pd_batch_decode_paged_kv_bs.argtypes = [P] * 8 + [i32, i32, f32,
+                                                                ctypes.POINTER(DecodeDesc), P]
+            L.pd_batch_decode_paged_kv_bs.restype = i32
+            L.pd_workspace_size_bs.argtypes = [ctypes.POINTER(DecodeDesc), i32, i32]
+            L.pd_workspace_size_bs.restype = ctypes.c_size_t
+            L.pd_qk_norm_rope.argtypes = [P] * 8 + [ctypes.POINTER(QkDesc), P]
+            L.pd_qk_norm_rope.restype = i32
+            f64 = ctypes.c_double
+            L.pd_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, P]
+            L.pd_rope_frequencies.restype = i32
             L.pd_workspace_size.argtypes = [ctypes.POINTER(DecodeDesc)]
             L.pd_workspace_size.restype = ctypes.c_size_t
             L.pd_workspace_init.argtypes = [P, ctypes.c_size_t, P]
@@ -284,6 +327,182 @@ def batch_decode_paged_kv_mq(Q, pages, page_table_indptr, page_table_values, len
         _ptr(lse), int(q_len), int(rotary_mode), float(rope_scale), float(rope_theta),
         float(sm_scale), ctypes.byref(desc), _stream(stream)))
     return output, lse
+
+
+def _on_current_device(*tensors):
+    """The kernels run on the current device and read these through raw addresses."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must be on the GPU")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device, cuda:{dev}")
+
+
+def _bs_shape(pages, scales):
+    """(max_pages, H_kv, P, D, scale_rows) of a block-scaled cache, checked."""
+    if pages.dim() != 5 or pages.shape[1] != 2 or pages.dtype not in BS_DTYPE_CODES:
+        raise ValueError("pages must be [max_pages, 2, H_kv, P, D] of float8_e4m3fn or int8")
+    max_pages, _, H_kv, P, D = pages.shape
+    if scales.dtype != torch.float32 or scales.dim() != 4 or scales.shape[:3] != pages.shape[:3]:
+        raise ValueError("scales must be float32 [max_pages, 2, H_kv, P / scale_rows]")
+    n_sb = scales.shape[3]
+    if n_sb < 1 or P % n_sb:
+        raise ValueError("the blocks of a page must divide it")
+    return max_pages, H_kv, P, D, P // n_sb
+
+
+def _bs_table(page_table_indptr, page_table_values, length_info, B):
+    for t in (page_table_indptr, page_table_values, length_info):
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError("the page table and length_info must be int32")
+    if page_table_indptr.numel() != B + 1 or length_info.numel() not in (B, 3 * B):
+        raise ValueError("page_table_indptr [B+1] and length_info [B] or [3,B]")
+
+
+def batch_decode_paged_kv_bs(Q, pages, scales, page_table_indptr, page_table_values, length_info,
+                             output, lse, sm_scale=None, *, num_splits=0, workspace=None,
+                             early_inputs=False, sink=None, host_meta=None, stream=None):
+    """pd_batch_decode_paged_kv_bs: decode over 8-bit pages (float8_e4m3fn or int8) with
+    scales [max_pages, 2, H_kv, blocks per page] float32.  Q [B, H_qo, D], or
+    [B, q_len, H_qo, D] for several query tokens per sequence (causal among them); output
+    like Q, lse [B, H_qo] or [B, q_len, H_qo].  K is used as stored and Q as given: rotate
+    both with qk_norm_rope."""
+    max_pages, H_kv, P, D, scale_rows = _bs_shape(pages, scales)
+    shape = Q.shape
+    if len(shape) not in (3, 4) or shape[-1] != D:
+        raise ValueError("Q must be [B, H_qo, D] or [B, q_len, H_qo, D]")
+    if output.shape != shape or lse.shape != shape[:-1] or lse.dtype != torch.float32:
+        raise ValueError("output must be shaped like Q and lse float32 like its heads")
+    B, H_qo, q_len = shape[0], shape[-2], shape[1] if len(shape) == 4 else 1
+    _bs_table(page_table_indptr, page_table_values, length_info, B)
+    desc = DecodeDesc(
+        B, H_qo, H_kv, D, P, DTYPE_CODES[Q.dtype], BS_DTYPE_CODES[pages.dtype],
+        DTYPE_CODES[output.dtype], int(length_info.dim() == 2), int(num_splits), max_pages,
+        0 if page_table_values is None else page_table_values.numel(), 0, 1.0, 1.0,
+        DECODE_EARLY_INPUTS if early_inputs else 0,
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _sink_ptr(sink, H_qo),
+        None if host_meta is None else _host_i32(host_meta[0], B + 1),
+        None if host_meta is None else _host_i32(host_meta[1], length_info.numel()))
+    _on_current_device(Q, pages, scales, page_table_indptr, page_table_values, length_info, output,
+                       lse, workspace, sink)
+    _check(lib().pd_batch_decode_paged_kv_bs(
+        _ptr(Q), _ptr(pages), _ptr(scales), _ptr(page_table_indptr), _ptr(page_table_values),
+        _ptr(length_info), _ptr(output), _ptr(lse), q_len, scale_rows,
+        D ** -0.5 if sm_scale is None else sm_scale, ctypes.byref(desc), _stream(stream)))
+    return output, lse
+
+
+def workspace_size_bs(desc: DecodeDesc, q_len: int, scale_rows: int) -> int:
+    return int(lib().pd_workspace_size_bs(ctypes.byref(desc), q_len, scale_rows))
+
+
+def append_paged_kv_bs(pages, scales, k_new, v_new, append_indptr, page_table_indptr,
+                       page_table_values, length_info, stream=None):
+    """pd_append_paged_kv_bs: quantises new tokens' K/V [T, H_kv, D] into 8-bit pages with
+    block scales (both updated in place).  append_indptr [B+1] int32: sequence b brings
+    tokens append_indptr[b] .. append_indptr[b+1] - 1, its last rows in the page table and
+    length_info as they stand after the append.  k_new and v_new may be slices of a larger
+    tensor along the heads (any token stride)."""
+    max_pages, H_kv, P, D, scale_rows = _bs_shape(pages, scales)
+    T = k_new.shape[0]
+    if k_new.shape != (T, H_kv, D) or v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+        raise ValueError("k_new and v_new must be [T, H_kv, D] of one dtype")
+    ks, vs = k_new.stride(), v_new.stride()
+    if T and ((ks[2] != 1 or vs[2] != 1) or (H_kv > 1 and (ks[1] != D or vs[1] != D))):
+        raise ValueError("the heads of k_new and v_new must be contiguous")
+    B = append_indptr.numel() - 1
+    if append_indptr.dtype != torch.int32 or B < 0:
+        raise ValueError("append_indptr must be int32 [B+1]")
+    _bs_table(page_table_indptr, page_table_values, length_info, B)
+    row = H_kv * D
+    _on_current_device(pages, scales, k_new, v_new, append_indptr, page_table_indptr,
+                       page_table_values, length_info)
+    _check(lib().pd_append_paged_kv_bs(
+        _ptr(pages), _ptr(scales), k_new.data_ptr(), v_new.data_ptr(), _ptr(append_indptr),
+        _ptr(page_table_indptr), _ptr(page_table_values), _ptr(length_info), T, B, H_kv, D, P,
+        scale_rows, max_pages, page_table_values.numel(), ks[0] if T > 1 else row,
+        vs[0] if T > 1 else row, DTYPE_CODES[k_new.dtype], BS_DTYPE_CODES[pages.dtype],
+        _stream(stream)))
+    return pages, scales
+
+
+ROPE_SCALINGS = {None: 0, "linear": 1, "theta": 2, "parts": 3}
+
+
+def rope_frequencies(rotary_dim, rope_theta=1e4, scaling=None, factor=1.0, original_context=0.0,
+                     low_turns=1.0, high_turns=4.0, device="cuda"):
+    """pd_rope_frequencies: float64 [rotary_dim / 2] radians per position on `device`, plain or
+    extended to longer contexts ("linear", "theta" or "parts" scaling by `factor`)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {tuple(ROPE_SCALINGS)}")
+    out = (ctypes.c_double * max(1, int(rotary_dim) // 2))()
+    _check(lib().pd_rope_frequencies(int(rotary_dim), float(rope_theta), ROPE_SCALINGS[scaling],
+                                     float(factor), float(original_context), float(low_turns),
+                                     float(high_turns), out))
+    return torch.tensor(list(out), dtype=torch.float64, device=device)
+
+
+def _heads(t, T, D, dtype, what, written=False):
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or t.dtype != dtype:
+        raise ValueError(f"{what} must be [T, heads, D] like the other rows")
+    st = t.stride()
+    if D > 1 and st[2] != 1:
+        raise ValueError(f"the last dim of {what} must be contiguous")
+    if written and ((T > 1 and st[0] == 0) or (t.shape[1] > 1 and st[1] == 0)):
+        raise ValueError(f"{what} must not be an expanded tensor")
+    return st
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out=None, k_out=None, *,
+                 rotary_mode=1, eps=1e-6, weight_offset=0.0, attention_factor=1.0, stream=None):
+    """pd_qk_norm_rope: RMS norm of each head of q [T, H_q, D] and k [T, H_k, D] (weights [D],
+    or None: no norm), then the rotation of the first 2 * len(inv_freq) dims at positions
+    (int32 [T]; rotary_mode 1 rotate-half, 2 interleaved; inv_freq None: no rotation).
+    k may be None.  q and k may be slices along the heads of a projection's output; q_out and
+    k_out default to new tensors and may be q and k.  Returns (q_out, k_out)."""
+    T, H_q, D = q.shape
+    dtype = q.dtype
+    if q_out is None:
+        q_out = torch.empty((T, H_q, D), dtype=dtype, device=q.device)
+    qs, qos = _heads(q, T, D, dtype, "q"), _heads(q_out, T, D, dtype, "q_out", True)
+    if q_out.shape[1] != H_q:
+        raise ValueError("q_out must be shaped like q")
+    H_k, ks, kos = 0, (0, 0, 1), (0, 0, 1)
+    if k is not None:
+        H_k = k.shape[1]
+        if k_out is None:
+            k_out = torch.empty((T, H_k, D), dtype=dtype, device=k.device)
+        ks, kos = _heads(k, T, D, dtype, "k"), _heads(k_out, T, D, dtype, "k_out", True)
+        if k_out.shape[1] != H_k:
+            raise ValueError("k_out must be shaped like k")
+    w = q_weight if q_weight is not None else k_weight
+    for x in (q_weight, k_weight):
+        if x is not None and (x.shape != (D,) or x.dtype != w.dtype):
+            raise ValueError("the weights must be [D], of one dtype")
+    rd = 0
+    if inv_freq is not None and rotary_mode:
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be float64 [rotary_dim / 2]")
+        if positions.dtype != torch.int32 or positions.shape != (T,):
+            raise ValueError("positions must be int32 [T]")
+        rd = 2 * inv_freq.numel()
+    _on_current_device(q, k, q_weight, k_weight, positions if rd else None,
+                       inv_freq if rd else None, q_out, k_out)
+    desc = QkDesc(T, H_q, H_k, D, DTYPE_CODES[dtype], 0 if w is None else DTYPE_CODES[w.dtype],
+                  int(rotary_mode), rd, eps, weight_offset, attention_factor, qs[0], ks[0], qs[1],
+                  ks[1], qos[0], kos[0], qos[1], kos[1])
+    _check(lib().pd_qk_norm_rope(
+        q.data_ptr(), None if k is None else k.data_ptr(), _ptr(q_weight), _ptr(k_weight),
+        _ptr(positions) if rd else None, _ptr(inv_freq) if rd else None, q_out.data_ptr(),
+        None if k is None else k_out.data_ptr(), ctypes.byref(desc), _stream(stream)))
+    return q_out, k_out
 
 
 def merge_state_inplace(V, S, V_other, S_other, stream=None):

@@ -3,6 +3,7 @@
 // include/pageddecode.h is defined here, except pd_batch_decode_paged_kv_noalloc
 // (decode_noalloc.cu), which calls pd_batch_decode_paged_kv.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdio>
@@ -57,6 +58,8 @@ struct DeviceState {
   // [mma][q_dtype][kv_dtype][D 64/128/256][kernel RoPE mode 0..4][single / multi-query /
   // pages of 8 rows]; 0 = not yet known
   int occupancy[2][4][4][3][5][3] = {};
+  // the same of the block-scaled kernels: [mma][q_dtype][e4m3 / int8][D][single / multi-query]
+  int bs_occupancy[2][4][2][3][2] = {};
 };
 constexpr int kMaxDevices = 64;
 static DeviceState g_dev[kMaxDevices];
@@ -86,6 +89,7 @@ static int elem_bytes(int dt) {
     case kF16: return 2;
     case kBF16: return 2;
     case kE4M3: return 1;
+    case kI8: return 1;
   }
   return 0;
 }
@@ -102,8 +106,16 @@ static int arena_zero(void*, void* p, size_t bytes, void* st) {
 }
 static const ArenaOps kCudaArenaOps = {nullptr, arena_alloc, arena_release, arena_zero};
 
+// An 8-bit cache with one fp32 scale per (page, K | V, KV head, block of scale_rows rows):
+// scales [max_pages, 2, H_kv, page_size / scale_rows].
+struct BlockScales {
+  const float* scales;
+  int scale_rows;
+};
+
 // ---------------------------------------------------------------------------- validation
-static pd_status validate_desc(const pd_decode_desc* d) {
+// bs: the desc is of a block-scaled cache (its k_scale, v_scale are not read).
+static pd_status validate_desc(const pd_decode_desc* d, const BlockScales* bs = nullptr) {
   if (!d) return fail(PD_ERR_INVALID_ARG, "desc is NULL");
   if (d->B < 0) return fail(PD_ERR_INVALID_ARG, "B < 0");
   if (d->H_kv <= 0 || d->H_qo <= 0 || d->H_qo % d->H_kv != 0)
@@ -113,7 +125,12 @@ static pd_status validate_desc(const pd_decode_desc* d) {
   if (d->page_size <= 0 || d->page_size > 256) return fail(PD_ERR_INVALID_ARG, "page_size must be in [1, 256]");
   if (d->q_dtype != kF32 && d->q_dtype != kF16 && d->q_dtype != kBF16)
     return fail(PD_ERR_INVALID_ARG, "q_dtype must be F32, F16 or BF16");
-  if (d->kv_dtype < kF32 || d->kv_dtype > kE4M3) return fail(PD_ERR_INVALID_ARG, "bad kv_dtype");
+  if (bs) {
+    if (d->kv_dtype != kE4M3 && d->kv_dtype != kI8)
+      return fail(PD_ERR_INVALID_ARG, "a block-scaled cache is E4M3 or I8");
+  } else if (d->kv_dtype < kF32 || d->kv_dtype > kE4M3) {
+    return fail(PD_ERR_INVALID_ARG, "bad kv_dtype");
+  }
   if (d->out_dtype != kF32 && d->out_dtype != kF16 && d->out_dtype != kBF16)
     return fail(PD_ERR_INVALID_ARG, "out_dtype must be F32, F16 or BF16");
   if (d->max_pages <= 0 && d->B > 0) return fail(PD_ERR_INVALID_ARG, "max_pages must be positive");
@@ -123,6 +140,11 @@ static pd_status validate_desc(const pd_decode_desc* d) {
   if (d->num_splits < 0) return fail(PD_ERR_INVALID_ARG, "num_splits < 0");
   if (d->flags & ~(PD_DECODE_EARLY_INPUTS | PD_DECODE_K_ROTATED))
     return fail(PD_ERR_INVALID_ARG, "unknown bits in flags");
+  if (bs) {
+    if (bs->scale_rows <= 0 || d->page_size % bs->scale_rows != 0)
+      return fail(PD_ERR_INVALID_ARG, "scale_rows must divide page_size");
+    return PD_OK;
+  }
   if (d->kv_dtype == kE4M3 && !(d->k_scale > 0.f && d->v_scale > 0.f && std::isfinite(d->k_scale) &&
                                 std::isfinite(d->v_scale)))
     return fail(PD_ERR_INVALID_ARG, "E4M3 KV needs finite positive k_scale and v_scale");
@@ -181,6 +203,49 @@ static bool mma_path(const pd_decode_desc* d, const void* pages) {
   if (d->kv_dtype == kBF16 || d->kv_dtype == kF16) return d->D == 64 || d->D == 128;
   if (d->kv_dtype == kE4M3) return d->D == 128 && (d->q_dtype == kBF16 || d->q_dtype == kF16);
   return false;
+}
+
+// The same for a block-scaled cache: 16-row tiles whose rows share a scale.
+static bool bs_mma_path(const pd_decode_desc* d, const BlockScales* bs) {
+  return d->page_size % 16 == 0 && bs->scale_rows % 16 == 0 && (d->D == 64 || d->D == 128) &&
+         (d->q_dtype == kBF16 || d->q_dtype == kF16);
+}
+
+static cudaError_t bs_mma_dispatch(const DecodeParams& p, const CUtensorMap& tm, int q_dtype, int kv_dtype,
+                                   dim3 grid, cudaStream_t st, MmaConfig* cfg) {
+  return kv_dtype == kE4M3 ? launch_bs_e4m3(p, tm, q_dtype, grid, st, cfg)
+                           : launch_bs_int(p, tm, q_dtype, grid, st, cfg);
+}
+
+// The pages of an 8-bit cache as TMA boxes of 16 rows: [max_pages * 2 * H_kv, P, D] bytes,
+// swizzled by row size (the layout decode_bs.cuh reads).
+static pd_status page_boxes(const pd_decode_desc& d, const void* pages, CUtensorMap* tm) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+  static std::atomic<Encode> known{nullptr};
+  Encode encode = known.load();
+  if (!encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDriverEntryPointByVersion");
+    if (!fn || found != cudaDriverEntryPointSuccess)
+      return fail(PD_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    encode = reinterpret_cast<Encode>(fn);
+    known.store(encode);
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)d.D, (cuuint64_t)d.page_size, (cuuint64_t)d.max_pages * 2 * d.H_kv};
+  const cuuint64_t strides[2] = {(cuuint64_t)d.D, (cuuint64_t)d.D * d.page_size};
+  const cuuint32_t box[3] = {(cuuint32_t)d.D, 16, 1}, step[3] = {1, 1, 1};
+  const CUresult r = encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pages), dims, strides, box,
+                            step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            d.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PD_ERR_CUDA, "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")");
+  return PD_OK;
 }
 
 static cudaError_t mma_dispatch(const DecodeParams& p, int q_dtype, int kv_dtype, dim3 grid,
@@ -296,6 +361,31 @@ static pd_status occupancy_for(const pd_decode_desc* d, bool use_mma, int rm, in
   return PD_OK;
 }
 
+static pd_status bs_occupancy_for(const pd_decode_desc* d, bool use_mma, int* ctas, DeviceState* ds, int q_len) {
+  const int di = d->D == 64 ? 0 : d->D == 128 ? 1 : 2;
+  int& cached = ds->bs_occupancy[use_mma ? 1 : 0][d->q_dtype & 3][d->kv_dtype == kI8 ? 1 : 0][di][q_len > 1 ? 1 : 0];
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (cached == 0) {
+    DecodeParams p{};
+    p.D = d->D;
+    p.P = d->page_size;
+    p.q_len = q_len;
+    cudaError_t e;
+    int n = 0;
+    if (use_mma) {
+      MmaConfig cfg{};
+      e = bs_mma_dispatch(p, CUtensorMap{}, d->q_dtype, d->kv_dtype, dim3(1), nullptr, &cfg);
+      n = cfg.ctas_per_sm;
+    } else {
+      e = launch_decode_simt_bs(p, d->q_dtype, d->kv_dtype, dim3(1), nullptr, &n);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
+    cached = std::max(n, 1);
+  }
+  *ctas = cached;
+  return PD_OK;
+}
+
 static size_t workspace_size_q(const pd_decode_desc* desc, int q_len) {
   if (validate_desc(desc) != PD_OK || q_len < 1) return 0;
   DeviceState* ds = nullptr;
@@ -323,6 +413,19 @@ size_t pd_workspace_size_mq(const pd_decode_desc* desc, int32_t q_len) {
   return workspace_size_q(desc, q_len);
 }
 
+size_t pd_workspace_size_bs(const pd_decode_desc* desc, int32_t q_len, int32_t scale_rows) {
+  const BlockScales bs{nullptr, scale_rows};
+  if (validate_desc(desc, &bs) != PD_OK || q_len < 1) return 0;
+  DeviceState* ds = nullptr;
+  if (device_state(&ds) != PD_OK) return 0;
+  const bool mma = bs_mma_path(desc, &bs);
+  int ctas = 1, mode, grid;
+  if ((!mma && q_len > 1) || bs_occupancy_for(desc, mma, &ctas, ds, q_len) != PD_OK) return 0;
+  size_t ws;
+  plan_impl(desc, ds->num_sms, ctas, mma ? kMmaWarps : 1, &mode, &grid, &ws, q_len);
+  return ws;
+}
+
 pd_status pd_workspace_init(void* workspace, size_t bytes, pd_stream_t stream) {
   if (!workspace && bytes) return fail(PD_ERR_INVALID_ARG, "workspace is NULL");
   cudaError_t e = cudaMemsetAsync(workspace, 0, bytes, (cudaStream_t)stream);
@@ -332,14 +435,16 @@ pd_status pd_workspace_init(void* workspace, size_t bytes, pd_stream_t stream) {
 
 }  // extern "C"
 
-// Both decode entry points: q_len query tokens per sequence (1: batch_decode_paged_kv).
+// All decode entry points: q_len query tokens per sequence (1: batch_decode_paged_kv);
+// bs: the cache's block scales (nullptr: a cache without).
 static pd_status decode_call(const void* Q, const void* pages, const int32_t* page_table_indptr,
                              const int32_t* page_table_values, const int32_t* length_info,
                              const int32_t* k_rope_pos_offset, const int32_t* q_rope_position,
                              void* output, float* lse, int q_len, int32_t rotary_mode,
                              float rope_scale, float rope_theta, float sm_scale,
-                             const pd_decode_desc* desc, pd_stream_t stream) {
-  pd_status st = validate_desc(desc);
+                             const pd_decode_desc* desc, pd_stream_t stream,
+                             const BlockScales* bs = nullptr) {
+  pd_status st = validate_desc(desc, bs);
   if (st != PD_OK) return st;
   const pd_decode_desc& d = *desc;
   if (rotary_mode < 0 || rotary_mode > 2) return fail(PD_ERR_INVALID_ARG, "rotary_mode must be 0, 1 or 2");
@@ -365,17 +470,29 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   if ((reinterpret_cast<uintptr_t>(pages) % 16) != 0 || (reinterpret_cast<uintptr_t>(Q) % 16) != 0)
     return fail(PD_ERR_INVALID_ARG, "Q and pages must be 16-byte aligned");
 
+  if (bs && (!bs->scales || (reinterpret_cast<uintptr_t>(bs->scales) % 4) != 0))
+    return fail(PD_ERR_INVALID_ARG, "scales is NULL or not 4-byte aligned");
+
+  const bool use_mma = bs ? bs_mma_path(desc, bs) : mma_path(desc, pages);
+  if (bs && q_len > 1 && !use_mma)
+    return fail(PD_ERR_UNSUPPORTED, "several query tokens run on the tensor-core kernel only: f16/bf16 Q, "
+                                    "D 64 or 128, page_size and scale_rows multiples of 16");
   DeviceState* ds = nullptr;
   st = device_state(&ds);
   if (st != PD_OK) return st;
-  const bool use_mma = mma_path(desc, pages);
-  if (q_len > 1 && (!use_mma || d.page_size % 16 != 0))
+  if (!bs && q_len > 1 && (!use_mma || d.page_size % 16 != 0))
     return fail(PD_ERR_UNSUPPORTED, "multi-query decode runs on the tensor-core kernel only: "
                                     "f16/bf16 (D 64 or 128) or E4M3 (D 128) KV, page size a multiple of 16");
   int ctas = 1;
   const bool k_rotated = rotary_mode != 0 && (d.flags & PD_DECODE_K_ROTATED);
-  st = occupancy_for(desc, use_mma, rotary_mode + (k_rotated ? 2 : 0), &ctas, ds, q_len);
+  st = bs ? bs_occupancy_for(desc, use_mma, &ctas, ds, q_len)
+          : occupancy_for(desc, use_mma, rotary_mode + (k_rotated ? 2 : 0), &ctas, ds, q_len);
   if (st != PD_OK) return st;
+  CUtensorMap tm{};
+  if (bs && use_mma) {
+    st = page_boxes(d, pages, &tm);
+    if (st != PD_OK) return st;
+  }
   int mode = 0, grid_blocks = 0;
   size_t ws_need = 0;
   const int wpb = use_mma ? kMmaWarps : 1;
@@ -478,16 +595,25 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   p.k_rotated = k_rotated ? 1 : 0;
   p.sink = d.sink;
   const double log2e = 1.4426950408889634073599246810019;
-  const double kdeq = d.kv_dtype == kE4M3 ? (double)d.k_scale : 1.0;
+  const double kdeq = d.kv_dtype == kE4M3 && !bs ? (double)d.k_scale : 1.0;
   p.score_scale = (float)((double)sm_scale * log2e * kdeq);
   p.q_prescale = p.score_scale;
-  p.out_scale = d.kv_dtype == kE4M3 ? d.v_scale : 1.f;
+  p.out_scale = d.kv_dtype == kE4M3 && !bs ? d.v_scale : 1.f;
+  if (bs) {
+    p.scales = bs->scales;
+    p.scale_rows = bs->scale_rows;
+    p.n_sb = d.page_size / bs->scale_rows;
+  }
   if (rotary_mode) rope_table(rope_scale, rope_theta, d.D, p.rope_F);
   if (d.host_indptr && d.host_length_info) fill_host_plan(d, p);
 
   const dim3 grid((unsigned)grid_blocks);
   cudaError_t e;
-  if (use_mma) {
+  if (bs) {
+    e = use_mma ? bs_mma_dispatch(p, tm, d.q_dtype, d.kv_dtype, grid, s, nullptr)
+                : launch_decode_simt_bs(p, d.q_dtype, d.kv_dtype, grid, s);
+    t_last_variant = use_mma ? "mma" : "simt";
+  } else if (use_mma) {
     e = mma_dispatch(p, d.q_dtype, d.kv_dtype, grid, s, nullptr);
     t_last_variant = "mma";
   } else {
@@ -530,6 +656,21 @@ pd_status pd_batch_decode_paged_kv_mq(const void* Q, const void* pages,
   return decode_call(Q, pages, page_table_indptr, page_table_values, length_info,
                      k_rope_pos_offset, q_rope_position, output, lse, q_len, rotary_mode,
                      rope_scale, rope_theta, sm_scale, desc, stream);
+}
+
+pd_status pd_batch_decode_paged_kv_bs(const void* Q, const void* pages, const float* scales,
+                                      const int32_t* page_table_indptr,
+                                      const int32_t* page_table_values, const int32_t* length_info,
+                                      void* output, float* lse, int32_t q_len, int32_t scale_rows,
+                                      float sm_scale, const pd_decode_desc* desc,
+                                      pd_stream_t stream) {
+  if (q_len < 1) return fail(PD_ERR_INVALID_ARG, "q_len must be >= 1");
+  if (desc && q_len > 1 && desc->sliding_window)
+    return fail(PD_ERR_UNSUPPORTED, "multi-query decode has no sliding-window form");
+  if (desc && (long long)desc->B * q_len > INT_MAX) return fail(PD_ERR_UNSUPPORTED, "B * q_len exceeds 2^31");
+  const BlockScales bs{scales, scale_rows};
+  return decode_call(Q, pages, page_table_indptr, page_table_values, length_info, nullptr, nullptr,
+                     output, lse, q_len, 0, 1.f, 1e4f, sm_scale, desc, stream, &bs);
 }
 
 pd_status pd_merge_state_inplace(void* V, float* S, const void* V_other, const float* S_other,
@@ -664,6 +805,153 @@ pd_status pd_append_paged_kv_rope(void* pages, const void* k_new, const void* v_
   return append_call(pages, k_new, v_new, slot_mapping, T, H_kv, D, page_size, max_pages, in_dtype,
                      kv_dtype, k_scale, v_scale, positions, rotary_mode, rope_scale, rope_theta,
                      stream);
+}
+
+pd_status pd_append_paged_kv_bs(void* pages, float* scales, const void* k_new, const void* v_new,
+                                const int32_t* append_indptr, const int32_t* page_table_indptr,
+                                const int32_t* page_table_values, const int32_t* length_info,
+                                int32_t T, int32_t B, int32_t H_kv, int32_t D, int32_t page_size,
+                                int32_t scale_rows, int64_t max_pages, int64_t nnz_pages,
+                                int64_t k_stride, int64_t v_stride, int32_t in_dtype,
+                                int32_t kv_dtype, pd_stream_t stream) {
+  if (T < 0 || B < 0 || H_kv <= 0 || max_pages <= 0 || nnz_pages < 0)
+    return fail(PD_ERR_INVALID_ARG, "bad T/B/H_kv/max_pages/nnz_pages");
+  if (D != 64 && D != 128 && D != 256) return fail(PD_ERR_UNSUPPORTED, "head dim must be 64, 128 or 256");
+  if (page_size <= 0 || page_size > 256) return fail(PD_ERR_INVALID_ARG, "page_size must be in [1, 256]");
+  if (scale_rows <= 0 || page_size % scale_rows != 0)
+    return fail(PD_ERR_INVALID_ARG, "scale_rows must divide page_size");
+  if (in_dtype != kF32 && in_dtype != kF16 && in_dtype != kBF16)
+    return fail(PD_ERR_INVALID_ARG, "in_dtype must be F32, F16 or BF16");
+  if (kv_dtype != kE4M3 && kv_dtype != kI8) return fail(PD_ERR_INVALID_ARG, "a block-scaled cache is E4M3 or I8");
+  const long long row = (long long)H_kv * D;
+  if (T > 1 && (k_stride < row || v_stride < row))
+    return fail(PD_ERR_INVALID_ARG, "k_stride and v_stride must be at least H_kv * D");
+  if (max_pages * 2 * H_kv > INT_MAX) return fail(PD_ERR_UNSUPPORTED, "max_pages * 2 * H_kv exceeds 2^31");
+  if ((long long)T / scale_rows + 2ll * B > INT_MAX || H_kv > 200000)
+    return fail(PD_ERR_UNSUPPORTED, "T, B or H_kv too large");
+  if (T == 0 || B == 0) return PD_OK;
+  if (!pages || !scales || !k_new || !v_new || !append_indptr || !page_table_indptr || !page_table_values ||
+      !length_info)
+    return fail(PD_ERR_INVALID_ARG, "NULL device pointer");
+  if ((reinterpret_cast<uintptr_t>(pages) % 16) != 0 || (reinterpret_cast<uintptr_t>(scales) % 4) != 0)
+    return fail(PD_ERR_INVALID_ARG, "pages must be 16-byte and scales 4-byte aligned");
+  DeviceState* ds = nullptr;
+  pd_status st = device_state(&ds);
+  if (st != PD_OK) return st;
+  AppendBsParams a{};
+  a.pages = (uint8_t*)pages;
+  a.scales = scales;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.append_indptr = append_indptr;
+  a.indptr = page_table_indptr;
+  a.values = page_table_values;
+  a.length_info = length_info;
+  a.err = ds->err;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.max_pages = max_pages;
+  a.nnz = nnz_pages;
+  a.T = T;
+  a.B = B;
+  a.H_kv = H_kv;
+  a.P = page_size;
+  a.S = scale_rows;
+  const cudaError_t e = launch_append_bs(a, D, in_dtype, kv_dtype, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "append launch");
+  return PD_OK;
+}
+
+pd_status pd_rope_frequencies(int32_t rotary_dim, double rope_theta, int32_t scaling, double factor,
+                              double original_context, double low_turns, double high_turns,
+                              double* inv_freq) {
+  if (rotary_dim <= 0 || rotary_dim % 2) return fail(PD_ERR_INVALID_ARG, "rotary_dim must be positive and even");
+  if (!(rope_theta > 0.0) || !std::isfinite(rope_theta))
+    return fail(PD_ERR_INVALID_ARG, "rope_theta must be finite and positive");
+  if (scaling < PD_ROPE_PLAIN || scaling > PD_ROPE_PARTS) return fail(PD_ERR_INVALID_ARG, "bad scaling");
+  if (scaling != PD_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor)))
+    return fail(PD_ERR_INVALID_ARG, "factor must be finite and positive");
+  if (scaling == PD_ROPE_PARTS &&
+      (!(original_context > 0.0) || !std::isfinite(original_context) || !std::isfinite(low_turns) ||
+       !std::isfinite(high_turns) || !(high_turns > low_turns)))
+    return fail(PD_ERR_INVALID_ARG, "scaling by parts needs a positive original_context and low_turns < high_turns");
+  if (!inv_freq) return fail(PD_ERR_INVALID_ARG, "inv_freq is NULL");
+  const int n = rotary_dim / 2;
+  double theta = rope_theta;
+  // the lowest frequency (i = n - 1) slowed by `factor`, the highest kept
+  if (scaling == PD_ROPE_THETA && n > 1) theta *= std::pow(factor, (double)n / (n - 1));
+  for (int i = 0; i < n; ++i) {
+    double f = std::pow(theta, -(double)i / n);
+    if (scaling == PD_ROPE_LINEAR) f /= factor;
+    if (scaling == PD_ROPE_PARTS) {
+      const double turns = original_context * f / 6.283185307179586476925286766559;
+      const double keep = std::min(1.0, std::max(0.0, (turns - low_turns) / (high_turns - low_turns)));
+      f = (1.0 - keep) * f / factor + keep * f;
+    }
+    inv_freq[i] = f;
+  }
+  return PD_OK;
+}
+
+pd_status pd_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                          const int32_t* positions, const double* inv_freq, void* q_out, void* k_out,
+                          const pd_qk_desc* desc, pd_stream_t stream) {
+  if (!desc) return fail(PD_ERR_INVALID_ARG, "desc is NULL");
+  const pd_qk_desc& d = *desc;
+  if (d.T < 0 || d.H_q < 0 || d.H_k < 0 || (long long)d.H_q + d.H_k > 65535)
+    return fail(PD_ERR_INVALID_ARG, "bad T/H_q/H_k");
+  if (d.D <= 0 || d.D > 512) return fail(PD_ERR_UNSUPPORTED, "head dim must be in [1, 512]");
+  if (d.dtype != kF32 && d.dtype != kF16 && d.dtype != kBF16)
+    return fail(PD_ERR_INVALID_ARG, "dtype must be F32, F16 or BF16");
+  if ((q_weight || k_weight) && d.weight_dtype != kF32 && d.weight_dtype != kF16 && d.weight_dtype != kBF16)
+    return fail(PD_ERR_INVALID_ARG, "weight_dtype must be F32, F16 or BF16");
+  if (d.rotary_mode < 0 || d.rotary_mode > 2) return fail(PD_ERR_INVALID_ARG, "rotary_mode must be 0, 1 or 2");
+  if (d.rotary_mode && (d.rotary_dim < 0 || d.rotary_dim % 2 || d.rotary_dim > d.D))
+    return fail(PD_ERR_INVALID_ARG, "rotary_dim must be even and at most D");
+  if (!std::isfinite(d.eps) || d.eps < 0.f || !std::isfinite(d.weight_offset) || !std::isfinite(d.attention_factor))
+    return fail(PD_ERR_INVALID_ARG, "eps must be finite and >= 0, weight_offset and attention_factor finite");
+  const int rd = d.rotary_mode ? d.rotary_dim : 0;
+  if (d.T == 0 || d.H_q + d.H_k == 0) return PD_OK;
+  if ((d.H_q && (!q || !q_out)) || (d.H_k && (!k || !k_out))) return fail(PD_ERR_INVALID_ARG, "NULL device pointer");
+  if (rd && (!positions || !inv_freq)) return fail(PD_ERR_INVALID_ARG, "the rotation needs positions and inv_freq");
+  const int eb = elem_bytes(d.dtype);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(d.H_q ? q : k) | reinterpret_cast<uintptr_t>(d.H_q ? q_out : k_out) |
+                       reinterpret_cast<uintptr_t>(d.H_k ? k : q) | reinterpret_cast<uintptr_t>(d.H_k ? k_out : q_out);
+  if (at % eb) return fail(PD_ERR_INVALID_ARG, "q, k, q_out and k_out must be aligned to their elements");
+  DeviceState* ds = nullptr;
+  pd_status st = device_state(&ds);
+  if (st != PD_OK) return st;
+  QkParams a{};
+  a.q = d.H_q ? q : k;  // (unused where there are no such heads)
+  a.k = d.H_k ? k : q;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.positions = positions;
+  a.freq = inv_freq;
+  a.q_out = d.H_q ? q_out : k_out;
+  a.k_out = d.H_k ? k_out : q_out;
+  a.q_stride = d.H_q ? d.q_stride : 0;
+  a.k_stride = d.H_k ? d.k_stride : 0;
+  a.q_out_stride = d.H_q ? d.q_out_stride : 0;
+  a.k_out_stride = d.H_k ? d.k_out_stride : 0;
+  a.q_head = d.H_q ? d.q_head_stride : 0;
+  a.k_head = d.H_k ? d.k_head_stride : 0;
+  a.q_out_head = d.H_q ? d.q_out_head_stride : 0;
+  a.k_out_head = d.H_k ? d.k_out_head_stride : 0;
+  a.T = d.T;
+  a.Hq = d.H_q;
+  a.Hk = d.H_k;
+  a.D = d.D;
+  a.rd = rd;
+  a.mode = d.rotary_mode;
+  a.w_dtype = d.weight_dtype;
+  a.eps = d.eps;
+  a.inv_D = 1.f / (float)d.D;
+  a.w_offset = d.weight_offset;
+  a.attention_factor = d.attention_factor;
+  const cudaError_t e = launch_qk_norm_rope(a, d.dtype, ds->num_sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rope launch");
+  return PD_OK;
 }
 
 pd_status pd_release_stream_workspace(pd_stream_t stream) {

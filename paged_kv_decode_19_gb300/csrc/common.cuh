@@ -18,10 +18,10 @@
 namespace pd {
 
 // dtype codes (mirror pd_dtype in include/pageddecode.h)
-enum : int { kF32 = 0, kF16 = 1, kBF16 = 2, kE4M3 = 3 };
+enum : int { kF32 = 0, kF16 = 1, kBF16 = 2, kE4M3 = 3, kI8 = 4 };
 
 // device error word bits
-// (kErrTimeout is reserved: the current kernels have no wait that could time out)
+// (kErrTimeout: a bounded wait for a kernel's own copies ran out; decode_bs.cuh)
 enum : unsigned { kErrBadPage = 1u, kErrBadLength = 2u, kErrBadSlot = 4u, kErrTimeout = 8u };
 
 // Initial running max of the online softmax (the TVM decode kernel's -5e4 sentinel);
@@ -29,6 +29,7 @@ enum : unsigned { kErrBadPage = 1u, kErrBadLength = 2u, kErrBadSlot = 4u, kErrTi
 constexpr float kEmptyM = -5e4f;
 
 struct F8 { uint8_t v; };  // storage type of an e4m3 element
+struct I8 { int8_t v; };   // storage type of an 8-bit integer code
 
 template <typename T> struct ElemBytes { static constexpr int v = sizeof(T); };
 template <> struct ElemBytes<F8> { static constexpr int v = 1; };
@@ -48,6 +49,8 @@ __device__ __forceinline__ float to_f32(F8 x) {
   uint32_t h = e4m3x2_to_f16x2((uint16_t)x.v);
   return __half2float(__ushort_as_half((unsigned short)(h & 0xffff)));
 }
+
+__device__ __forceinline__ float to_f32(I8 x) { return (float)x.v; }
 
 // f32 -> one e4m3 code, round to nearest even, saturating to +-448.
 __device__ __forceinline__ uint8_t f32_to_e4m3(float x) {

@@ -1,0 +1,11 @@
+// Instantiations of the block-scaled tensor-core decode (decode_bs.cuh) for 8-bit integer codes.
+#include "decode_bs.cuh"
+
+namespace pd {
+
+cudaError_t launch_bs_int(const DecodeParams& p, const CUtensorMap& tm, int q_dtype, dim3 grid,
+                           cudaStream_t st, MmaConfig* cfg) {
+  return launch_bs_any<I8>(p, tm, q_dtype, grid, st, cfg);
+}
+
+}  // namespace pd

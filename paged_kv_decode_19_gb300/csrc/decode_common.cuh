@@ -63,6 +63,8 @@ struct DecodeParams {
   float score_scale;  // raw q.k -> log2 units (sm_scale * log2 e [* k_scale])
   float q_prescale;   // split-operand MMA path: Q is pre-multiplied by this
   float out_scale;    // applied to the final output (v_scale for e4m3 KV)
+  const float* scales;  // 8-bit cache with a scale per block of rows: [max_pages, 2, H_kv, n_sb]
+  int scale_rows, n_sb; // rows per block, blocks per page (scale_rows * n_sb = P)
   unsigned long long rope_F[kMaxHalfDim];  // fixed-point turns/position per frequency
   // Host plan: when hp_B > 0 the caller gave host copies of page_table_indptr and
   // length_info, and the launch carries them: hp[0 .. B] = prefix sums over the

@@ -60,6 +60,48 @@ struct AppendRope {
   int mode;
   unsigned long long F[kMaxHalfDim];       // fixed-point turns per frequency
 };
+// 8-bit cache with a scale per block of rows (DecodeParams::scales): the tensor-core decode
+// (decode_bs.cuh; tm: the pages as boxes of 16 rows) and the SIMT one.
+cudaError_t launch_bs_e4m3(const DecodeParams& p, const CUtensorMap& tm, int q_dtype, dim3 grid,
+                           cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_bs_int(const DecodeParams& p, const CUtensorMap& tm, int q_dtype, dim3 grid,
+                          cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_decode_simt_bs(const DecodeParams& p, int q_dtype, int kv_dtype, dim3 grid,
+                                  cudaStream_t st, int* ctas = nullptr);
+// Append to such a cache.
+struct AppendBsParams {
+  uint8_t* pages;
+  float* scales;
+  const void* k_new;
+  const void* v_new;
+  const int32_t* append_indptr;  // [B+1] new tokens of each sequence
+  const int32_t* indptr;         // page table after the append
+  const int32_t* values;
+  const int32_t* length_info;    // [B] last page lengths after the append
+  unsigned* err;
+  long long k_stride, v_stride;  // elements from token to token
+  long long max_pages, nnz;
+  int T, B, H_kv, P, S;
+};
+cudaError_t launch_append_bs(const AppendBsParams& a, int D, int in_dtype, int kv_dtype, cudaStream_t st);
+
+// qk_norm_rope
+struct QkParams {
+  const void* q;
+  const void* k;
+  const void* q_weight;  // nullptr: no norm
+  const void* k_weight;
+  const int32_t* positions;
+  const double* freq;    // [rd / 2] radians per position
+  void* q_out;
+  void* k_out;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements from token to token
+  long long q_head, k_head, q_out_head, k_out_head;          // elements from head to head
+  int T, Hq, Hk, D, rd, mode, w_dtype;
+  float eps, inv_D, w_offset, attention_factor;
+};
+cudaError_t launch_qk_norm_rope(const QkParams& a, int dtype, int num_sms, cudaStream_t st);
+
 cudaError_t launch_append(void* pages, const void* k_new, const void* v_new,
                           const int64_t* slot_mapping, int T, int H_kv, int D, int P,
                           long long max_pages, int in_dtype, int kv_dtype, float k_scale,
