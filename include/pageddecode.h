@@ -369,8 +369,8 @@ typedef struct {
  * strides of desc; q_weight, k_weight [D] or NULL; positions [T] int32; inv_freq
  * [rotary_dim / 2] float64, radians per position (pd_rope_frequencies, copied to the device).
  * q_out may be q and k_out may be k (same strides); outputs must not overlap otherwise.
- * Heads whose rows are 16-byte aligned, D a multiple of 8 up to 256 and a rotated part that is
- * a multiple of 16 (mode 1) or 8 (mode 2) run with 16-byte accesses; the rest element by element.
+ * Heads whose rows are 16-byte aligned, with D a multiple of 8 up to 256 and rotary_dim a
+ * multiple of 8, run with vector accesses; the rest element by element.
  */
 pd_status pd_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
                           const int32_t* positions, const double* inv_freq, void* q_out, void* k_out,

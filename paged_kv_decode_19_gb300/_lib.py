@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -160,12 +161,11 @@ def lib():
             L.pd_append_paged_kv_rope.restype = i32
             L.pd_append_paged_kv_bs.argtypes = [P] * 8 + [i32] * 6 + [i64] * 4 + [i32, i32, P]
             L.pd_append_paged_kv_bs.restype = i32
-            L.pd_batch_decode_paged_kv_bs.argtypes = [P] * 8 + [i32, i32, f32,
-                                                                ctypes.POINTER(DecodeDesc), P]
+            L.pd_batch_decode_paged_kv_bs.argtypes = [P] * 8 + [i32, i32, f32, P, P]
             L.pd_batch_decode_paged_kv_bs.restype = i32
             L.pd_workspace_size_bs.argtypes = [ctypes.POINTER(DecodeDesc), i32, i32]
             L.pd_workspace_size_bs.restype = ctypes.c_size_t
-            L.pd_qk_norm_rope.argtypes = [P] * 8 + [ctypes.POINTER(QkDesc), P]
+            L.pd_qk_norm_rope.argtypes = [P] * 8 + [P, P]
             L.pd_qk_norm_rope.restype = i32
             f64 = ctypes.c_double
             L.pd_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, P]
@@ -205,7 +205,7 @@ def _ptr(t: Optional[torch.Tensor]):
 def _stream(stream) -> int:
     """cudaStream_t of `stream` (a torch stream or a raw handle); None: the current stream."""
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -237,10 +237,10 @@ def make_desc(Q, pages, indptr, values, length_info, out, *, num_splits=0, max_k
 
 
 def _host_i32(a, n):
-    import numpy as np
-    if not isinstance(a, np.ndarray) or a.dtype != np.int32 or not a.flags.c_contiguous or a.size != n:
+    ai = getattr(a, "__array_interface__", None)  # (built once per access)
+    if ai is None or ai["typestr"] != "<i4" or ai["strides"] is not None or a.size != n:
         raise ValueError(f"host copies must be contiguous numpy int32 arrays of {n} entries")
-    return a.__array_interface__["data"][0]
+    return ai["data"][0]
 
 
 def host_meta_of(indptr, length_info):
@@ -329,39 +329,49 @@ def batch_decode_paged_kv_mq(Q, pages, page_table_indptr, page_table_values, len
     return output, lse
 
 
-def _on_current_device(*tensors):
-    """The kernels run on the current device and read these through raw addresses."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must be on the GPU")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device, cuda:{dev}")
+def _addr(t, dev, contiguous=True):
+    """Device address of a tensor on device `dev` (the current one, where the kernel runs)."""
+    if t.get_device() != dev:
+        raise ValueError(f"tensors must be on the current device, cuda:{dev}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _device():
+    """The current device's index, without setting CUDA up where there is none."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
 
 
 def _bs_shape(pages, scales):
-    """(max_pages, H_kv, P, D, scale_rows) of a block-scaled cache, checked."""
-    if pages.dim() != 5 or pages.shape[1] != 2 or pages.dtype not in BS_DTYPE_CODES:
+    """(max_pages, H_kv, P, D, blocks per page) of a block-scaled cache, checked."""
+    shape, sshape = pages.shape, scales.shape
+    if len(shape) != 5 or shape[1] != 2 or pages.dtype not in BS_DTYPE_CODES:
         raise ValueError("pages must be [max_pages, 2, H_kv, P, D] of float8_e4m3fn or int8")
-    max_pages, _, H_kv, P, D = pages.shape
-    if scales.dtype != torch.float32 or scales.dim() != 4 or scales.shape[:3] != pages.shape[:3]:
+    if scales.dtype != torch.float32 or len(sshape) != 4 or sshape[:3] != shape[:3]:
         raise ValueError("scales must be float32 [max_pages, 2, H_kv, P / scale_rows]")
-    n_sb = scales.shape[3]
+    max_pages, _, H_kv, P, D = shape
+    n_sb = sshape[3]
     if n_sb < 1 or P % n_sb:
         raise ValueError("the blocks of a page must divide it")
-    return max_pages, H_kv, P, D, P // n_sb
+    return max_pages, H_kv, P, D, n_sb
 
 
 def _bs_table(page_table_indptr, page_table_values, length_info, B):
-    for t in (page_table_indptr, page_table_values, length_info):
-        if t is not None and t.dtype != torch.int32:
-            raise ValueError("the page table and length_info must be int32")
-    if page_table_indptr.numel() != B + 1 or length_info.numel() not in (B, 3 * B):
+    i32 = torch.int32
+    if (page_table_indptr.dtype != i32 or length_info.dtype != i32
+            or (page_table_values is not None and page_table_values.dtype != i32)):
+        raise ValueError("the page table and length_info must be int32")
+    n = length_info.numel()
+    if page_table_indptr.numel() != B + 1 or (n != B and n != 3 * B):
         raise ValueError("page_table_indptr [B+1] and length_info [B] or [3,B]")
+    return n
+
+
+# The descs of the calls below, packed: a ctypes.Structure of twenty fields costs more to fill
+# than the call it is passed to.
+_PACK_DECODE = struct.Struct("@10i2qi2fi5Q").pack
+_PACK_QK = struct.Struct("@8i3f8q").pack
 
 
 def batch_decode_paged_kv_bs(Q, pages, scales, page_table_indptr, page_table_values, length_info,
@@ -372,30 +382,37 @@ def batch_decode_paged_kv_bs(Q, pages, scales, page_table_indptr, page_table_val
     [B, q_len, H_qo, D] for several query tokens per sequence (causal among them); output
     like Q, lse [B, H_qo] or [B, q_len, H_qo].  K is used as stored and Q as given: rotate
     both with qk_norm_rope."""
-    max_pages, H_kv, P, D, scale_rows = _bs_shape(pages, scales)
+    max_pages, H_kv, P, D, n_sb = _bs_shape(pages, scales)
     shape = Q.shape
-    if len(shape) not in (3, 4) or shape[-1] != D:
+    if len(shape) == 3:
+        (B, H_qo, D_q), q_len = shape, 1
+    elif len(shape) == 4:
+        B, q_len, H_qo, D_q = shape
+    else:
+        D_q = -1
+    if D_q != D:
         raise ValueError("Q must be [B, H_qo, D] or [B, q_len, H_qo, D]")
     if output.shape != shape or lse.shape != shape[:-1] or lse.dtype != torch.float32:
         raise ValueError("output must be shaped like Q and lse float32 like its heads")
-    B, H_qo, q_len = shape[0], shape[-2], shape[1] if len(shape) == 4 else 1
-    _bs_table(page_table_indptr, page_table_values, length_info, B)
-    desc = DecodeDesc(
+    n_li = _bs_table(page_table_indptr, page_table_values, length_info, B)
+    dev = _device()
+    vals = page_table_values
+    desc = _PACK_DECODE(
         B, H_qo, H_kv, D, P, DTYPE_CODES[Q.dtype], BS_DTYPE_CODES[pages.dtype],
-        DTYPE_CODES[output.dtype], int(length_info.dim() == 2), int(num_splits), max_pages,
-        0 if page_table_values is None else page_table_values.numel(), 0, 1.0, 1.0,
-        DECODE_EARLY_INPUTS if early_inputs else 0,
-        None if workspace is None else workspace.data_ptr(),
+        DTYPE_CODES[output.dtype], length_info.dim() == 2, num_splits, max_pages,
+        0 if vals is None else vals.numel(), 0, 1.0, 1.0, DECODE_EARLY_INPUTS if early_inputs else 0,
+        0 if workspace is None else _addr(workspace, dev),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _sink_ptr(sink, H_qo),
-        None if host_meta is None else _host_i32(host_meta[0], B + 1),
-        None if host_meta is None else _host_i32(host_meta[1], length_info.numel()))
-    _on_current_device(Q, pages, scales, page_table_indptr, page_table_values, length_info, output,
-                       lse, workspace, sink)
-    _check(lib().pd_batch_decode_paged_kv_bs(
-        _ptr(Q), _ptr(pages), _ptr(scales), _ptr(page_table_indptr), _ptr(page_table_values),
-        _ptr(length_info), _ptr(output), _ptr(lse), q_len, scale_rows,
-        D ** -0.5 if sm_scale is None else sm_scale, ctypes.byref(desc), _stream(stream)))
+        0 if sink is None else _sink_ptr(sink, H_qo) and _addr(sink, dev),
+        0 if host_meta is None else _host_i32(host_meta[0], B + 1),
+        0 if host_meta is None else _host_i32(host_meta[1], n_li))
+    st = (_lib or lib()).pd_batch_decode_paged_kv_bs(
+        _addr(Q, dev), _addr(pages, dev), _addr(scales, dev), _addr(page_table_indptr, dev),
+        None if vals is None else _addr(vals, dev), _addr(length_info, dev), _addr(output, dev),
+        _addr(lse, dev), q_len, P // n_sb, D ** -0.5 if sm_scale is None else sm_scale, desc,
+        _stream(stream))
+    if st:
+        _check(st)
     return output, lse
 
 
@@ -410,26 +427,28 @@ def append_paged_kv_bs(pages, scales, k_new, v_new, append_indptr, page_table_in
     tokens append_indptr[b] .. append_indptr[b+1] - 1, its last rows in the page table and
     length_info as they stand after the append.  k_new and v_new may be slices of a larger
     tensor along the heads (any token stride)."""
-    max_pages, H_kv, P, D, scale_rows = _bs_shape(pages, scales)
-    T = k_new.shape[0]
-    if k_new.shape != (T, H_kv, D) or v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+    max_pages, H_kv, P, D, n_sb = _bs_shape(pages, scales)
+    shape, dtype = k_new.shape, k_new.dtype
+    if len(shape) != 3 or shape[1] != H_kv or shape[2] != D or v_new.shape != shape or v_new.dtype != dtype:
         raise ValueError("k_new and v_new must be [T, H_kv, D] of one dtype")
-    ks, vs = k_new.stride(), v_new.stride()
-    if T and ((ks[2] != 1 or vs[2] != 1) or (H_kv > 1 and (ks[1] != D or vs[1] != D))):
+    T = shape[0]
+    (ks, kh, kd), (vs, vh, vd) = k_new.stride(), v_new.stride()
+    if T and (kd != 1 or vd != 1 or (H_kv > 1 and (kh != D or vh != D))):
         raise ValueError("the heads of k_new and v_new must be contiguous")
     B = append_indptr.numel() - 1
     if append_indptr.dtype != torch.int32 or B < 0:
         raise ValueError("append_indptr must be int32 [B+1]")
     _bs_table(page_table_indptr, page_table_values, length_info, B)
-    row = H_kv * D
-    _on_current_device(pages, scales, k_new, v_new, append_indptr, page_table_indptr,
-                       page_table_values, length_info)
-    _check(lib().pd_append_paged_kv_bs(
-        _ptr(pages), _ptr(scales), k_new.data_ptr(), v_new.data_ptr(), _ptr(append_indptr),
-        _ptr(page_table_indptr), _ptr(page_table_values), _ptr(length_info), T, B, H_kv, D, P,
-        scale_rows, max_pages, page_table_values.numel(), ks[0] if T > 1 else row,
-        vs[0] if T > 1 else row, DTYPE_CODES[k_new.dtype], BS_DTYPE_CODES[pages.dtype],
-        _stream(stream)))
+    if T < 2:
+        ks = vs = H_kv * D
+    dev = _device()
+    st = (_lib or lib()).pd_append_paged_kv_bs(
+        _addr(pages, dev), _addr(scales, dev), _addr(k_new, dev, False), _addr(v_new, dev, False),
+        _addr(append_indptr, dev), _addr(page_table_indptr, dev), _addr(page_table_values, dev),
+        _addr(length_info, dev), T, B, H_kv, D, P, P // n_sb, max_pages, page_table_values.numel(),
+        ks, vs, DTYPE_CODES[dtype], BS_DTYPE_CODES[pages.dtype], _stream(stream))
+    if st:
+        _check(st)
     return pages, scales
 
 
@@ -449,15 +468,16 @@ def rope_frequencies(rotary_dim, rope_theta=1e4, scaling=None, factor=1.0, origi
     return torch.tensor(list(out), dtype=torch.float64, device=device)
 
 
-def _heads(t, T, D, dtype, what, written=False):
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or t.dtype != dtype:
+def _heads(t, T, H, D, dtype, what, written=False):
+    """(token stride, head stride) of rows [T, H, D], checked."""
+    if t.shape != (T, H, D) or t.dtype != dtype:
         raise ValueError(f"{what} must be [T, heads, D] like the other rows")
-    st = t.stride()
-    if D > 1 and st[2] != 1:
+    a, b, c = t.stride()
+    if c != 1 and D > 1:
         raise ValueError(f"the last dim of {what} must be contiguous")
-    if written and ((T > 1 and st[0] == 0) or (t.shape[1] > 1 and st[1] == 0)):
+    if written and ((a == 0 and T > 1) or (b == 0 and H > 1)):
         raise ValueError(f"{what} must not be an expanded tensor")
-    return st
+    return a, b
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out=None, k_out=None, *,
@@ -471,37 +491,42 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out=None, k_ou
     dtype = q.dtype
     if q_out is None:
         q_out = torch.empty((T, H_q, D), dtype=dtype, device=q.device)
-    qs, qos = _heads(q, T, D, dtype, "q"), _heads(q_out, T, D, dtype, "q_out", True)
-    if q_out.shape[1] != H_q:
-        raise ValueError("q_out must be shaped like q")
-    H_k, ks, kos = 0, (0, 0, 1), (0, 0, 1)
+    qs, qh = _heads(q, T, H_q, D, dtype, "q")
+    qos, qoh = _heads(q_out, T, H_q, D, dtype, "q_out", True)
+    dev = _device()
+    H_k = ks = kh = kos = koh = 0
+    k_at = ko_at = None
     if k is not None:
         H_k = k.shape[1]
         if k_out is None:
             k_out = torch.empty((T, H_k, D), dtype=dtype, device=k.device)
-        ks, kos = _heads(k, T, D, dtype, "k"), _heads(k_out, T, D, dtype, "k_out", True)
-        if k_out.shape[1] != H_k:
-            raise ValueError("k_out must be shaped like k")
+        ks, kh = _heads(k, T, H_k, D, dtype, "k")
+        kos, koh = _heads(k_out, T, H_k, D, dtype, "k_out", True)
+        k_at, ko_at = _addr(k, dev, False), _addr(k_out, dev, False)
     w = q_weight if q_weight is not None else k_weight
-    for x in (q_weight, k_weight):
-        if x is not None and (x.shape != (D,) or x.dtype != w.dtype):
+    qw_at = kw_at = None
+    if w is not None:
+        if w.shape != (D,) or (k_weight is not None and (k_weight.shape != (D,) or k_weight.dtype != w.dtype)):
             raise ValueError("the weights must be [D], of one dtype")
+        qw_at = None if q_weight is None else _addr(q_weight, dev)
+        kw_at = None if k_weight is None else _addr(k_weight, dev)
     rd = 0
+    pos_at = freq_at = None
     if inv_freq is not None and rotary_mode:
         if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be float64 [rotary_dim / 2]")
         if positions.dtype != torch.int32 or positions.shape != (T,):
             raise ValueError("positions must be int32 [T]")
         rd = 2 * inv_freq.numel()
-    _on_current_device(q, k, q_weight, k_weight, positions if rd else None,
-                       inv_freq if rd else None, q_out, k_out)
-    desc = QkDesc(T, H_q, H_k, D, DTYPE_CODES[dtype], 0 if w is None else DTYPE_CODES[w.dtype],
-                  int(rotary_mode), rd, eps, weight_offset, attention_factor, qs[0], ks[0], qs[1],
-                  ks[1], qos[0], kos[0], qos[1], kos[1])
-    _check(lib().pd_qk_norm_rope(
-        q.data_ptr(), None if k is None else k.data_ptr(), _ptr(q_weight), _ptr(k_weight),
-        _ptr(positions) if rd else None, _ptr(inv_freq) if rd else None, q_out.data_ptr(),
-        None if k is None else k_out.data_ptr(), ctypes.byref(desc), _stream(stream)))
+        pos_at, freq_at = _addr(positions, dev), _addr(inv_freq, dev)
+    desc = _PACK_QK(T, H_q, H_k, D, DTYPE_CODES[dtype], 0 if w is None else DTYPE_CODES[w.dtype],
+                    rotary_mode, rd, eps, weight_offset, attention_factor, qs, ks, qh, kh, qos, kos,
+                    qoh, koh)
+    st = (_lib or lib()).pd_qk_norm_rope(
+        _addr(q, dev, False), k_at, qw_at, kw_at, pos_at, freq_at, _addr(q_out, dev, False), ko_at,
+        desc, _stream(stream))
+    if st:
+        _check(st)
     return q_out, k_out
 
 

@@ -27,6 +27,11 @@ constexpr int kMaxWaves = 8;
 // Cost of a segment's set-up and finish in the tensor-core schedule, in 16-row tiles
 // (measured: a warp crossing a segment boundary loses about 4-6 tiles' time).
 constexpr int kSegCostTiles = PD_SEG_COST_TILES;
+// The same of the block-scaled kernel, whose tiles hold half the bytes.
+#ifndef PD_BS_SEG_COST_TILES
+#define PD_BS_SEG_COST_TILES 4
+#endif
+constexpr int kBsSegCostTiles = PD_BS_SEG_COST_TILES;
 constexpr size_t kWsAlign = 256;
 
 static thread_local std::string t_last_error;
@@ -293,6 +298,29 @@ static bool fill_host_plan(const pd_decode_desc& d, DecodeParams& p) {
   return true;
 }
 
+// Block-scaled cache with host copies of the table: whether one block per (sequence, KV head)
+// beats equal shares of all pages.  A segment within a block is merged in shared memory; one
+// that crosses blocks costs about as much as kCrossTiles tiles of a warp more (a fence, an atomic
+// and two trips to L2: 64 rows alone took 6.8 us in one block and 11.9 us across four).  So the
+// longest segment's share of a warp may be that much larger than the equal share; all segments
+// must be resident at once, with a slice per KV head.
+constexpr int kCrossTiles = 10;
+static bool block_per_segment(const pd_decode_desc& d, int n_z, int wave) {
+  if (!d.host_indptr || d.num_splits != 0 || n_z != 1 || (long long)d.B * d.H_kv > wave) return false;
+  const int tiles_per_page = d.page_size / 16, B = d.B;
+  long long total = 0, most = 0;
+  for (int b = 0; b < B; ++b) {
+    const int32_t* li = d.host_length_info;
+    bool bad = false;
+    const SeqInfo s = seq_from(d.host_indptr[b], d.host_indptr[b + 1], li[b], d.sliding_window ? li[B + b] : 0,
+                               d.sliding_window ? li[2 * B + b] : 0, d.page_size, d.sliding_window != 0, bad);
+    const long long n = (long long)units_of(s, d.page_size) * tiles_per_page;
+    total += n;
+    most = std::max(most, n);
+  }
+  return (most + kMmaWarps - 1) / kMmaWarps <= total * d.H_kv / ((long long)wave * kMmaWarps) + kCrossTiles;
+}
+
 // Fixed-point RoPE frequencies: F_i = 2^64 * frac(rope_scale / rope_theta^(2i/D) / (2 pi)).
 static void rope_table(float rope_scale, float rope_theta, int D, unsigned long long* F) {
   const double two_pi = 6.283185307179586476925286766559;
@@ -498,6 +526,12 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   const int wpb = use_mma ? kMmaWarps : 1;
   plan_impl(desc, ds->num_sms, ctas, wpb, &mode, &grid_blocks, &ws_need, q_len);
   if (grid_blocks == 0) return PD_OK;
+  if (bs && use_mma && block_per_segment(d, (d.H_qo / d.H_kv * q_len + kMaxGroupPerCta - 1) / kMaxGroupPerCta,
+                                         ds->num_sms * ctas)) {
+    mode = kSchedPerBlock;
+    grid_blocks = d.B * d.H_kv;
+    ws_need = 0;
+  }
 
   cudaStream_t s = (cudaStream_t)stream;
   const int group = d.H_qo / d.H_kv;
@@ -587,8 +621,9 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   p.rotary = rotary_mode;
   p.mode = mode;
   // tensor-core schedule: a segment's set-up and finish cost about kSegCostTiles tiles
-  p.seg_cost = use_mma && mode == kSchedBalanced && kSegCostTiles > 0
-                   ? std::max(1, kSegCostTiles * 16 / d.page_size) : 0;
+  const int seg_tiles = bs ? kBsSegCostTiles : kSegCostTiles;
+  p.seg_cost = use_mma && mode == kSchedBalanced && seg_tiles > 0
+                   ? std::max(1, seg_tiles * 16 / d.page_size) : 0;
   p.out_dtype = d.out_dtype;
   p.out_vec16 = (reinterpret_cast<uintptr_t>(output) % 16) == 0 ? 1 : 0;
   p.early_inputs = (d.flags & PD_DECODE_EARLY_INPUTS) ? 1 : 0;
@@ -603,6 +638,7 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
     p.scales = bs->scales;
     p.scale_rows = bs->scale_rows;
     p.n_sb = d.page_size / bs->scale_rows;
+    p.sb_mul = ((1 << 20) + bs->scale_rows - 1) / bs->scale_rows;
   }
   if (rotary_mode) rope_table(rope_scale, rope_theta, d.D, p.rope_F);
   if (d.host_indptr && d.host_length_info) fill_host_plan(d, p);

@@ -152,19 +152,43 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
   const int kv = item / a.H_kv, h = item - kv * a.H_kv;
   const int S = a.S, P = a.P;
 
-  // the last sequence b with append_indptr[b] / S + 2 b <= slot, 32 candidates per round
+  // The last sequence b with append_indptr[b] / S + 2 b <= slot.  A lane takes one candidate and
+  // loads all of its sequence's numbers at once, so that the search costs one round trip when b
+  // is among the 32 around the place that even sequences give (always, up to 32 sequences);
+  // else 32 candidates a round narrow the range first.
   const int slot = blockIdx.x;
-  int b = 0;
-  for (int n = a.B; n > 1;) {
-    const int step = (n + 31) / 32;
-    const int c = b + lane * step;
-    const bool le = lane * step < n && a.append_indptr[c] / S + 2 * c <= slot;
-    const int cnt = max(__popc(__ballot_sync(0xffffffffu, le)), 1);
-    b += (cnt - 1) * step;
-    n = min(step, n - (cnt - 1) * step);
+  int c_a0 = 0, c_a1 = 0, c_i0 = 0, c_i1 = 0, c_last = 0;
+  auto among = [&](int base) -> int {  // how many of candidates base .. base + 31 start at or before slot
+    const int c = base + lane;
+    bool le = false;
+    if (c < a.B) {
+      c_a0 = a.append_indptr[c];
+      c_a1 = a.append_indptr[c + 1];
+      c_i0 = a.indptr[c];
+      c_i1 = a.indptr[c + 1];
+      c_last = a.length_info[c];
+      le = c_a0 / S + 2 * c <= slot;
+    }
+    return __popc(__ballot_sync(0xffffffffu, le));
+  };
+  int base = max(0, min((int)((long long)slot * a.B / gridDim.x) - 16, a.B - 32));
+  int cnt = among(base);
+  if ((cnt == 0 && base > 0) || (cnt == 32 && base + 32 < a.B)) {
+    base = 0;
+    for (int n = a.B; n > 32;) {
+      const int step = (n + 31) / 32;
+      const int c = base + lane * step;
+      const bool le = lane * step < n && a.append_indptr[c] / S + 2 * c <= slot;
+      const int k = max(__popc(__ballot_sync(0xffffffffu, le)), 1) - 1;
+      base += k * step;
+      n = min(step, n - k * step);
+    }
+    cnt = among(base);
   }
-  const int a0 = a.append_indptr[b], a1 = a.append_indptr[b + 1];
-  const int i0 = a.indptr[b], i1 = a.indptr[b + 1], last = a.length_info[b];
+  const int win = min(max(cnt, 1) - 1, a.B - 1 - base), b = base + win;
+  const int a0 = __shfl_sync(0xffffffffu, c_a0, win), a1 = __shfl_sync(0xffffffffu, c_a1, win);
+  const int i0 = __shfl_sync(0xffffffffu, c_i0, win), i1 = __shfl_sync(0xffffffffu, c_i1, win);
+  const int last = __shfl_sync(0xffffffffu, c_last, win);
   const int n_new = a1 - a0;
   const long long L = i1 > i0 ? (long long)(i1 - i0 - 1) * P + last : 0;
   if (a0 < 0 || n_new < 0 || a1 > a.T || i0 < 0 || i1 < i0 || i1 > a.nnz || n_new > L || last > P || last < 0 ||
@@ -241,21 +265,44 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
   const unsigned sb = __float_as_uint(scale);
   const bool pow2 = (sb & 0x807fffffu) == 0u && sb != 0u && sb < 0x7f000000u;  // (warp-uniform)
   const float inv = pow2 ? __uint_as_float(0x7f000000u - sb) : 0.f;           // 2^-k, exact
+  uint8_t* const to = rows + (size_t)n_old * D + c8;
   for (int r0 = 0; r0 < n; r0 += kKeep * RPS) {
+    if (n > kKeep * RPS) {  // the rows did not all stay in registers
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i) {
-      const int r = r0 + i * RPS + sub;
-      if (r < n) {
-        if (n > kKeep * RPS) keep[i] = load_row8<IT, VEC>(src + r * stride + c8);
+      for (int i = 0; i < kKeep; ++i) {
+        const int r = r0 + i * RPS + sub;
+        if (r < n) keep[i] = load_row8<IT, VEC>(src + r * stride + c8);
+      }
+    }
+    if (pow2) {
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        const int r = r0 + i * RPS + sub;
         float x[8];
         row8_f32<IT>(keep[i], x);
-        uint2 code = make_uint2(0u, 0u);
-        if (ok) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = pow2 ? x[k] * inv : x[k] / scale;
-          code = encode8<CT>(x);
+        for (int k = 0; k < 8; ++k) x[k] *= inv;
+        if (r < n) *reinterpret_cast<uint2*>(to + (size_t)r * D) = encode8<CT>(x);
+      }
+    } else {  // a caller's scale that is no power of two, or NaN (codes 0)
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        const int r = r0 + i * RPS + sub;
+        float x[8];
+        row8_f32<IT>(keep[i], x);
+        if (r < n) {
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            uint32_t one = 0;
+            if (ok) {
+              const float q[8] = {__fdiv_rn(x[0], scale), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+              one = encode8<CT>(q).x;
+            }
+            to[(size_t)r * D + k] = (uint8_t)one;
+#pragma unroll
+            for (int e = 0; e < 7; ++e) x[e] = x[e + 1];
+          }
         }
-        *reinterpret_cast<uint2*>(rows + (size_t)(n_old + r) * D + c8) = code;
       }
     }
   }

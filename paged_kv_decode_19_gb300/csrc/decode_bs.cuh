@@ -39,7 +39,7 @@
 namespace pd {
 
 #ifndef PD_BS_STAGES
-#define PD_BS_STAGES 6
+#define PD_BS_STAGES 2
 #endif
 #ifndef PD_BS_BLOCKS
 #define PD_BS_BLOCKS 2
@@ -59,6 +59,9 @@ __device__ __forceinline__ void mbar_init_fence() {
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // One arrival once this thread's cp.async copies so far have landed.
 __device__ __forceinline__ void mbar_arrive_cp_async(uint32_t bar) {
@@ -96,10 +99,14 @@ struct BsTile {
   static constexpr int RL = D / 8;       // V bytes (output dims) per row and thread
   static constexpr int kBytes = 16 * RB; // one tile of K (or V) codes
   static constexpr int kStage = 2 * kBytes;
+  static constexpr int NQ = D == 64 ? 4 : 2;      // tiles computed together
+  static constexpr int NST = PD_BS_STAGES * NQ;   // ring stages per warp
+  static constexpr int kState = kMaxGroupPerCta * D * 4;  // a partial state's outputs, fp32
   static_assert(D == 64 || D == 128, "head dim");
 };
-template <int D, int NW, int NST>
-constexpr int bs_smem_bytes() { return NW * NST * BsTile<D>::kStage + 1024; }
+// the warps' rings, then the state each may hold from its first segment
+template <int D, int NW>
+constexpr int bs_smem_bytes() { return NW * (BsTile<D>::NST * BsTile<D>::kStage + BsTile<D>::kState) + 1024; }
 
 // Row of the tile that fragment row g (0..7; g + 8: the row + 8) holds.  Even g keep their
 // row, odd g take (g - 1) ^ 5: rows 2i and 2i + 1 of K, read by one phase of 8 lanes, then
@@ -131,25 +138,55 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   }
 }
 
+// Four consecutive output dims at element idx (a multiple of 4).
+__device__ __forceinline__ void store_four(const DecodeParams& p, size_t idx, float4 v) {
+  if (p.out_dtype == kF32) {
+    float* o = reinterpret_cast<float*>(p.out) + idx;
+    if (p.out_vec16) *reinterpret_cast<float4*>(o) = v;
+    else o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+  } else {
+    const bool bf = p.out_dtype == kBF16;
+    const uint32_t a = bf ? pack2<__nv_bfloat16>(v.x, v.y) : pack2<__half>(v.x, v.y);
+    const uint32_t b = bf ? pack2<__nv_bfloat16>(v.z, v.w) : pack2<__half>(v.z, v.w);
+    uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + idx;
+    if (p.out_vec16) *reinterpret_cast<uint2*>(o) = make_uint2(a, b);
+    else o[0] = (uint16_t)a, o[1] = (uint16_t)(a >> 16), o[2] = (uint16_t)b, o[3] = (uint16_t)(b >> 16);
+  }
+}
+
+// A warp's partial state of a segment: the segment (its place on the cost line, sequence, head
+// slice, units) and how many of its units the state holds; b < 0: none.
+struct PartEntry {
+  long long off;
+  int b, hz, mine, n;
+};
 // ----------------------------------------------------------------------------- kernel
-template <typename CT, typename QT, int D, bool MQ, int NW, int NST>
+template <typename CT, typename QT, int D, bool MQ, int NW>
 __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
     decode_bs_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tm) {
   using T = BsTile<D>;
   constexpr int NT = NW * 32;
-  constexpr int KT = T::KT, KCH = T::KCH, RL = T::RL;
+  constexpr int KT = T::KT, KCH = T::KCH, RL = T::RL, NQ = T::NQ, NST = T::NST;
   extern __shared__ uint8_t s_raw[];
-  __shared__ int s_units[kStartCacheB];            // start-up scan scratch
-  __shared__ float s_mw[NW][34][kMaxGroupPerCta];  // per-warp merge scratch
-  __shared__ int s_msl[NW][32];
-  __shared__ long long s_pend[NW][2][4];           // per-warp deferred merges
+  __shared__ PartEntry s_part[NW][2];              // each warp's partial states: first, last segment
+  __shared__ float s_plse[NW][2][kMaxGroupPerCta]; // their lse
+  __shared__ int s_last[2 * NW];
   __shared__ WorkerStart s_start[NW];
   __shared__ __align__(8) uint64_t s_bar[NW][NST];
-  __shared__ __align__(8) float2 s_sc[NW][NST];    // scales (K, V) of the stage's tile
-  __shared__ int4 s_info[NW][NST];                 // its attended rows [x, y), first row's index z
+  __shared__ float4 s_meta[NW][NST];  // of the stage's tile: K and V scale, attended rows, first row's index
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t ring = ((smem_u32(s_raw) + 1023u) & ~1023u) + (uint32_t)(warp * NST * T::kStage);
+  uint8_t* const rings = s_raw + (((smem_u32(s_raw) + 1023u) & ~1023u) - smem_u32(s_raw));
+  const uint32_t bar0 = smem_u32(&s_bar[warp][0]), meta0 = smem_u32(&s_meta[warp][0]);
+  uint8_t* const my_ring = rings + warp * NST * T::kStage;
+  const uint32_t ring = smem_u32(my_ring);
+  // the rings' space before the first fill: scratch of the start-up scan; after a warp's last
+  // tile, its part: the state of its last segment
+  static_assert(NW * NST * T::kStage >= kStartCacheB * 4 && NST * T::kStage >= T::kState, "scratch");
+  int* const s_units = reinterpret_cast<int*>(rings);
+  auto state_of = [&](int w, int side) -> float* {
+    return reinterpret_cast<float*>(side ? rings + w * NST * T::kStage : rings + NW * NST * T::kStage + w * T::kState);
+  };
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tm) : "memory");
     prefetch_l2_share(p.Q, (size_t)p.B * p.q_len * p.H_qo * D * sizeof(QT), blockIdx.x, gridDim.x);
@@ -157,36 +194,36 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
   }
   if (lane == 0) {
     // two arrivals per fill: the issuing lane's (with the boxes' bytes) and its cp.async copies'
-    for (int i = 0; i < NST; ++i) mbar_init(smem_u32(&s_bar[warp][i]), 2);
+    for (int i = 0; i < NST; ++i) mbar_init(bar0 + i * 8, 2);
     mbar_init_fence();
   }
-  if (!p.early_inputs) {
+  // With a host plan the start-up reads launch parameters alone and runs under the tail of the
+  // kernel before; otherwise, as everywhere, nothing of the caller's is read before it completes.
+  bool waited = false;
+  if (!p.early_inputs && !p.hp_B) {
     pdl_wait();
     pdl_release();
+    waited = true;
   }
-  worker_starts<NT, NW>(p, s_start, s_units);  // the last block-wide barrier of the kernel
+  worker_starts<NT, NW>(p, s_start, s_units);
+  // the scan's shared memory accesses before the fills that overwrite its scratch
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  if (lane < 2) s_part[warp][lane].b = -1;
+  __syncthreads();  // no block-wide barrier until every warp has finished its range
 
   const int g_id = lane >> 2, q4 = lane & 3;
   const WorkerStart ws = s_start[warp];
-  if (ws.b < 0) return;  // no units for this worker
-
   const int P = p.P;
   const int zg = p.mode == kSchedBalanced ? p.zg : 1;
-  const long long Wn = (long long)gridDim.x * NW / zg;
-  const long long wid = (long long)blockIdx.x * NW + warp;
 
   Segment sg;
-  sg.b = ws.b;
+  sg.b = max(ws.b, 0);  // (ws.b < 0: no units for this worker)
   sg.hz = ws.hz;
   sg.off = ws.off;
   sg.seq = load_seq(p, sg.b);
   sg.n = units_of(sg.seq, P);
   const int C = p.mode == kSchedBalanced ? p.seg_cost : 0;
-  const long long cx1 = p.mode == kSchedBalanced ? ws.x1 : sg.off + sg.n;
-
-  int npend = 0;
-  if (lane < 2) s_pend[warp][lane][0] = -1;
-  __syncwarp();
+  const long long cx1 = p.mode != kSchedPerSegment ? ws.x1 : sg.off + sg.n;
 
   // this thread's fragment rows (+ 8: the second half) and their byte offsets in a tile
   const int kr = tile_row(g_id);
@@ -198,12 +235,16 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
   for (int i = 0; i < 2; ++i) voff[i] = tile_off<D>(vr[i], RL * g_id);
 
   // The ring: tiles are filled into stage `ist` and read from stage `cst`, in order.
-  int ist = 0, cst = 0, in_flight = 0;
-  uint32_t cph = 0;      // parity of the fill that stage cst waits for
-  bool waited = !p.early_inputs;
-  bool dead = false;     // a wait ran out: no further fills
+  int ist = 0, cst = 0;
+  uint32_t cph = 0;   // parity of the fill that stage cst waits for
+  bool dead = false;  // a wait ran out: no further fills
+  if (!p.early_inputs && !waited) {
+    pdl_wait();
+    pdl_release();
+    waited = true;
+  }
 
-  for (;;) {
+  while (ws.b >= 0) {
   const int ua = (int)min(max(ws.x0 - sg.off - C, 0ll), (long long)sg.n);
   const int ub = (int)min(max(cx1 - sg.off - C, 0ll), (long long)sg.n);
   if (ua < ub) {
@@ -231,80 +272,68 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
   }
 
   // ---------------------------------------------------------------- tile stream
-  // Pieces (page, slot range) [ua, pend) in order, 32 at a time: lane i holds piece
-  // pb_base + i, handed out with shuffles.
-  struct Tile {
-    int blk;                      // K block (page, hk) of the cache; -1: no more tiles
-    int piece, t, s_lo, s_hi, r_lo;
+  // The share's pieces are whole pages of at most two runs of attended offsets (A: the sinks,
+  // or every row; B: the window), so its tiles are the multiples of 16 of each run in order.
+  // Tiles come 32 at a time: lane i holds tile 32 m + i and issues it; the page ids of the
+  // next 32 are loaded meanwhile.
+  const int a_lo = max(pcs.ra0, (pcs.pa + min(ua, pcs.na)) * P), a_hi = min(pcs.ra1, (pcs.pa + min(pend, pcs.na)) * P);
+  const int b_lo = max(pcs.ob0, (pcs.pb + max(ua - pcs.na, 0)) * P), b_hi = min(pcs.ob1, (pcs.pb + max(pend - pcs.na, 0)) * P);
+  const int n_a = a_hi > a_lo ? ((a_hi + 15) >> 4) - (a_lo >> 4) : 0;
+  int n_tiles = n_a + (b_hi > b_lo ? ((b_hi + 15) >> 4) - (b_lo >> 4) : 0);
+  auto tile_at = [&](int k) { return k < n_a ? ((a_lo >> 4) + k) << 4 : ((b_lo >> 4) + k - n_a) << 4; };  // offset
+  auto load_page = [&](int k) -> int {  // page id of tile k, unchecked; -1 out of the table
+    if (k >= n_tiles) return -1;
+    const int pidx = tile_at(k) / P;
+    return pidx < sg.seq.npages && (long long)sg.seq.page_begin + pidx < p.nnz_pages
+               ? __ldg(p.values + sg.seq.page_begin + pidx) : -1;
   };
-  int pb_base = -64, pb_page = -1, pb_slots = 0, pb_row = 0;
-  auto first_tile_from = [&](int j) -> Tile {
-    Tile tl;
-    tl.blk = -1;
-    tl.piece = pend;
-    tl.t = tl.s_lo = tl.s_hi = tl.r_lo = 0;
-    for (; j < pend; ++j) {
-      if (j >= pb_base + 32) {
-        pb_base = j;
-        pb_page = -1;
-        if (j + lane < pend) {
-          const Piece pc = get_piece(pcs, j + lane, P);
-          pb_page = lookup_page(p, sg.seq, pc.page_idx);  // -1 (error recorded) if out of range
-          pb_slots = pc.s_lo | (pc.s_hi << 16);
-          pb_row = pc.r_lo;
-        }
+  int t_blk = -1, t_row = 0, t_span = 0, t_r0 = 0, page_next = load_page(lane);
+  auto load_batch = [&](int k0) {  // tiles k0 .. k0 + 31
+    const int k = k0 + lane, page = page_next;
+    page_next = load_page(k + 32);
+    const int o = tile_at(k);
+    const bool in_a = k < n_a;
+    t_row = o % P;
+    t_span = max((in_a ? a_lo : b_lo) - o, 0) | (min((in_a ? a_hi : b_hi) - o, 16) << 8);
+    t_r0 = in_a ? o : o - pcs.shift;
+    t_blk = page * 2 * p.H_kv + hk;
+    if (page < 0 || page >= p.max_pages) {
+      if (k < n_tiles) set_error(p.err, kErrBadPage);
+      t_blk = -1;  // no such tile, or its rows do not count
+    }
+  };
+  // tile k (the next in order) -> stage ist
+  auto issue = [&](int k) {
+    if ((k & 31) == 0) load_batch(k);
+    if (lane == (k & 31)) {
+      const uint32_t bar = bar0 + ist * 8, dst = ring + ist * T::kStage, meta = meta0 + ist * 16;
+      if (t_blk >= 0) {
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(meta + 8), "r"(t_span), "r"(t_r0) : "memory");
+        const float* ks = p.scales + (size_t)t_blk * p.n_sb + ((t_row * p.sb_mul) >> 20);
+        cp_async_scale(meta, ks);
+        cp_async_scale(meta + 4, ks + (size_t)p.H_kv * p.n_sb);
+        mbar_arrive_cp_async(bar);
+        mbar_arrive_expect_tx(bar, T::kStage);
+        tma_load_box(dst, &tm, 0, t_row, t_blk, bar);
+        tma_load_box(dst + T::kBytes, &tm, 0, t_row, t_blk + p.H_kv, bar);
+      } else {  // no attended row, zero scales
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(meta), "r"(0) : "memory");
+        mbar_arrive(bar);
+        mbar_arrive(bar);
       }
-      const int src = j - pb_base;
-      const int pg = __shfl_sync(0xffffffffu, pb_page, src);
-      if (pg < 0) continue;  // bad page id: its rows are skipped
-      const int sl = __shfl_sync(0xffffffffu, pb_slots, src);
-      tl.piece = j;
-      tl.s_lo = sl & 0xffff;
-      tl.s_hi = sl >> 16;
-      tl.t = tl.s_lo >> 4;
-      tl.r_lo = __shfl_sync(0xffffffffu, pb_row, src);
-      tl.blk = pg * 2 * p.H_kv + hk;
-      break;
-    }
-    return tl;
-  };
-  auto next_tile = [&](const Tile& c) -> Tile {
-    if ((c.t + 1) * 16 < c.s_hi) {  // (warp-uniform)
-      Tile n = c;
-      n.t = c.t + 1;
-      return n;
-    }
-    return first_tile_from(c.piece + 1);
-  };
-  // the tile's boxes and scales -> stage ist
-  auto issue = [&](const Tile& c) {
-    if (lane == 0) {
-      const uint32_t bar = smem_u32(&s_bar[warp][ist]);
-      const uint32_t dst = ring + ist * T::kStage;
-      s_info[warp][ist] = make_int4(c.s_lo - c.t * 16, c.s_hi - c.t * 16, c.r_lo + c.t * 16 - c.s_lo, 0);
-      const float* ks = p.scales + (size_t)c.blk * p.n_sb + (c.t * 16) / p.scale_rows;
-      cp_async_scale(smem_u32(&s_sc[warp][ist].x), ks);
-      cp_async_scale(smem_u32(&s_sc[warp][ist].y), ks + (size_t)p.H_kv * p.n_sb);
-      mbar_arrive_cp_async(bar);
-      mbar_arrive_expect_tx(bar, T::kStage);
-      tma_load_box(dst, &tm, 0, c.t * 16, c.blk, bar);
-      tma_load_box(dst + T::kBytes, &tm, 0, c.t * 16, c.blk + p.H_kv, bar);
     }
     ist = ist + 1 == NST ? 0 : ist + 1;
-    ++in_flight;
   };
 
-  Tile nxt = first_tile_from(ua);
   if (!waited) {  // pages and scales may still be written by the previous kernel until here
     pdl_wait();
     pdl_release();
     waited = true;
   }
+  // tiles are computed NQ at a time: the last few may be empty ones
+  int k_issued = 0, k_end = dead ? 0 : (n_tiles + NQ - 1) / NQ * NQ;
 #pragma unroll 1
-  for (int i = 0; i < NST && nxt.blk >= 0 && !dead; ++i) {
-    issue(nxt);
-    nxt = next_tile(nxt);
-  }
+  for (; k_issued < min(NST, k_end); ++k_issued) issue(k_issued);
 
   // ---------------------------------------------------------------- Q^T B fragments
   // k-tile kt: dims 16 (4 (kt >> 2) + q4) + 4 (kt & 3) + {0, 1} and + {2, 3} of column g_id,
@@ -342,123 +371,145 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
 #pragma unroll
   for (int i = 0; i < KT; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
 
-  __syncwarp();  // lane 0's s_info is read by the warp
+  // NQ tiles from the ring: their chains of loads, products and exponentials are independent and
+  // overlap in the warp, and share the vote and the rescale
 #pragma unroll 1
-  while (in_flight > 0) {
-    const bool ok = mbar_wait(smem_u32(&s_bar[warp][cst]), cph, dead ? 1024u : kWaitPolls);
-    if (__any_sync(0xffffffffu, !ok)) {
-      dead = true;  // what follows is not used: the error word says so
-      if (lane == 0) set_error(p.err, kErrTimeout);
+  for (int k = 0; k < k_end; k += NQ) {
+    int stg[NQ];
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      stg[i] = cst;
+      ok = mbar_wait(bar0 + cst * 8, cph, dead ? 1024u : kWaitPolls) && ok;
+      cst = cst + 1 == NST ? 0 : cst + 1;
+      if (cst == 0) cph ^= 1;
     }
-    const uint8_t* kt_base = s_raw + (ring - smem_u32(s_raw)) + cst * T::kStage;
-    const uint8_t* vt_base = kt_base + T::kBytes;
-    const int4 info = s_info[warp][cst];
-    const float2 sc2 = s_sc[warp][cst];
-    // ---------------------------------------------------------------- S^T = C Q^T
-    uint4 ka[2][KCH];
+    float4 meta[NQ];  // K scale, V scale, attended rows [lo, hi) (bits 0-7, 8-15), first row's index
+    float qacc[NQ][2][4];
 #pragma unroll
-    for (int c = 0; c < KCH; ++c) {
-      ka[0][c] = *reinterpret_cast<const uint4*>(kt_base + koff[c]);
-      ka[1][c] = *reinterpret_cast<const uint4*>(kt_base + 8 * D + koff[c]);
-    }
-    float qacc[2][4];
+    for (int i = 0; i < NQ; ++i) {
+      meta[i] = s_meta[warp][stg[i]];
+      const uint8_t* kt_base = my_ring + stg[i] * T::kStage;
+      // -------------------------------------------------------------- S^T = C Q^T
+      uint4 ka[2][KCH];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) qacc[c][0] = qacc[c][1] = qacc[c][2] = qacc[c][3] = 0.f;
+      for (int c = 0; c < KCH; ++c) {
+        ka[0][c] = *reinterpret_cast<const uint4*>(kt_base + koff[c]);
+        ka[1][c] = *reinterpret_cast<const uint4*>(kt_base + 8 * D + koff[c]);
+      }
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      uint32_t a[4];
-      codes_to_f16<CT>(comp(ka[0][kt >> 2], kt & 3), a[0], a[2]);
-      codes_to_f16<CT>(comp(ka[1][kt >> 2], kt & 3), a[1], a[3]);
-      Mma<__half>::run(qacc[kt & 1], a, qf[kt][0], qf[kt][1]);
+      for (int c = 0; c < 2; ++c) qacc[i][c][0] = qacc[i][c][1] = qacc[i][c][2] = qacc[i][c][3] = 0.f;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        uint32_t a[4];
+        codes_to_f16<CT>(comp(ka[0][kt >> 2], kt & 3), a[0], a[2]);
+        codes_to_f16<CT>(comp(ka[1][kt >> 2], kt & 3), a[1], a[3]);
+        Mma<__half>::run(qacc[i][kt & 1], a, qf[kt][0], qf[kt][1]);
+      }
     }
     // V rows vr[0], vr[1], vr[0] + 8, vr[1] + 8: bytes RL g_id .. + RL - 1
-    uint32_t va[4][RL / 4];
+    uint32_t va[NQ][4][RL / 4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint8_t* src = vt_base + (i >> 1) * 8 * D + voff[i & 1];
-      if constexpr (RL == 16) {
-        const uint4 v = *reinterpret_cast<const uint4*>(src);
-        va[i][0] = v.x;
-        va[i][1] = v.y;
-        va[i][2] = v.z;
-        va[i][3] = v.w;
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(src);
-        va[i][0] = v.x;
-        va[i][1] = v.y;
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t* src = my_ring + stg[i] * T::kStage + T::kBytes + (j >> 1) * 8 * D + voff[j & 1];
+        if constexpr (RL == 16) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src);
+          va[i][j][0] = v.x;
+          va[i][j][1] = v.y;
+          va[i][j][2] = v.z;
+          va[i][j][3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(src);
+          va[i][j][0] = v.x;
+          va[i][j][1] = v.y;
+        }
       }
-    }
     // ---------------------------------------------------------------- online softmax (log2)
-    const bool full = info.x <= 0 && info.y >= 16;
-    const float f0 = cs0 * sc2.x, f1 = cs1 * sc2.x;
-    float sc[4];
-    sc[0] = (qacc[0][0] + qacc[1][0]) * f0;  // row kr, columns 2 q4, 2 q4 + 1
-    sc[1] = (qacc[0][1] + qacc[1][1]) * f1;
-    sc[2] = (qacc[0][2] + qacc[1][2]) * f0;  // row kr + 8
-    sc[3] = (qacc[0][3] + qacc[1][3]) * f1;
-    if (!full) {
-      if (kr < info.x || kr >= info.y) sc[0] = sc[1] = -INFINITY;
-      if (kr + 8 < info.x || kr + 8 >= info.y) sc[2] = sc[3] = -INFINITY;
-      // rows outside may hold any code (e4m3 NaN): their V bytes are zeroed
+    float sc[NQ][4], lv[NQ];
+    float t0 = -INFINITY, t1 = -INFINITY, u0 = -INFINITY, u1 = -INFINITY;  // maxima of s, s + log2 vs
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = vr[i & 1] + 8 * (i >> 1);
-        if (r < info.x || r >= info.y) {
+    for (int i = 0; i < NQ; ++i) {
+      const float f0 = cs0 * meta[i].x, f1 = cs1 * meta[i].x;
+      sc[i][0] = (qacc[i][0][0] + qacc[i][1][0]) * f0;  // row kr, columns 2 q4, 2 q4 + 1
+      sc[i][1] = (qacc[i][0][1] + qacc[i][1][1]) * f1;
+      sc[i][2] = (qacc[i][0][2] + qacc[i][1][2]) * f0;  // row kr + 8
+      sc[i][3] = (qacc[i][0][3] + qacc[i][1][3]) * f1;
+      const int span = __float_as_int(meta[i].z);
+      if (span != (16 << 8)) {  // (warp-uniform)
+        const int lo = span & 0xff, hi = span >> 8;
+        if (kr < lo || kr >= hi) sc[i][0] = sc[i][1] = -INFINITY;
+        if (kr + 8 < lo || kr + 8 >= hi) sc[i][2] = sc[i][3] = -INFINITY;
+        // rows outside may hold any code (e4m3 NaN): their V bytes are zeroed
 #pragma unroll
-          for (int k = 0; k < RL / 4; ++k) va[i][k] = 0u;
+        for (int j = 0; j < 4; ++j) {
+          const int r = vr[j & 1] + 8 * (j >> 1);
+          if (r < lo || r >= hi) {
+#pragma unroll
+            for (int k = 0; k < RL / 4; ++k) va[i][j][k] = 0u;
+          }
         }
       }
+      if constexpr (MQ) {  // causal among the new tokens
+        const int r0 = __float_as_int(meta[i].w) + kr;
+        if (r0 >= lim0) sc[i][0] = -INFINITY;
+        if (r0 >= lim1) sc[i][1] = -INFINITY;
+        if (r0 + 8 >= lim0) sc[i][2] = -INFINITY;
+        if (r0 + 8 >= lim1) sc[i][3] = -INFINITY;
+      }
+      lv[i] = __log2f(meta[i].y);
+      const float x0 = fmaxf(sc[i][0], sc[i][2]), x1 = fmaxf(sc[i][1], sc[i][3]);
+      t0 = fmaxf(t0, x0);
+      t1 = fmaxf(t1, x1);
+      u0 = fmaxf(u0, x0 + lv[i]);
+      u1 = fmaxf(u1, x1 + lv[i]);
     }
-    if constexpr (MQ) {  // causal among the new tokens
-      const int r0 = info.z + kr;
-      if (r0 >= lim0) sc[0] = -INFINITY;
-      if (r0 >= lim1) sc[1] = -INFINITY;
-      if (r0 + 8 >= lim0) sc[2] = -INFINITY;
-      if (r0 + 8 >= lim1) sc[3] = -INFINITY;
-    }
-    const float lv = __log2f(sc2.y);
-    {
-      const float t0 = fmaxf(sc[0], sc[2]), t1 = fmaxf(sc[1], sc[3]);
-      const float over = fmaxf(fmaxf(t0 - st_m[0], t1 - st_m[1]),
-                               fmaxf(t0 + lv - st_n[0], t1 + lv - st_n[1]));
-      if (__any_sync(0xffffffffu, over > kLazyMaxBs)) {
-        const float tm0 = max_over_groups(t0), tm1 = max_over_groups(t1);
-        const float mn0 = fmaxf(st_m[0], tm0), mn1 = fmaxf(st_m[1], tm1);
-        st_d[0] *= fast_exp2(st_m[0] - mn0);
-        st_d[1] *= fast_exp2(st_m[1] - mn1);
-        st_m[0] = mn0;
-        st_m[1] = mn1;
-        const float nn0 = fmaxf(st_n[0], tm0 + lv), nn1 = fmaxf(st_n[1], tm1 + lv);
-        const float a0 = fast_exp2(st_n[0] - nn0), a1 = fast_exp2(st_n[1] - nn1);
-        st_n[0] = nn0;
-        st_n[1] = nn1;
+    const float over = fmaxf(fmaxf(t0 - st_m[0], t1 - st_m[1]), fmaxf(u0 - st_n[0], u1 - st_n[1]));
+    if (__any_sync(0xffffffffu, over > kLazyMaxBs || !ok)) {
+      if (__any_sync(0xffffffffu, !ok)) {
+        dead = true;  // the tiles in flight are still waited for; the error word says the rest
+        k_end = k_issued;
+        if (lane == 0) set_error(p.err, kErrTimeout);
+      }
+      const float mn0 = fmaxf(st_m[0], max_over_groups(t0)), mn1 = fmaxf(st_m[1], max_over_groups(t1));
+      st_d[0] *= fast_exp2(st_m[0] - mn0);
+      st_d[1] *= fast_exp2(st_m[1] - mn1);
+      st_m[0] = mn0;
+      st_m[1] = mn1;
+      const float nn0 = fmaxf(st_n[0], max_over_groups(u0)), nn1 = fmaxf(st_n[1], max_over_groups(u1));
+      const float a0 = fast_exp2(st_n[0] - nn0), a1 = fast_exp2(st_n[1] - nn1);
+      st_n[0] = nn0;
+      st_n[1] = nn1;
 #pragma unroll
-        for (int mt = 0; mt < KT; ++mt) {
-          oacc[mt][0] *= a0;
-          oacc[mt][1] *= a1;
-          oacc[mt][2] *= a0;
-          oacc[mt][3] *= a1;
-        }
+      for (int mt = 0; mt < KT; ++mt) {
+        oacc[mt][0] *= a0;
+        oacc[mt][1] *= a1;
+        oacc[mt][2] *= a0;
+        oacc[mt][3] *= a1;
       }
     }
-    float pr[4];
-    pr[0] = fast_exp2(sc[0] - st_m[0]);
-    pr[1] = fast_exp2(sc[1] - st_m[1]);
-    pr[2] = fast_exp2(sc[2] - st_m[0]);
-    pr[3] = fast_exp2(sc[3] - st_m[1]);
-    st_d[0] += pr[0] + pr[2];
-    st_d[1] += pr[1] + pr[3];
-    // weights of P.V: 2^(s - n) vs = p 2^(m - n) vs; a row that does not count weighs 0
-    // whatever the scale (the exponent is capped so that a zero scale stays zero)
-    const float w0 = sc2.y * fast_exp2(fminf(st_m[0] - st_n[0], 126.f));
-    const float w1 = sc2.y * fast_exp2(fminf(st_m[1] - st_n[1], 126.f));
-    pr[0] = pr[0] == 0.f ? 0.f : pr[0] * w0;
-    pr[1] = pr[1] == 0.f ? 0.f : pr[1] * w1;
-    pr[2] = pr[2] == 0.f ? 0.f : pr[2] * w0;
-    pr[3] = pr[3] == 0.f ? 0.f : pr[3] * w1;
-    // P^T as a B fragment: fragment rows 2q, 2q + 1 | 2q + 8, 2q + 9 of column g_id
-    uint32_t pb0, pb1;
-    {
+    // weights of P.V: 2^(s - n) vs = p 2^(m - n) vs (the exponent is capped so that a zero
+    // scale stays zero); of several queries one that does not attend a row weighs it 0
+    // whatever the scale
+    const float g0 = fast_exp2(fminf(st_m[0] - st_n[0], 126.f)), g1 = fast_exp2(fminf(st_m[1] - st_n[1], 126.f));
+    uint32_t pb[NQ][2];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      float pr[4];
+      pr[0] = fast_exp2(sc[i][0] - st_m[0]);
+      pr[1] = fast_exp2(sc[i][1] - st_m[1]);
+      pr[2] = fast_exp2(sc[i][2] - st_m[0]);
+      pr[3] = fast_exp2(sc[i][3] - st_m[1]);
+      st_d[0] += pr[0] + pr[2];
+      st_d[1] += pr[1] + pr[3];
+      const float w0 = meta[i].y * g0, w1 = meta[i].y * g1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = pr[e] * (e & 1 ? w1 : w0);
+        pr[e] = MQ && pr[e] == 0.f ? 0.f : w;
+      }
+      // P^T as a B fragment: fragment rows 2q, 2q + 1 | 2q + 8, 2q + 9 of column g_id
       const uint32_t x0 = pack2<__half>(pr[0], pr[2]);  // column 2q: rows of g_id, g_id + 8
       const uint32_t x1 = pack2<__half>(pr[1], pr[3]);  // column 2q + 1
       const int srcA = 8 * q4 + (g_id >> 1), srcB = srcA + 4;
@@ -467,43 +518,42 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
       const uint32_t b0 = __shfl_sync(0xffffffffu, x0, srcB);
       const uint32_t b1 = __shfl_sync(0xffffffffu, x1, srcB);
       const uint32_t wa = (g_id & 1) ? a1 : a0, wb = (g_id & 1) ? b1 : b0;
-      pb0 = __byte_perm(wa, wb, 0x5410);
-      pb1 = __byte_perm(wa, wb, 0x7632);
+      pb[i][0] = __byte_perm(wa, wb, 0x5410);
+      pb[i][1] = __byte_perm(wa, wb, 0x7632);
     }
     // ---------------------------------------------------------------- O^T += V^T P^T
     // m-tile mt: rows g_id / g_id + 8 are dims RL g_id + 2 mt / + 1
 #pragma unroll
     for (int mt = 0; mt < KT; ++mt) {
       const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;
-      uint32_t a[4];
-      codes_to_f16<CT>(__byte_perm(va[0][mt >> 1], va[1][mt >> 1], sel), a[0], a[1]);
-      codes_to_f16<CT>(__byte_perm(va[2][mt >> 1], va[3][mt >> 1], sel), a[2], a[3]);
-      Mma<__half>::run(oacc[mt], a, pb0, pb1);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        uint32_t a[4];
+        codes_to_f16<CT>(__byte_perm(va[i][0][mt >> 1], va[i][1][mt >> 1], sel), a[0], a[1]);
+        codes_to_f16<CT>(__byte_perm(va[i][2][mt >> 1], va[i][3][mt >> 1], sel), a[2], a[3]);
+        Mma<__half>::run(oacc[mt], a, pb[i][0], pb[i][1]);
+      }
     }
-    // every lane has its codes in registers: the stage takes the next tile
-    cst = cst + 1 == NST ? 0 : cst + 1;
-    if (cst == 0) cph ^= 1;
-    --in_flight;
+    // every lane has its codes in registers: the stages take the next tiles
     __syncwarp();
-    if (nxt.blk >= 0 && !dead) {
-      issue(nxt);
-      nxt = next_tile(nxt);
-      __syncwarp();
-    }
+#pragma unroll 1
+    for (int i = 0; i < NQ && k_issued < k_end; ++i, ++k_issued) issue(k_issued);
   }
   st_d[0] = sum_over_groups(st_d[0]);
   st_d[1] = sum_over_groups(st_d[1]);
 
   // ---------------------------------------------------------------- finish the segment
-  // This thread holds columns 2 q4 (o0, o2) and 2 q4 + 1 (o1, o3), dims RL g_id .. + RL - 1
+  // This thread holds columns 2 q4 (o0, o2) and 2 q4 + 1 (o1, o3), dims RL g_id .. + RL - 1.
+  // A segment within the range goes to out/lse; else its state (O / d, lse) waits in shared
+  // memory for the block's other warps.
   const bool whole = (ua == 0 && ub == sg.n);
-  const size_t slot = (size_t)(2 * wid + (sg.off <= ws.x0 ? 0 : 1)) * kMaxGroupPerCta;
+  const int side = sg.off <= ws.x0 ? 0 : 1;
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh) {
     const int j = 2 * q4 + hh;
     if (j < hcount) {
       const bool empty = st_d[hh] == 0.f;
-      float inv = empty ? 0.f : exp2f(st_n[hh] - st_m[hh]) / st_d[hh];
+      float inv = empty ? 0.f : fast_exp2(st_n[hh] - st_m[hh]) / st_d[hh];
       float l = empty ? kEmptyM : st_m[hh] + log2f(st_d[hh]);
       const size_t row = col_row<MQ>(p, sg.b, hk, c0 + j);
       if (whole && p.sink) {
@@ -511,67 +561,171 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
         inv *= sa.scale;
         l = sa.lse;
       }
-      float v[RL];
 #pragma unroll
-      for (int o = 0; o < RL; ++o) v[o] = oacc[o >> 1][hh + 2 * (o & 1)] * inv;
-      if (whole) {
-        store_run<RL>(p, row * D + RL * g_id, v);
-      } else {
-        float4* po = reinterpret_cast<float4*>(p.part_o + (slot + j) * D + RL * g_id);
-#pragma unroll
-        for (int i = 0; i < RL / 4; ++i) po[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      for (int o = 0; o < RL / 4; ++o) {
+        const float4 v = make_float4(oacc[2 * o][hh] * inv, oacc[2 * o][hh + 2] * inv,
+                                     oacc[2 * o + 1][hh] * inv, oacc[2 * o + 1][hh + 2] * inv);
+        if (whole) store_four(p, row * D + RL * g_id + 4 * o, v);
+        else reinterpret_cast<float4*>(state_of(warp, side) + j * D + RL * g_id)[o] = v;
       }
       if (g_id == 0) {
         if (whole) p.lse[row] = l;
-        else p.part_lse[slot + j] = l;
+        else s_plse[warp][side][j] = l;
       }
     }
   }
-  if (!whole) {
-    // publish the partial; the worker completing the segment's count merges later
-    fence_acq_rel_gpu();
-    __syncwarp();
-    int last = 0;
-    if (lane == 0) {
-      int* cnt = p.counters + (size_t)sg.b * p.H_kv * p.n_z + sg.hz;
-      const int mine = ub - ua;
-      const int prev = atomicAdd(cnt, mine);
-      last = (prev + mine == sg.n);
-      if (last) *cnt = 0;
-    }
-    last = __shfl_sync(0xffffffffu, last, 0);
-    if (last) {
-      fence_acq_rel_gpu();
-      if (lane == 0) {
-        s_pend[warp][npend][0] = sg.b;
-        s_pend[warp][npend][1] = sg.hz;
-        s_pend[warp][npend][2] = sg.off;
-        s_pend[warp][npend][3] = sg.n;
-      }
-      npend = 1;  // at most two entries
-    }
-  }
+  if (!whole && lane == 0) s_part[warp][side] = PartEntry{sg.off, sg.b, sg.hz, ub - ua, sg.n};
   }  // ua < ub
   if (sg.off + C + sg.n >= cx1 || !next_segment(p, sg, C)) break;
   }  // segments
+  if (!waited) pdl_wait();  // (a worker without units: the block's partials still follow it)
 
-  // ---------------------------------------------------------------- deferred merges
-  __syncwarp();
-  for (int i = 0; i < 2; ++i) {
-    const long long b = s_pend[warp][i][0];
-    if (b < 0) continue;
-    const int hz = (int)s_pend[warp][i][1];
-    const long long off = s_pend[warp][i][2];
-    const int n = (int)s_pend[warp][i][3];
-    const int hk = hz / p.n_z, z = hz - hk * p.n_z;
-    const int c0 = z * kMaxGroupPerCta;
-    const int hcount = min(kMaxGroupPerCta, p.ncol - c0);
-    constexpr int kBudget = 8;  // float4 partial rows per lane in flight
-    constexpr int kV4 = (4 * (D / 4) + 31) / 32, kV8 = (8 * (D / 4) + 31) / 32;
-    if (hcount <= 4)
-      warp_merge<D, 4, (kBudget / kV4 > 1 ? kBudget / kV4 : 1), MQ>(p, (int)b, off, C, n, ws.U, Wn, hk, c0, hcount, s_mw[warp], s_msl[warp], zg, (int)(wid % zg));
-    else
-      warp_merge<D, 8, (kBudget / kV8 > 1 ? kBudget / kV8 : 1), MQ>(p, (int)b, off, C, n, ws.U, Wn, hk, c0, hcount, s_mw[warp], s_msl[warp], zg, (int)(wid % zg));
+  // ---------------------------------------------------------------- partial states
+  // A segment's states within the block are merged first (lse = M + log2 sum 2^(lse_s - M), out =
+  // sum 2^(lse_s - M) o_s / sum 2^(lse_s - M)).  If the block holds all of its units that is the
+  // result; else the block publishes one state and adds its units to the segment's counter, and
+  // the block that completes the count merges the blocks' states.  So a segment split over the
+  // four warps of a block never leaves it, and one over several blocks costs a state per block.
+  if (!__syncthreads_or(lane < 2 && s_part[warp][lane].b >= 0)) return;
+  // lane k < 2 NW of every warp holds entry k; `same`: the entries of its segment
+  const PartEntry mine_e = s_part[(lane >> 1) % NW][lane & 1];
+  const bool held = lane < 2 * NW && mine_e.b >= 0;
+  const long long key = held ? (long long)mine_e.b * p.H_kv * p.n_z + mine_e.hz : -1 - lane;
+  const unsigned same_l = __match_any_sync(0xffffffffu, key);
+  int units = 0;  // of its segment in the block
+#pragma unroll
+  for (int k = 0; k < 2 * NW; ++k) {
+    const int x = __shfl_sync(0xffffffffu, mine_e.mine, k);
+    if ((same_l >> k) & 1) units += x;
+  }
+  const unsigned leaders = __ballot_sync(0xffffffffu, held && (same_l & ((1u << lane) - 1)) == 0);
+  const unsigned whole_l = __ballot_sync(0xffffffffu, held && units == mine_e.n);
+  const long long U = s_start[0].U, G = gridDim.x;
+  // one output (final) or one state in slot `to`: four dims from `acc`, unnormalised, of a column
+  auto put = [&](int b, int hz, int j, int d, float M, float den, float4 acc, bool final, long long to) {
+    const bool empty = den == 0.f;
+    float inv = empty ? 0.f : 1.f / den;
+    float l = empty ? kEmptyM : M + log2f(den);
+    const int hk = hz / p.n_z, c = (hz - hk * p.n_z) * kMaxGroupPerCta + j;
+    if (final && p.sink) {
+      const SinkAdj sa = apply_sink(p, col_head<MQ>(p, hk, c), l);
+      inv *= sa.scale;
+      l = sa.lse;
+    }
+    const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (final) {
+      const size_t row = col_row<MQ>(p, b, hk, c);
+      store_four(p, row * D + d, v);
+      if (d == 0) p.lse[row] = l;
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (to * kMaxGroupPerCta + j) * D + d) = v;
+      if (d == 0) p.part_lse[to * kMaxGroupPerCta + j] = l;
+    }
+  };
+  auto weighted = [](float4& acc, float w, float4 o) {
+    acc.x = fmaf(w, o.x, acc.x);
+    acc.y = fmaf(w, o.y, acc.y);
+    acc.z = fmaf(w, o.z, acc.z);
+    acc.w = fmaf(w, o.w, acc.w);
+  };
+  // Slots of block c, for slice z of a segment: two per block and slice, for the segment that the
+  // block's range starts in (or at) and the one that it ends in.
+  auto slot_of = [&](long long c, long long off, int hz) {
+    return (2 * c + (off <= div_floor(c * U, G) ? 0 : 1)) * zg + hz % zg;
+  };
+#pragma unroll 1
+  for (unsigned m = leaders; m; m &= m - 1) {
+    const int L = __ffs(m) - 1, b = s_part[L >> 1][L & 1].b, hz = s_part[L >> 1][L & 1].hz;
+    unsigned rest = __shfl_sync(0xffffffffu, same_l, L);
+    int id[NW];  // the segment's states: at most one per warp
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      id[i] = rest ? __ffs(rest) - 1 : -1;
+      rest &= rest - 1;
+    }
+    const bool all = (whole_l >> L) & 1;
+    const long long to = all ? 0 : slot_of(blockIdx.x, s_part[L >> 1][L & 1].off, hz);
+    const int hcount = min(kMaxGroupPerCta, p.ncol - hz % p.n_z * kMaxGroupPerCta);
+#pragma unroll 1
+    for (int it = threadIdx.x; it < hcount * (D / 4); it += NT) {
+      const int j = it / (D / 4), d = it % (D / 4) * 4;
+      float l[NW], M = kEmptyM, den = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        l[i] = id[i] >= 0 ? s_plse[id[i] >> 1][id[i] & 1][j] : kEmptyM;
+        M = fmaxf(M, l[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        if (l[i] <= kEmptyM) continue;  // (NaN counts)
+        const float w = fast_exp2(l[i] - M);
+        den += w;
+        weighted(acc, w, *reinterpret_cast<const float4*>(state_of(id[i] >> 1, id[i] & 1) + j * D + d));
+      }
+      put(b, hz, j, d, M, den, acc, all, to);
+    }
+  }
+  const unsigned open = leaders & ~whole_l;
+  if (!open) return;
+  fence_acq_rel_gpu();
+  __syncthreads();
+  if (warp == 0 && (open >> lane) & 1) {
+    int* cnt = p.counters + key;
+    const int prev = atomicAdd(cnt, units);
+    s_last[lane] = prev + units == mine_e.n;
+    if (s_last[lane]) *cnt = 0;  // every other block's units have arrived: reset for reuse
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (unsigned m = open; m; m &= m - 1) {
+    const int L = __ffs(m) - 1;
+    if (!s_last[L]) continue;
+    fence_acq_rel_gpu();
+    const PartEntry e = s_part[L >> 1][L & 1];
+    const int hcount = min(kMaxGroupPerCta, p.ncol - e.hz % p.n_z * kMaxGroupPerCta);
+    const long long first = share_of(e.off + C, U, G), slot0 = slot_of(first, e.off, e.hz);
+    const int ns = (int)(share_of(e.off + C + e.n - 1, U, G) - first + 1);
+    // state i: block first + i's; only the first can hold the segment as the one it ends in.  With
+    // fewer positions than blocks some blocks between have no units and wrote nothing.
+    auto slot_at = [&](int i) { return i ? 2 * (first + i) * zg + e.hz % zg : slot0; };
+    auto holds = [&](int i) {
+      return U >= G || div_floor((first + i) * U, G) < div_floor((first + i + 1) * U, G);
+    };
+#pragma unroll 1
+    for (int it = threadIdx.x; it < hcount * (D / 4); it += NT) {
+      const int j = it / (D / 4), d = it % (D / 4) * 4;
+      float M = kEmptyM, den = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int i0 = 0; i0 < ns; i0 += 8) {  // eight states' lse and rows in flight together
+        float l[8], m8 = M;
+        float4 o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const long long sl = slot_at(min(i0 + i, ns - 1)) * kMaxGroupPerCta + j;
+          l[i] = __ldcg(p.part_lse + sl);
+          o[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + sl * D + d));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i0 + i >= ns || !holds(i0 + i)) l[i] = kEmptyM;
+          m8 = fmaxf(m8, l[i]);
+        }
+        const float f = fast_exp2(M - m8);
+        M = m8;
+        den *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (l[i] <= kEmptyM) continue;
+          const float w = fast_exp2(l[i] - M);
+          den += w;
+          weighted(acc, w, o[i]);
+        }
+      }
+      put(e.b, e.hz, j, d, M, den, acc, true, 0);
+    }
   }
 }
 
@@ -579,9 +733,9 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
 template <typename CT, typename QT, int D, bool MQ>
 static cudaError_t launch_bs_t(const DecodeParams& p, const CUtensorMap& tm, dim3 grid,
                                cudaStream_t st, MmaConfig* cfg) {
-  constexpr int NW = kMmaWarps, NST = PD_BS_STAGES;
-  constexpr int dyn = bs_smem_bytes<D, NW, NST>();
-  auto kern = decode_bs_kernel<CT, QT, D, MQ, NW, NST>;
+  constexpr int NW = kMmaWarps;
+  constexpr int dyn = bs_smem_bytes<D, NW>();
+  auto kern = decode_bs_kernel<CT, QT, D, MQ, NW>;
   // the dynamic shared memory above 48 KB is opted into on every query of the launch
   // configuration, which the host makes once per device and variant before the first launch
   if (cfg) {

@@ -24,7 +24,8 @@ constexpr int kHostPlanInts = 1024;
 // Block schedules (DecodeParams::mode)
 enum : int {
   kSchedBalanced = 0,   // all pages of all (sequence, head-slice) segments, cut into G equal shares
-  kSchedPerSegment = 1  // one block per (sequence, head-slice) segment: no split
+  kSchedPerSegment = 1, // one block per (sequence, head-slice) segment: no split
+  kSchedPerBlock = 2    // block-scaled kernel: one block per segment, split over its warps
 };
 
 struct DecodeParams {
@@ -65,6 +66,7 @@ struct DecodeParams {
   float out_scale;    // applied to the final output (v_scale for e4m3 KV)
   const float* scales;  // 8-bit cache with a scale per block of rows: [max_pages, 2, H_kv, n_sb]
   int scale_rows, n_sb; // rows per block, blocks per page (scale_rows * n_sb = P)
+  int sb_mul;           // ceil(2^20 / scale_rows): row r < 256 of a page is in block (r * sb_mul) >> 20
   unsigned long long rope_F[kMaxHalfDim];  // fixed-point turns/position per frequency
   // Host plan: when hp_B > 0 the caller gave host copies of page_table_indptr and
   // length_info, and the launch carries them: hp[0 .. B] = prefix sums over the
@@ -465,6 +467,21 @@ __device__ void worker_starts(const DecodeParams& p, WorkerStart* s_ws, int* s_u
       } else {
         s.x1 = s.x0;
       }
+      s_ws[tid] = s;
+    }
+    __syncthreads();
+    return;
+  }
+  if (p.mode == kSchedPerBlock) {
+    if (tid < WPB) {
+      WorkerStart s;
+      s.b = (int)(blockIdx.x / HZ);
+      s.hz = (int)(blockIdx.x - (unsigned)s.b * HZ);
+      s.off = 0;
+      s.U = units_of(load_seq(p, s.b), p.P);
+      s.x0 = tid * s.U / WPB;
+      s.x1 = (tid + 1) * s.U / WPB;
+      if (s.x0 == s.x1) s.b = -1;
       s_ws[tid] = s;
     }
     __syncthreads();

@@ -98,6 +98,7 @@ struct QkParams {
   long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements from token to token
   long long q_head, k_head, q_out_head, k_out_head;          // elements from head to head
   int T, Hq, Hk, D, rd, mode, w_dtype;
+  int parts;  // warps that share a token's heads (set by the launch)
   float eps, inv_D, w_offset, attention_factor;
 };
 cudaError_t launch_qk_norm_rope(const QkParams& a, int dtype, int num_sms, cudaStream_t st);

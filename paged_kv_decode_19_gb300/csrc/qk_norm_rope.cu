@@ -12,10 +12,9 @@
 //
 // Bound by the bytes, 2 x row, for many tokens and by launch and load latency for few.  A
 // row is read by D / 8 lanes in 16-byte chunks (one for 16-bit types) and stays in
-// registers: the mean needs log2(D / 8) shuffles and the rotate-half partner is a shuffle of
-// the normalised values.  The angles depend on the token alone, so a block computes a token's
-// rd / 2 cosines and sines once, in shared memory, for all its heads; they cost about 40
-// instructions each, which one row a lane would otherwise pay eight times over.
+// registers; the mean needs log2(D / 8) shuffles.  The angles depend on the token alone, so a
+// warp computes a token's rd / 2 cosines and sines once, in shared memory, for all the heads it
+// takes; they cost about 40 instructions each, which a row's lanes would otherwise pay per value.
 #include <type_traits>
 
 #include "common.cuh"
@@ -47,139 +46,204 @@ struct Vec8 {
   uint4 v[sizeof(XT) * 8 / 16];
 };
 template <typename XT>
-__device__ __forceinline__ void unpack8(const Vec8<XT>& r, float (&x)[8]) {
-  if constexpr (sizeof(XT) == 4) {
+__device__ __forceinline__ void unpack8(const Vec8<XT>& r, float2 (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float((&r.v[i >> 2].x)[i & 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2<XT>((&r.v[0].x)[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(XT) == 4)
+      x[i] = make_float2(__uint_as_float((&r.v[i >> 1].x)[2 * (i & 1)]), __uint_as_float((&r.v[i >> 1].x)[2 * (i & 1) + 1]));
+    else
+      x[i] = unpack2<XT>((&r.v[0].x)[i]);
   }
 }
 template <typename XT>
-__device__ __forceinline__ Vec8<XT> pack8(const float (&x)[8]) {
+__device__ __forceinline__ Vec8<XT> pack8(const float2 (&x)[4]) {
   Vec8<XT> r;
-  if constexpr (sizeof(XT) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) (&r.v[i >> 2].x)[i & 3] = __float_as_uint(x[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) (&r.v[0].x)[i] = pack2<XT>(x[2 * i], x[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(XT) == 4) {
+      (&r.v[i >> 1].x)[2 * (i & 1)] = __float_as_uint(x[i].x);
+      (&r.v[i >> 1].x)[2 * (i & 1) + 1] = __float_as_uint(x[i].y);
+    } else {
+      (&r.v[0].x)[i] = pack2<XT>(x[i].x, x[i].y);
+    }
   }
   return r;
 }
 
-// Rows in 16-byte chunks: D a multiple of 8 (at most 8 LPR), 16-byte aligned rows, a rotated
-// part that ends on a chunk (rotate-half: each half does).  MODE 0 no rotation, 1 rotate-half,
-// 2 interleaved.  blockIdx.y: which RU * 256 / LPR heads of the token; tokens by grid stride.
-template <typename XT, int MODE, int LPR, int RU>
-__global__ void __launch_bounds__(kQkThreads)
+// Four floats of shared memory at `a` and four at `b` (16-byte aligned) as pairs.
+__device__ __forceinline__ void load_pairs(const float* a, const float* b, float2 (&v)[4]) {
+  const float4 x = *reinterpret_cast<const float4*>(a), y = *reinterpret_cast<const float4*>(b);
+  v[0] = make_float2(x.x, x.y);
+  v[1] = make_float2(x.z, x.w);
+  v[2] = make_float2(y.x, y.y);
+  v[3] = make_float2(y.z, y.w);
+}
+
+// Rows in vectors: D a multiple of 8 (at most 8 LPR), 16-byte aligned rows, a rotated part that
+// is a multiple of 8.  MODE 0 no rotation, 1 rotate-half, 2 interleaved; a lane holds eight dims,
+// both of every rotated pair (rotate-half: four of each half, as two 8-byte accesses of a 16-bit
+// row; a 16-byte chunk and a shuffle for the partner cost 4 us more of {NEW}).  A pass is 32 / LPR heads of one token, all queries or all keys; a warp takes
+// part `p` of the `parts` of a token's passes (grid stride over the T * parts tasks), GP passes
+// at a time, the next GP loaded while these are computed.  No block barrier after the start:
+// the warps drift apart, so that loads, products and stores of different tokens overlap (with
+// a block per token and a barrier for its angles the same loads took 48 us instead of {NEW}
+// for 8192 tokens of 40 heads).
+//
+// With x' the rotation partner of x, an output is rs (x A + x' B), A = w cos and B = -+ w' sin:
+// A and B are the same for every query (key) head of a token, so a row costs two products per
+// value, packed in pairs.
+template <typename XT, int MODE, int LPR>
+__global__ void __launch_bounds__(kQkThreads, 3)
     qk_norm_rope_kernel(const __grid_constant__ QkParams a) {
-  constexpr int RG = kQkThreads / LPR;  // rows per pass of the block
+  constexpr int NW = kQkThreads / 32, RW = 32 / LPR;  // rows per pass
+  constexpr int NV = (int)sizeof(XT) * 8 / 16, GP = sizeof(XT) == 4 ? 2 : 4;
+  constexpr int NF = MODE ? 4 * LPR : 4;              // frequencies, at most
   __shared__ __align__(16) float s_w[2][8 * LPR];
-  __shared__ __align__(16) float s_cos[2][MODE ? 4 * LPR : 4], s_sin[2][MODE ? 4 * LPR : 4];
+  __shared__ unsigned long long s_F[NF];
+  __shared__ __align__(16) float s_ang[NW][2][NF];    // a warp's token: cosines, sines
   pdl_wait();
   pdl_release();
-  const int tid = threadIdx.x, sub = tid % LPR, row0 = blockIdx.y * (RG * RU) + tid / LPR;
-  const int H = a.Hq + a.Hk, nf = a.rd / 2;
-  for (int i = tid; i < 2 * a.D; i += kQkThreads) {
-    const int k = i >= a.D, d = i - k * a.D;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane % LPR, row = lane / LPR;
+  const int nf = a.rd / 2, q_passes = (a.Hq + RW - 1) / RW, passes = q_passes + (a.Hk + RW - 1) / RW;
+  for (int i = tid; i < 16 * LPR; i += kQkThreads) {
+    const int k = i / (8 * LPR), d = i % (8 * LPR);
     const void* w = k ? a.k_weight : a.q_weight;
-    if (w) s_w[k][d] = weight_at(w, a.w_dtype, d) + a.w_offset;
+    s_w[k][d] = w && d < a.D ? weight_at(w, a.w_dtype, d) + a.w_offset : 1.f;
   }
-  unsigned long long F = 0;
-  if (MODE && tid < nf) F = freq_turns(__ldg(a.freq + tid));
-  const int c = sub * 8;             // this lane's dims
-  const bool live = c < a.D, turns = MODE && c < a.rd;
-  // rotate-half: this lane's chunk and its partner's, half a rotated part away
-  const bool first_half = c < nf;
-  const int partner = (tid & 31) + (first_half ? nf / 8 : -(nf / 8));
-  const int f0 = MODE == 1 ? (first_half ? c : c - nf) : c / 2;
-  for (int t = blockIdx.x, buf = 0; t < a.T; t += gridDim.x, buf ^= 1) {
-    Vec8<XT> raw[RU];
+  if (MODE && tid < nf) s_F[tid] = freq_turns(__ldg(a.freq + tid));
+  __syncthreads();
+  // This lane's dims: d .. d + 3 and d + apart .. + 3.  Rotate-half: pairs of the rotated part,
+  // then of what passes; else eight in a row.
+  int d = sub * 8, apart = 4;
+  if (MODE == 1) {
+    const int i = sub * 4;
+    d = i < nf ? i : a.rd + i - nf;
+    apart = i < nf ? nf : (a.D - a.rd) / 2;
+  }
+  const bool live = sub * 8 < a.D, turns = MODE && d < a.rd;
+  const int f0 = MODE == 1 ? d : d / 2;  // this lane's first frequency
+  const long long tasks = (long long)a.T * a.parts;
+  for (long long task = (long long)blockIdx.x * NW + warp; task < tasks; task += (long long)gridDim.x * NW) {
+    const int t = (int)(task / a.parts), part = (int)(task - (long long)t * a.parts);
+    const int p0 = part * passes / a.parts, p1 = (part + 1) * passes / a.parts;
+    bool have_angles = MODE == 0;
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {  // the queries' passes of the part, then the keys'
+      const int s0 = k ? max(p0 - q_passes, 0) : min(p0, q_passes);
+      int n = (k ? max(p1 - q_passes, 0) : min(p1, q_passes)) - s0;
+      if (n <= 0) continue;
+      const long long step = RW * (k ? a.k_head : a.q_head), step_to = RW * (k ? a.k_out_head : a.q_out_head);
+      const XT* src = reinterpret_cast<const XT*>(k ? a.k : a.q) + (k ? t * a.k_stride : t * a.q_stride) +
+                      row * (k ? a.k_head : a.q_head) + d + s0 * step;
+      XT* dst = reinterpret_cast<XT*>(k ? a.k_out : a.q_out) + (k ? t * a.k_out_stride : t * a.q_out_stride) +
+                row * (k ? a.k_out_head : a.q_out_head) + d + s0 * step_to;
+      // passes with a head for this lane: all but perhaps the side's last
+      int mine = live ? min(n, ((k ? a.Hk : a.Hq) - row + RW - 1) / RW - s0) : 0;
+      const bool normed = k ? a.k_weight != nullptr : a.q_weight != nullptr;
+      auto load = [&](Vec8<XT> (&raw)[GP]) {  // the next GP passes
 #pragma unroll
-    for (int u = 0; u < RU; ++u) {
-      const int r = row0 + u * RG;
+        for (int u = 0; u < GP; ++u)
+          if (u < mine) {
+            if constexpr (MODE == 1 && NV == 1) {
+              const uint2 x = *reinterpret_cast<const uint2*>(src + u * step);
+              const uint2 y = *reinterpret_cast<const uint2*>(src + u * step + apart);
+              raw[u].v[0] = make_uint4(x.x, x.y, y.x, y.y);
+            } else {
 #pragma unroll
-      for (int i = 0; i < (int)(sizeof(XT) * 8 / 16); ++i) raw[u].v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < H && live) {
-        const bool k = r >= a.Hq;
-        const XT* src = reinterpret_cast<const XT*>(k ? a.k : a.q) +
-                        (k ? t * a.k_stride + (r - a.Hq) * a.k_head : t * a.q_stride + r * a.q_head) + c;
+              for (int i = 0; i < NV; ++i) raw[u].v[i] = *reinterpret_cast<const uint4*>(src + u * step + i * apart);
+            }
+          }
+        src += GP * step;
+      };
+      Vec8<XT> cur[GP], nxt[GP];
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(XT) * 8 / 16); ++i)
-          raw[u].v[i] = *(reinterpret_cast<const uint4*>(src) + i);
+      for (int u = 0; u < GP; ++u)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) cur[u].v[i] = nxt[u].v[i] = make_uint4(0u, 0u, 0u, 0u);
+      load(cur);
+      if constexpr (MODE != 0) {
+        if (!have_angles) {
+          have_angles = true;
+          const int pos = __ldg(a.positions + t);
+          __syncwarp();  // the last token's angles have been read
+#pragma unroll
+          for (int i = 0; i < NF; i += 32) {
+            if (i + lane < nf) {
+              float co, si;
+              rope_cos_sin_accurate(pos, s_F[i + lane], co, si);
+              s_ang[warp][0][i + lane] = co * a.attention_factor;
+              s_ang[warp][1][i + lane] = si * a.attention_factor;
+            }
+          }
+          __syncwarp();
+        }
       }
-    }
-    if (MODE && tid < nf) {
-      float co, si;
-      rope_cos_sin_accurate(__ldg(a.positions + t), F, co, si);
-      s_cos[buf][tid] = co * a.attention_factor;
-      s_sin[buf][tid] = si * a.attention_factor;
-    }
-    __syncthreads();  // (two buffers: one barrier per token)
-    float co[8], si[8];  // MODE 2 uses the first four
+      float2 A[4], B[4];
+      load_pairs(&s_w[k][d], &s_w[k][live ? d + apart : d], A);
+      if constexpr (MODE != 0) {
+        float2 co[4], si[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) co[i] = si[i] = 0.f;
-    if (turns) {
-#pragma unroll
-      for (int i = 0; i < (MODE == 1 ? 8 : 4); i += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(&s_cos[buf][f0 + i]);
-        const float4 y = *reinterpret_cast<const float4*>(&s_sin[buf][f0 + i]);
-        co[i] = x.x; co[i + 1] = x.y; co[i + 2] = x.z; co[i + 3] = x.w;
-        si[i] = y.x; si[i + 1] = y.y; si[i + 2] = y.z; si[i + 3] = y.w;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < RU; ++u) {
-      const int r = row0 + u * RG;
-      const bool k = r >= a.Hq;
-      float x[8];
-      unpack8<XT>(raw[u], x);
-      if (a.q_weight || a.k_weight) {  // (the shuffles take the whole warp)
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (k ? a.k_weight != nullptr : a.q_weight != nullptr) {
-          const float rs = rsqrtf(ss * a.inv_D + a.eps);
-#pragma unroll
-          for (int i = 0; i < 8; i += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(&s_w[k][c + i]);
-            x[i] *= rs * w.x;
-            x[i + 1] *= rs * w.y;
-            x[i + 2] *= rs * w.z;
-            x[i + 3] *= rs * w.w;
+        for (int i = 0; i < 4; ++i) co[i] = make_float2(1.f, 1.f), si[i] = make_float2(0.f, 0.f);
+        if (turns) {
+          const float4 x = *reinterpret_cast<const float4*>(&s_ang[warp][0][f0]);
+          const float4 y = *reinterpret_cast<const float4*>(&s_ang[warp][1][f0]);
+          if constexpr (MODE == 1) {
+            co[0] = co[2] = make_float2(x.x, x.y), co[1] = co[3] = make_float2(x.z, x.w);
+            si[2] = make_float2(y.x, y.y), si[3] = make_float2(y.z, y.w);
+            si[0] = make_float2(-y.x, -y.y), si[1] = make_float2(-y.z, -y.w);
+          } else {
+            co[0] = make_float2(x.x, x.x), co[1] = make_float2(x.y, x.y);
+            co[2] = make_float2(x.z, x.z), co[3] = make_float2(x.w, x.w);
+            si[0] = make_float2(-y.x, y.x), si[1] = make_float2(-y.y, y.y);
+            si[2] = make_float2(-y.z, y.z), si[3] = make_float2(-y.w, y.w);
           }
         }
-      }
-      if constexpr (MODE == 1) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float other = __shfl_sync(0xffffffffu, x[i], partner & 31);
-          if (turns) x[i] = x[i] * co[i] + (first_half ? -other : other) * si[i];
-        }
-      } else if constexpr (MODE == 2) {
-        if (turns) {
+        for (int i = 0; i < 4; ++i)
+          B[i] = mul_f2(MODE == 1 ? A[i ^ 2] : make_float2(A[i].y, A[i].x), si[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) A[i] = mul_f2(A[i], co[i]);
+      }
+#pragma unroll 1
+      for (; n > 0; n -= GP) {
+        const int now = mine;
+        mine -= GP;
+        load(nxt);  // (none left: nothing)
+#pragma unroll
+        for (int u = 0; u < GP; ++u) {
+          if (u >= n) break;  // (warp-uniform)
+          float2 x[4], y[4];
+          unpack8<XT>(cur[u], x);
+          float rs = 1.f;
+          if (normed) {
+            float2 ss = mul_f2(x[0], x[0]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) ss = fma_f2(x[i], x[i], ss);
+            float sum = ss.x + ss.y;
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            rs = rsqrtf(sum * a.inv_D + a.eps);
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float p = x[2 * i], q = x[2 * i + 1];
-            x[2 * i] = p * co[i] - q * si[i];
-            x[2 * i + 1] = q * co[i] + p * si[i];
+            float2 z = mul_f2(x[i], A[i]);
+            if (MODE && turns) z = fma_f2(MODE == 1 ? x[i ^ 2] : make_float2(x[i].y, x[i].x), B[i], z);
+            y[i] = mul_f2(z, make_float2(rs, rs));
+          }
+          if (u < now) {
+            const Vec8<XT> o = pack8<XT>(y);
+            if constexpr (MODE == 1 && NV == 1) {
+              *reinterpret_cast<uint2*>(dst + u * step_to) = make_uint2(o.v[0].x, o.v[0].y);
+              *reinterpret_cast<uint2*>(dst + u * step_to + apart) = make_uint2(o.v[0].z, o.v[0].w);
+            } else {
+#pragma unroll
+              for (int i = 0; i < NV; ++i) *reinterpret_cast<uint4*>(dst + u * step_to + i * apart) = o.v[i];
+            }
           }
         }
-      }
-      if (r < H && live) {
-        XT* dst = reinterpret_cast<XT*>(k ? a.k_out : a.q_out) +
-                  (k ? t * a.k_out_stride + (r - a.Hq) * a.k_out_head : t * a.q_out_stride + r * a.q_out_head) + c;
-        const Vec8<XT> o = pack8<XT>(x);
+        dst += GP * step_to;
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(XT) * 8 / 16); ++i) *(reinterpret_cast<uint4*>(dst) + i) = o.v[i];
+        for (int u = 0; u < GP; ++u) cur[u] = nxt[u];
       }
     }
   }
@@ -249,21 +313,16 @@ __global__ void __launch_bounds__(kQkThreads)
 
 // ------------------------------------------------------------------------- dispatch
 template <typename XT, int MODE, int LPR>
-static cudaError_t launch_vec(const QkParams& a, int num_sms, cudaStream_t st) {
-  constexpr int RG = kQkThreads / LPR;
-  const int H = a.Hq + a.Hk;
-  // Few tokens: one pass of rows per block, so that every row is in flight at once.  Many:
-  // up to four passes per block share a token's angles and barrier.
-  const int passes = (H + RG - 1) / RG;
-  if ((long long)a.T * passes <= 8ll * num_sms || passes == 1) {
-    const dim3 grid((unsigned)min((long long)a.T, 8ll * num_sms), (unsigned)passes);
-    return launch_pdl(qk_norm_rope_kernel<XT, MODE, LPR, 1>, grid, dim3(kQkThreads), 0, st, a);
-  }
-  const int per = passes <= 2 ? 2 : passes == 3 ? 3 : 4;
-  const dim3 grid((unsigned)min((long long)a.T, 8ll * num_sms), (unsigned)((passes + per - 1) / per));
-  if (per == 2) return launch_pdl(qk_norm_rope_kernel<XT, MODE, LPR, 2>, grid, dim3(kQkThreads), 0, st, a);
-  if (per == 3) return launch_pdl(qk_norm_rope_kernel<XT, MODE, LPR, 3>, grid, dim3(kQkThreads), 0, st, a);
-  return launch_pdl(qk_norm_rope_kernel<XT, MODE, LPR, 4>, grid, dim3(kQkThreads), 0, st, a);
+static cudaError_t launch_vec(QkParams a, int num_sms, cudaStream_t st) {
+  constexpr int NW = kQkThreads / 32, RW = 32 / LPR;
+  const int passes = (a.Hq + RW - 1) / RW + (a.Hk + RW - 1) / RW;
+  // A token's angles and coefficients are worth sharing among its heads while there are warps
+  // enough (about 16 a multiprocessor); with fewer tokens the heads are spread over more warps.
+  const long long want = 16ll * num_sms;
+  a.parts = (int)min((long long)passes, max(1ll, (want + a.T - 1) / a.T));
+  const long long tasks = (long long)a.T * a.parts;
+  const dim3 grid((unsigned)min((tasks + NW - 1) / NW, 4ll * num_sms));
+  return launch_pdl(qk_norm_rope_kernel<XT, MODE, LPR>, grid, dim3(kQkThreads), 0, st, a);
 }
 
 template <typename XT, int MODE>
@@ -282,7 +341,7 @@ static cudaError_t launch_x(const QkParams& a, int num_sms, cudaStream_t st) {
   const long long strides[8] = {a.q_stride, a.k_stride, a.q_out_stride, a.k_out_stride,
                                 a.q_head, a.k_head, a.q_out_head, a.k_out_head};
   for (long long s : strides) any |= (uintptr_t)(s * eb);
-  const bool vec = any % 16 == 0 && a.D % 8 == 0 && a.D <= 256 && a.rd % (mode == 1 ? 16 : 8) == 0;
+  const bool vec = any % 16 == 0 && a.D % 8 == 0 && a.D <= 256 && a.rd % 8 == 0;
   if (vec) {
     if (mode == 1) return launch_mode<XT, 1>(a, num_sms, st);
     if (mode == 2) return launch_mode<XT, 2>(a, num_sms, st);

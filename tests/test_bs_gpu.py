@@ -88,6 +88,24 @@ def test_decode_splits_and_lengths(splits, kv, D):
     _check(c, "mma", num_splits=splits, out_dt=torch.float32)
 
 
+@pytest.mark.parametrize("lengths,Hq,H,n", [([300], 32, 8, 1), ([64, 1, 0, 70, 3], 8, 8, 1), ([5000, 30, 200], 8, 2, 1),
+                                            ([40] * 37, 4, 4, 1), ([900, 3, 77], 8, 2, 2), ([700, 20], 32, 2, 1),
+                                            ([100, 16, 4000, 0], 16, 4, 4)])
+@pytest.mark.parametrize("kv,D,P,S", [("int8", 128, 16, 16), ("e4m3", 64, 64, 32)])
+def test_decode_planned_on_the_host(lengths, Hq, H, n, kv, D, P, S):
+    """Host copies of the table: a block per segment for short or even sequences, else equal
+    shares, at every warp count a segment can have."""
+    c = _case(lengths, Hq, H, D, P, S, kv, "bf16", n=n, seed=len(lengths))
+    host = pd.host_meta_of(c["indptr"], c["li"])
+    for early in (False, True):
+        _check(c, "mma", host_meta=host, early_inputs=early)
+    _check(c, "mma", host_meta=host, num_splits=3)
+    if n == 1:
+        w = _case(lengths, Hq, H, D, P, S, kv, "bf16", n=n, seed=len(lengths),
+                  wins=[(L // 2, min(4, L // 2)) for L in lengths])
+        _check(w, "mma", host_meta=pd.host_meta_of(w["indptr"], w["li"]), sink=torch.randn(Hq, device=DEV))
+
+
 def test_decode_one_long_sequence():
     _check(_case([70001], 8, 1, 128, 64, 16, "int8", "bf16", seed=8), "mma")
 
