@@ -306,7 +306,7 @@ static bool fill_host_plan(const pd_decode_desc& d, DecodeParams& p) {
 // must be resident at once, with a slice per KV head.
 constexpr int kCrossTiles = 10;
 static bool block_per_segment(const pd_decode_desc& d, int n_z, int wave) {
-  if (!d.host_indptr || d.num_splits != 0 || n_z != 1 || (long long)d.B * d.H_kv > wave) return false;
+  if (n_z != 1 || (long long)d.B * d.H_kv > wave) return false;
   const int tiles_per_page = d.page_size / 16, B = d.B;
   long long total = 0, most = 0;
   for (int b = 0; b < B; ++b) {
@@ -526,11 +526,21 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   const int wpb = use_mma ? kMmaWarps : 1;
   plan_impl(desc, ds->num_sms, ctas, wpb, &mode, &grid_blocks, &ws_need, q_len);
   if (grid_blocks == 0) return PD_OK;
-  if (bs && use_mma && block_per_segment(d, (d.H_qo / d.H_kv * q_len + kMaxGroupPerCta - 1) / kMaxGroupPerCta,
-                                         ds->num_sms * ctas)) {
-    mode = kSchedPerBlock;
-    grid_blocks = d.B * d.H_kv;
-    ws_need = 0;
+  if (bs && use_mma && mode == kSchedBalanced && d.num_splits == 0) {
+    const int wave = ds->num_sms * ctas;
+    if (d.host_indptr) {
+      if (block_per_segment(d, (d.H_qo / d.H_kv * q_len + kMaxGroupPerCta - 1) / kMaxGroupPerCta, wave)) {
+        mode = kSchedPerBlock;
+        grid_blocks = d.B * d.H_kv;
+        ws_need = 0;
+      }
+    } else if ((long long)d.B * d.H_kv < grid_blocks &&
+               d.nnz_pages * (d.page_size / 16) / d.B / kMmaWarps <=
+                   d.nnz_pages * (d.page_size / 16) * d.H_kv / ((long long)wave * kMmaWarps) + kCrossTiles) {
+      // without: as many equal shares as segments, by the mean length alone (even sequences then
+      // fall on block borders, and uneven ones are still shared equally)
+      grid_blocks = d.B * d.H_kv;
+    }
   }
 
   cudaStream_t s = (cudaStream_t)stream;

@@ -155,10 +155,11 @@ __device__ __forceinline__ void store_four(const DecodeParams& p, size_t idx, fl
 }
 
 // A warp's partial state of a segment: the segment (its place on the cost line, sequence, head
-// slice, units) and how many of its units the state holds; b < 0: none.
+// slice, units; the slice's KV head, first column and columns) and how many of its units the
+// state holds; b < 0: none.
 struct PartEntry {
   long long off;
-  int b, hz, mine, n;
+  int b, hz, mine, n, hk, c0, hcount;
 };
 // ----------------------------------------------------------------------------- kernel
 template <typename CT, typename QT, int D, bool MQ, int NW>
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
       }
     }
   }
-  if (!whole && lane == 0) s_part[warp][side] = PartEntry{sg.off, sg.b, sg.hz, ub - ua, sg.n};
+  if (!whole && lane == 0) s_part[warp][side] = PartEntry{sg.off, sg.b, sg.hz, ub - ua, sg.n, hk, c0, hcount};
   }  // ua < ub
   if (sg.off + C + sg.n >= cx1 || !next_segment(p, sg, C)) break;
   }  // segments
@@ -602,19 +603,18 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
   const unsigned whole_l = __ballot_sync(0xffffffffu, held && units == mine_e.n);
   const long long U = s_start[0].U, G = gridDim.x;
   // one output (final) or one state in slot `to`: four dims from `acc`, unnormalised, of a column
-  auto put = [&](int b, int hz, int j, int d, float M, float den, float4 acc, bool final, long long to) {
+  auto put = [&](const PartEntry& e, int j, int d, float M, float den, float4 acc, bool final, long long to) {
     const bool empty = den == 0.f;
     float inv = empty ? 0.f : 1.f / den;
     float l = empty ? kEmptyM : M + log2f(den);
-    const int hk = hz / p.n_z, c = (hz - hk * p.n_z) * kMaxGroupPerCta + j;
     if (final && p.sink) {
-      const SinkAdj sa = apply_sink(p, col_head<MQ>(p, hk, c), l);
+      const SinkAdj sa = apply_sink(p, col_head<MQ>(p, e.hk, e.c0 + j), l);
       inv *= sa.scale;
       l = sa.lse;
     }
     const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (final) {
-      const size_t row = col_row<MQ>(p, b, hk, c);
+      const size_t row = col_row<MQ>(p, e.b, e.hk, e.c0 + j);
       store_four(p, row * D + d, v);
       if (d == 0) p.lse[row] = l;
     } else {
@@ -630,12 +630,13 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
   };
   // Slots of block c, for slice z of a segment: two per block and slice, for the segment that the
   // block's range starts in (or at) and the one that it ends in.
-  auto slot_of = [&](long long c, long long off, int hz) {
-    return (2 * c + (off <= div_floor(c * U, G) ? 0 : 1)) * zg + hz % zg;
+  auto slot_of = [&](long long c, bool ends_in, int hz) {
+    return (2 * c + ends_in) * zg + (zg > 1 ? hz % zg : 0);
   };
 #pragma unroll 1
   for (unsigned m = leaders; m; m &= m - 1) {
-    const int L = __ffs(m) - 1, b = s_part[L >> 1][L & 1].b, hz = s_part[L >> 1][L & 1].hz;
+    const int L = __ffs(m) - 1;
+    const PartEntry e = s_part[L >> 1][L & 1];
     unsigned rest = __shfl_sync(0xffffffffu, same_l, L);
     int id[NW];  // the segment's states: at most one per warp
 #pragma unroll
@@ -644,10 +645,9 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
       rest &= rest - 1;
     }
     const bool all = (whole_l >> L) & 1;
-    const long long to = all ? 0 : slot_of(blockIdx.x, s_part[L >> 1][L & 1].off, hz);
-    const int hcount = min(kMaxGroupPerCta, p.ncol - hz % p.n_z * kMaxGroupPerCta);
+    const long long to = all ? 0 : slot_of(blockIdx.x, e.off > s_start[0].x0, e.hz);  // (x0: the block's)
 #pragma unroll 1
-    for (int it = threadIdx.x; it < hcount * (D / 4); it += NT) {
+    for (int it = threadIdx.x; it < e.hcount * (D / 4); it += NT) {
       const int j = it / (D / 4), d = it % (D / 4) * 4;
       float l[NW], M = kEmptyM, den = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
         den += w;
         weighted(acc, w, *reinterpret_cast<const float4*>(state_of(id[i] >> 1, id[i] & 1) + j * D + d));
       }
-      put(b, hz, j, d, M, den, acc, all, to);
+      put(e, j, d, M, den, acc, all, to);
     }
   }
   const unsigned open = leaders & ~whole_l;
@@ -683,17 +683,17 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
     if (!s_last[L]) continue;
     fence_acq_rel_gpu();
     const PartEntry e = s_part[L >> 1][L & 1];
-    const int hcount = min(kMaxGroupPerCta, p.ncol - e.hz % p.n_z * kMaxGroupPerCta);
-    const long long first = share_of(e.off + C, U, G), slot0 = slot_of(first, e.off, e.hz);
+    const long long first = share_of(e.off + C, U, G);
     const int ns = (int)(share_of(e.off + C + e.n - 1, U, G) - first + 1);
     // state i: block first + i's; only the first can hold the segment as the one it ends in.  With
     // fewer positions than blocks some blocks between have no units and wrote nothing.
-    auto slot_at = [&](int i) { return i ? 2 * (first + i) * zg + e.hz % zg : slot0; };
+    const bool ends_in = e.off > div_floor(first * U, G);
+    auto slot_at = [&](int i) { return slot_of(first + i, i == 0 && ends_in, e.hz); };
     auto holds = [&](int i) {
       return U >= G || div_floor((first + i) * U, G) < div_floor((first + i + 1) * U, G);
     };
 #pragma unroll 1
-    for (int it = threadIdx.x; it < hcount * (D / 4); it += NT) {
+    for (int it = threadIdx.x; it < e.hcount * (D / 4); it += NT) {
       const int j = it / (D / 4), d = it % (D / 4) * 4;
       float M = kEmptyM, den = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
           weighted(acc, w, o[i]);
         }
       }
-      put(e.b, e.hz, j, d, M, den, acc, true, 0);
+      put(e, j, d, M, den, acc, true, 0);
     }
   }
 }
