@@ -222,8 +222,8 @@ static cudaError_t bs_mma_dispatch(const DecodeParams& p, const CUtensorMap& tm,
                            : launch_bs_int(p, tm, q_dtype, grid, st, cfg);
 }
 
-// The pages of an 8-bit cache as TMA boxes of 16 rows: [max_pages * 2 * H_kv, P, D] bytes,
-// swizzled by row size (the layout decode_bs.cuh reads).
+// The pages of an 8-bit cache as TMA boxes of 16 rows of a head, K and V: [max_pages, 2, H_kv, P, D]
+// bytes, swizzled by row size (the layout decode_bs.cuh reads).
 static pd_status page_boxes(const pd_decode_desc& d, const void* pages, CUtensorMap* tm) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
@@ -242,10 +242,11 @@ static pd_status page_boxes(const pd_decode_desc& d, const void* pages, CUtensor
     encode = reinterpret_cast<Encode>(fn);
     known.store(encode);
   }
-  const cuuint64_t dims[3] = {(cuuint64_t)d.D, (cuuint64_t)d.page_size, (cuuint64_t)d.max_pages * 2 * d.H_kv};
-  const cuuint64_t strides[2] = {(cuuint64_t)d.D, (cuuint64_t)d.D * d.page_size};
-  const cuuint32_t box[3] = {(cuuint32_t)d.D, 16, 1}, step[3] = {1, 1, 1};
-  const CUresult r = encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pages), dims, strides, box,
+  const cuuint64_t row = (cuuint64_t)d.D, head = row * d.page_size, side = head * d.H_kv;
+  const cuuint64_t dims[5] = {row, (cuuint64_t)d.page_size, (cuuint64_t)d.H_kv, 2, (cuuint64_t)d.max_pages};
+  const cuuint64_t strides[4] = {row, head, side, 2 * side};
+  const cuuint32_t box[5] = {(cuuint32_t)d.D, 16, 1, 2, 1}, step[5] = {1, 1, 1, 1, 1};
+  const CUresult r = encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(pages), dims, strides, box,
                             step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             d.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

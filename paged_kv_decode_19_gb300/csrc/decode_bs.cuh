@@ -79,12 +79,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
-// Box of the tensor map at (x bytes, row y, block z) -> shared memory, counted on `bar`.
-__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* tm, int x, int y, int z,
-                                             uint32_t bar) {
+// Rows y .. y + 15 of a page's head, K then V (one box of the tensor map) -> shared memory,
+// counted on `bar`.
+__device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap* tm, int y, int head, int page,
+                                              uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-      ::"r"(dst), "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %2, %5}], [%6];"
+      ::"r"(dst), "l"(tm), "r"(0), "r"(y), "r"(head), "r"(page), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void cp_async_scale(uint32_t dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -98,9 +99,10 @@ struct BsTile {
   static constexpr int KCH = D / 64;     // 16-byte K chunks per row and thread
   static constexpr int RL = D / 8;       // V bytes (output dims) per row and thread
   static constexpr int kBytes = 16 * RB; // one tile of K (or V) codes
-  static constexpr int kStage = 2 * kBytes;
+  static constexpr int kPair = 2 * kBytes;  // K and V
   static constexpr int NQ = D == 64 ? 4 : 2;      // tiles computed together
-  static constexpr int NST = PD_BS_STAGES * NQ;   // ring stages per warp
+  static constexpr int NST = PD_BS_STAGES;        // ring stages per warp, of NQ tiles each
+  static constexpr int kStage = NQ * kPair;
   static constexpr int kState = kMaxGroupPerCta * D * 4;  // a partial state's outputs, fp32
   static_assert(D == 64 || D == 128, "head dim");
 };
@@ -174,11 +176,11 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
   __shared__ int s_last[2 * NW];
   __shared__ WorkerStart s_start[NW];
   __shared__ __align__(8) uint64_t s_bar[NW][NST];
-  __shared__ float4 s_meta[NW][NST];  // of the stage's tile: K and V scale, attended rows, first row's index
+  __shared__ float4 s_meta[NW][NST][NQ];  // of a tile: K and V scale, attended rows, first row's index
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint8_t* const rings = s_raw + (((smem_u32(s_raw) + 1023u) & ~1023u) - smem_u32(s_raw));
-  const uint32_t bar0 = smem_u32(&s_bar[warp][0]), meta0 = smem_u32(&s_meta[warp][0]);
+  const uint32_t bar0 = smem_u32(&s_bar[warp][0]), meta0 = smem_u32(&s_meta[warp][0][0]);
   uint8_t* const my_ring = rings + warp * NST * T::kStage;
   const uint32_t ring = smem_u32(my_ring);
   // the rings' space before the first fill: scratch of the start-up scan; after a warp's last
@@ -194,8 +196,8 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
     if (p.values) prefetch_l2_share(p.values, (size_t)p.nnz_pages * sizeof(int32_t), blockIdx.x, gridDim.x);
   }
   if (lane == 0) {
-    // two arrivals per fill: the issuing lane's (with the boxes' bytes) and its cp.async copies'
-    for (int i = 0; i < NST; ++i) mbar_init(bar0 + i * 8, 2);
+    // per tile two arrivals: the issuing lane's (with the box's bytes) and its cp.async copies'
+    for (int i = 0; i < NST; ++i) mbar_init(bar0 + i * 8, 2 * NQ);
     mbar_init_fence();
   }
   // With a host plan the start-up reads launch parameters alone and runs under the tail of the
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
 #pragma unroll
   for (int i = 0; i < 2; ++i) voff[i] = tile_off<D>(vr[i], RL * g_id);
 
-  // The ring: tiles are filled into stage `ist` and read from stage `cst`, in order.
+  // The ring: NQ tiles at a time are filled into stage `ist` and read from stage `cst`, in order.
   int ist = 0, cst = 0;
   uint32_t cph = 0;   // parity of the fill that stage cst waits for
   bool dead = false;  // a wait ran out: no further fills
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
     return pidx < sg.seq.npages && (long long)sg.seq.page_begin + pidx < p.nnz_pages
                ? __ldg(p.values + sg.seq.page_begin + pidx) : -1;
   };
-  int t_blk = -1, t_row = 0, t_span = 0, t_r0 = 0, page_next = load_page(lane);
+  int t_page = -1, t_row = 0, t_span = 0, t_r0 = 0, page_next = load_page(lane);
   auto load_batch = [&](int k0) {  // tiles k0 .. k0 + 31
     const int k = k0 + lane, page = page_next;
     page_next = load_page(k + 32);
@@ -297,26 +299,27 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
     t_row = o % P;
     t_span = max((in_a ? a_lo : b_lo) - o, 0) | (min((in_a ? a_hi : b_hi) - o, 16) << 8);
     t_r0 = in_a ? o : o - pcs.shift;
-    t_blk = page * 2 * p.H_kv + hk;
+    t_page = page;
     if (page < 0 || page >= p.max_pages) {
       if (k < n_tiles) set_error(p.err, kErrBadPage);
-      t_blk = -1;  // no such tile, or its rows do not count
+      t_page = -1;  // no such tile, or its rows do not count
     }
   };
-  // tile k (the next in order) -> stage ist
+  // tiles k .. k + NQ - 1 (the next in order; their lanes side by side) -> stage ist
   auto issue = [&](int k) {
     if ((k & 31) == 0) load_batch(k);
-    if (lane == (k & 31)) {
-      const uint32_t bar = bar0 + ist * 8, dst = ring + ist * T::kStage, meta = meta0 + ist * 16;
-      if (t_blk >= 0) {
+    const int i = lane - (k & 31);
+    if ((unsigned)i < (unsigned)NQ) {
+      const uint32_t bar = bar0 + ist * 8, dst = ring + ist * T::kStage + i * T::kPair;
+      const uint32_t meta = meta0 + (ist * NQ + i) * 16;
+      if (t_page >= 0) {
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(meta + 8), "r"(t_span), "r"(t_r0) : "memory");
-        const float* ks = p.scales + (size_t)t_blk * p.n_sb + ((t_row * p.sb_mul) >> 20);
+        const float* ks = p.scales + (size_t)(t_page * 2 * p.H_kv + hk) * p.n_sb + ((t_row * p.sb_mul) >> 20);
         cp_async_scale(meta, ks);
         cp_async_scale(meta + 4, ks + (size_t)p.H_kv * p.n_sb);
         mbar_arrive_cp_async(bar);
-        mbar_arrive_expect_tx(bar, T::kStage);
-        tma_load_box(dst, &tm, 0, t_row, t_blk, bar);
-        tma_load_box(dst + T::kBytes, &tm, 0, t_row, t_blk + p.H_kv, bar);
+        mbar_arrive_expect_tx(bar, T::kPair);
+        tma_load_tile(dst, &tm, t_row, hk, t_page, bar);
       } else {  // no attended row, zero scales
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(meta), "r"(0) : "memory");
         mbar_arrive(bar);
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
   // tiles are computed NQ at a time: the last few may be empty ones
   int k_issued = 0, k_end = dead ? 0 : (n_tiles + NQ - 1) / NQ * NQ;
 #pragma unroll 1
-  for (; k_issued < min(NST, k_end); ++k_issued) issue(k_issued);
+  for (; k_issued < min(NST * NQ, k_end); k_issued += NQ) issue(k_issued);
 
   // ---------------------------------------------------------------- Q^T B fragments
   // k-tile kt: dims 16 (4 (kt >> 2) + q4) + 4 (kt & 3) + {0, 1} and + {2, 3} of column g_id,
@@ -376,21 +379,14 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
   // overlap in the warp, and share the vote and the rescale
 #pragma unroll 1
   for (int k = 0; k < k_end; k += NQ) {
-    int stg[NQ];
-    bool ok = true;
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      stg[i] = cst;
-      ok = mbar_wait(bar0 + cst * 8, cph, dead ? 1024u : kWaitPolls) && ok;
-      cst = cst + 1 == NST ? 0 : cst + 1;
-      if (cst == 0) cph ^= 1;
-    }
+    const bool ok = mbar_wait(bar0 + cst * 8, cph, dead ? 1024u : kWaitPolls);
+    const uint8_t* const stage = my_ring + cst * T::kStage;
     float4 meta[NQ];  // K scale, V scale, attended rows [lo, hi) (bits 0-7, 8-15), first row's index
     float qacc[NQ][2][4];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      meta[i] = s_meta[warp][stg[i]];
-      const uint8_t* kt_base = my_ring + stg[i] * T::kStage;
+      meta[i] = s_meta[warp][cst][i];
+      const uint8_t* kt_base = stage + i * T::kPair;
       // -------------------------------------------------------------- S^T = C Q^T
       uint4 ka[2][KCH];
 #pragma unroll
@@ -414,7 +410,7 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint8_t* src = my_ring + stg[i] * T::kStage + T::kBytes + (j >> 1) * 8 * D + voff[j & 1];
+        const uint8_t* src = stage + i * T::kPair + T::kBytes + (j >> 1) * 8 * D + voff[j & 1];
         if constexpr (RL == 16) {
           const uint4 v = *reinterpret_cast<const uint4*>(src);
           va[i][j][0] = v.x;
@@ -535,10 +531,14 @@ __global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
         Mma<__half>::run(oacc[mt], a, pb[i][0], pb[i][1]);
       }
     }
-    // every lane has its codes in registers: the stages take the next tiles
+    // every lane has its codes in registers: the stage takes the next tiles
+    cst = cst + 1 == NST ? 0 : cst + 1;
+    if (cst == 0) cph ^= 1;
     __syncwarp();
-#pragma unroll 1
-    for (int i = 0; i < NQ && k_issued < k_end; ++i, ++k_issued) issue(k_issued);
+    if (k_issued < k_end) {
+      issue(k_issued);
+      k_issued += NQ;
+    }
   }
   st_d[0] = sum_over_groups(st_d[0]);
   st_d[1] = sum_over_groups(st_d[1]);
