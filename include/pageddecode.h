@@ -277,8 +277,9 @@ pd_status pd_batch_decode_paged_kv_mq(const void* Q, const void* pages,
  *   scales [max_pages, 2, H_kv, P / scale_rows] float32: row `slot` of a page's K (0) or
  *          V (1) block of a head stands for code * scales[page, K | V, head, slot / scale_rows].
  * scale_rows divides P; with scale_rows = P a page's head has one scale for K, one for V.
- * Scales are finite and >= 0; a NaN or infinite one makes the outputs that attend its block
- * non-finite, and nothing else.  The cache holds K as the decode uses it: rotate (and norm)
+ * Codes of attended rows are numbers (no E4M3 NaN code; the append writes none).  Scales are
+ * finite and >= 0; a NaN or infinite one makes the outputs that attend its block non-finite, and
+ * nothing else.  The cache holds K as the decode uses it: rotate (and norm)
  * the new K rows before the append, and Q before the decode, with pd_qk_norm_rope.
  *
  * pd_append_paged_kv_bs — quantises new tokens' K/V into such a cache.
@@ -289,7 +290,8 @@ pd_status pd_batch_decode_paged_kv_mq(const void* Q, const void* pages,
  * apart) and M = 448 (E4M3) or 127 (I8):
  *   need  = the smallest power of two 2^k, k >= -126, with amax <= M 2^k;
  *   scale = need if the block's first row is among the new ones, else max(scale, need), the
- *           block's earlier codes c becoming RN(c * old_scale / scale);
+ *           block's earlier codes c becoming RN(c * (old_scale / scale)), quotient and product in
+ *           fp32;
  *   code  = RN(x / scale), ties to even.
  * A power of two makes both quotients exact.  A non-finite new value makes its block's scale
  * NaN and its new codes 0, until the block is filled again from its first row.  Rows behind the

@@ -205,6 +205,8 @@ def _ptr(t: Optional[torch.Tensor]):
 def _stream(stream) -> int:
     """cudaStream_t of `stream` (a torch stream or a raw handle); None: the current stream."""
     if stream is None:
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 

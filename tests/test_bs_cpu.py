@@ -114,6 +114,15 @@ def test_qk_refusals(L, kw, status):
 
 
 def test_layouts():
+    import struct
+    assert struct.calcsize("@10i2qi2fi5Q") == ctypes.sizeof(_lib.DecodeDesc)
+    assert struct.calcsize("@8i3f8q") == ctypes.sizeof(_lib.QkDesc)
+    v = _lib._PACK_DECODE(*range(1, 11), 11, 12, 13, 14.0, 15.0, 16, 17, 18, 19, 20, 21)
+    d = _lib.DecodeDesc.from_buffer_copy(v)
+    assert [getattr(d, n) for n, _ in d._fields_] == list(range(1, 22))
+    v = _lib._PACK_QK(*range(1, 9), 9.0, 10.0, 11.0, *range(12, 20))
+    d = _lib.QkDesc.from_buffer_copy(v)
+    assert [getattr(d, n) for n, _ in d._fields_] == list(range(1, 20))
     assert ctypes.sizeof(_lib.QkDesc) == 112
     assert _lib.QkDesc.q_stride.offset == 48 and _lib.QkDesc.k_out_head_stride.offset == 104
 

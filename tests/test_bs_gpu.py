@@ -171,6 +171,46 @@ def test_decode_learned_sink_and_host_plan():
     _check(c, "mma", sink=sink, num_splits=1)
 
 
+@pytest.mark.parametrize("P", [16, 8])
+def test_decode_more_sequences_than_the_scan_caches(P):
+    g = torch.Generator().manual_seed(22)
+    lengths = torch.randint(0, 60, (1300,), generator=g).tolist()
+    _check(_case(lengths, 2, 1, 64, P, P, "int8", "f16", seed=23))
+
+
+@pytest.mark.parametrize("lengths,splits", [([40, 1000, 7], 0), ([40, 1000, 7], 1), ([5000], 0)])
+def test_decode_into_unaligned_outputs(lengths, splits):
+    c = _case(lengths, 8, 2, 128, 16, 16, "e4m3", "bf16", seed=24)
+    ref = _ref(c)
+    for dt in (torch.bfloat16, torch.float32):
+        buf = torch.zeros(len(lengths) * 8 * 128 + 9, dtype=dt, device=DEV)
+        out = buf[3:3 + len(lengths) * 8 * 128].view(len(lengths), 8, 128)
+        lse = torch.empty(len(lengths), 8, device=DEV)
+        pd.batch_decode_paged_kv_bs(c["Q"][:, 0].contiguous(), c["codes"].view(KV["e4m3"]), c["scales"], c["indptr"],
+                                    c["vals"], c["li"], out, lse, num_splits=splits)
+        assert pd.check_device_errors() == "PD_OK"
+        check_decode(out, lse, ref, max(lengths))
+        assert (buf[:3] == 0).all() and (buf[-6:] == 0).all()
+
+
+def test_decode_two_streams_at_once():
+    """Split decodes in flight together, each with its stream's own workspace."""
+    cs = [_case([3000, 900, 40], 8, 2, 128, 16, 16, "int8", "bf16", seed=25 + i) for i in range(2)]
+    refs = [_ref(c) for c in cs]
+    st = [torch.cuda.Stream() for _ in cs]
+    Q = [c["Q"][:, 0].contiguous() for c in cs]
+    outs = [torch.empty_like(q) for q in Q]
+    lses = [torch.empty(q.shape[:-1], device=DEV) for q in Q]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s, q, o, l in zip(cs, st, Q, outs, lses):
+            pd.batch_decode_paged_kv_bs(q, c["codes"], c["scales"], c["indptr"], c["vals"], c["li"], o, l, stream=s)
+    torch.cuda.synchronize()
+    assert pd.check_device_errors() == "PD_OK"
+    for o, l, r in zip(outs, lses, refs):
+        check_decode(o, l, r, 3000)
+
+
 def test_decode_is_the_same_every_time():
     c = _case([5000, 3, 900], 16, 2, 128, 16, 16, "int8", "bf16", seed=16)
     a = _run(c)
