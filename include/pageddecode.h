@@ -296,23 +296,33 @@ pd_status pd_batch_decode_paged_kv_mq(const void* Q, const void* pages,
  * A power of two makes both quotients exact.  A non-finite new value makes its block's scale
  * NaN and its new codes 0, until the block is filled again from its first row.  Rows behind the
  * sequence's last one, and blocks that receive nothing, are left as they were.
- * Arguments (device pointers): k_new, v_new [T, H_kv, D] of in_dtype (F32, F16, BF16), token t
- * at element t * k_stride (v_stride), heads contiguous (slices of a fused projection's output
- * need no copy); append_indptr [B+1] int32, append_indptr[0] = 0, append_indptr[B] = T;
+ * Arguments (device pointers): k_new, v_new [T, H_kv, D] of in_dtype, token t at element
+ * t * k_stride (v_stride), heads contiguous (slices of a fused projection's output need no
+ * copy); append_indptr [B+1] int32, append_indptr[0] = 0, append_indptr[B] = T;
  * page_table_indptr, page_table_values, length_info as for the decode (of a sliding-window
- * length_info [3,B] only the first row is read).  D is 64, 128 or 256; pages 16-byte aligned.
+ * length_info [3,B] only the first row is read); pages 16-byte aligned.
  * A sequence whose table does not hold its new rows is skipped (PD_ERR_BAD_LENGTH on the
  * device), as is a block whose page id is out of range (PD_ERR_BAD_PAGE).  Pages that receive
- * rows must belong to one sequence (a shared prefix is full and receives none).  k_stride,
- * v_stride >= H_kv * D.  The decode may follow with PD_DECODE_EARLY_INPUTS.
+ * rows must belong to one sequence (a shared prefix is full and receives none).  The decode may
+ * follow with PD_DECODE_EARLY_INPUTS.
  */
+typedef struct {
+  int32_t T, B;               /* new tokens, sequences */
+  int32_t H_kv;
+  int32_t D;                  /* head dim: 64, 128 or 256 */
+  int32_t page_size;          /* 1 to 256 */
+  int32_t scale_rows;         /* rows per scale: divides page_size */
+  int32_t in_dtype;           /* pd_dtype of k_new, v_new: F32, F16 or BF16 */
+  int32_t kv_dtype;           /* E4M3 or I8 */
+  int64_t max_pages;          /* as in pd_decode_desc */
+  int64_t nnz_pages;
+  int64_t k_stride, v_stride; /* elements from token to token, at least H_kv * D */
+  int32_t flags, reserved;    /* 0 */
+} pd_append_bs_desc;
 pd_status pd_append_paged_kv_bs(void* pages, float* scales, const void* k_new, const void* v_new,
                                 const int32_t* append_indptr, const int32_t* page_table_indptr,
                                 const int32_t* page_table_values, const int32_t* length_info,
-                                int32_t T, int32_t B, int32_t H_kv, int32_t D, int32_t page_size,
-                                int32_t scale_rows, int64_t max_pages, int64_t nnz_pages,
-                                int64_t k_stride, int64_t v_stride, int32_t in_dtype,
-                                int32_t kv_dtype, pd_stream_t stream);
+                                const pd_append_bs_desc* desc, pd_stream_t stream);
 
 /*
  * pd_batch_decode_paged_kv_bs — pd_batch_decode_paged_kv (q_len = 1) and

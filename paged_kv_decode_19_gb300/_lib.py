@@ -126,6 +126,25 @@ class QkDesc(ctypes.Structure):
     ]
 
 
+class AppendBsDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int32),
+        ("B", ctypes.c_int32),
+        ("H_kv", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("scale_rows", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("max_pages", ctypes.c_int64),
+        ("nnz_pages", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 def lib():
     """Load libpageddecode.so (raises if it has not been built)."""
     global _lib
@@ -159,7 +178,7 @@ def lib():
             L.pd_append_paged_kv_rope.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i64, i32,
                                                   i32, f32, f32, i32, f32, f32, P]
             L.pd_append_paged_kv_rope.restype = i32
-            L.pd_append_paged_kv_bs.argtypes = [P] * 8 + [i32] * 6 + [i64] * 4 + [i32, i32, P]
+            L.pd_append_paged_kv_bs.argtypes = [P] * 10
             L.pd_append_paged_kv_bs.restype = i32
             L.pd_batch_decode_paged_kv_bs.argtypes = [P] * 8 + [i32, i32, f32, P, P]
             L.pd_batch_decode_paged_kv_bs.restype = i32
@@ -239,10 +258,15 @@ def make_desc(Q, pages, indptr, values, length_info, out, *, num_splits=0, max_k
 
 
 def _host_i32(a, n):
-    ai = getattr(a, "__array_interface__", None)  # (built once per access)
-    if ai is None or ai["typestr"] != "<i4" or ai["strides"] is not None or a.size != n:
-        raise ValueError(f"host copies must be contiguous numpy int32 arrays of {n} entries")
-    return ai["data"][0]
+    try:
+        if a.size != n or a.dtype.char != "i":
+            raise ValueError
+        return ctypes.addressof(ctypes.c_char.from_buffer(a))  # (a writable C-contiguous buffer)
+    except (AttributeError, TypeError, ValueError):
+        ai = getattr(a, "__array_interface__", None)
+        if ai is None or ai["typestr"] != "<i4" or ai["strides"] is not None or a.size != n:
+            raise ValueError(f"host copies must be contiguous numpy int32 arrays of {n} entries") from None
+        return ai["data"][0]
 
 
 def host_meta_of(indptr, length_info):
@@ -331,49 +355,43 @@ def batch_decode_paged_kv_mq(Q, pages, page_table_indptr, page_table_values, len
     return output, lse
 
 
-def _addr(t, dev, contiguous=True):
-    """Device address of a tensor on device `dev` (the current one, where the kernel runs)."""
-    if t.get_device() != dev:
-        raise ValueError(f"tensors must be on the current device, cuda:{dev}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
-    return t.data_ptr()
+def _refuse(dev, *tensors):
+    """The error of a call whose tensors are not all on device `dev`, or not contiguous."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on the same GPU")
+    raise ValueError("tensors must be contiguous")
 
 
-def _device():
-    """The current device's index, without setting CUDA up where there is none."""
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
+def _device(t):
+    """The index of the tensor's device, which must be the current one: the kernels run there."""
+    dev = t.get_device()  # (-1: not on a GPU)
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("tensors must be on the current GPU")
+    return dev
 
 
-def _bs_shape(pages, scales):
-    """(max_pages, H_kv, P, D, blocks per page) of a block-scaled cache, checked."""
-    shape, sshape = pages.shape, scales.shape
-    if len(shape) != 5 or shape[1] != 2 or pages.dtype not in BS_DTYPE_CODES:
+def _bs_refuse(pages, scales, page_table_indptr, page_table_values, length_info, B):
+    """What is wrong with a block-scaled cache or its table."""
+    if pages.dim() != 5 or pages.shape[1] != 2 or pages.dtype not in BS_DTYPE_CODES:
         raise ValueError("pages must be [max_pages, 2, H_kv, P, D] of float8_e4m3fn or int8")
-    if scales.dtype != torch.float32 or len(sshape) != 4 or sshape[:3] != shape[:3]:
+    if scales.dtype != torch.float32 or scales.dim() != 4 or scales.shape[:3] != pages.shape[:3]:
         raise ValueError("scales must be float32 [max_pages, 2, H_kv, P / scale_rows]")
-    max_pages, _, H_kv, P, D = shape
-    n_sb = sshape[3]
-    if n_sb < 1 or P % n_sb:
+    if scales.shape[3] < 1 or pages.shape[3] % scales.shape[3]:
         raise ValueError("the blocks of a page must divide it")
-    return max_pages, H_kv, P, D, n_sb
+    for t in (page_table_indptr, page_table_values, length_info):
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError("the page table and length_info must be int32")
+    raise ValueError(f"page_table_indptr [{B} + 1] and length_info [{B}] or [3, {B}]")
 
 
-def _bs_table(page_table_indptr, page_table_values, length_info, B):
-    i32 = torch.int32
-    if (page_table_indptr.dtype != i32 or length_info.dtype != i32
-            or (page_table_values is not None and page_table_values.dtype != i32)):
-        raise ValueError("the page table and length_info must be int32")
-    n = length_info.numel()
-    if page_table_indptr.numel() != B + 1 or (n != B and n != 3 * B):
-        raise ValueError("page_table_indptr [B+1] and length_info [B] or [3,B]")
-    return n
-
-
-# The descs of the calls below, packed: a ctypes.Structure of twenty fields costs more to fill
-# than the call it is passed to.
+# The calls below are made once per layer and step, mostly on small batches: their checks stand in
+# one expression each, and the descs are packed rather than filled field by field (a
+# ctypes.Structure of twenty fields costs more to fill than the call it is passed to).
 _PACK_DECODE = struct.Struct("@10i2qi2fi5Q").pack
+_PACK_APPEND = struct.Struct("@8i4q2i").pack
 _PACK_QK = struct.Struct("@8i3f8q").pack
+_I32, _F32 = torch.int32, torch.float32
 
 
 def batch_decode_paged_kv_bs(Q, pages, scales, page_table_indptr, page_table_values, length_info,
@@ -384,35 +402,57 @@ def batch_decode_paged_kv_bs(Q, pages, scales, page_table_indptr, page_table_val
     [B, q_len, H_qo, D] for several query tokens per sequence (causal among them); output
     like Q, lse [B, H_qo] or [B, q_len, H_qo].  K is used as stored and Q as given: rotate
     both with qk_norm_rope."""
-    max_pages, H_kv, P, D, n_sb = _bs_shape(pages, scales)
-    shape = Q.shape
-    if len(shape) == 3:
-        (B, H_qo, D_q), q_len = shape, 1
-    elif len(shape) == 4:
-        B, q_len, H_qo, D_q = shape
+    shape, pshape, sshape, kv = Q.shape, pages.shape, scales.shape, BS_DTYPE_CODES.get(pages.dtype)
+    rank = len(shape)
+    if rank == 3:
+        (B, H_qo, D), q_len = shape, 1
+    elif rank == 4:
+        B, q_len, H_qo, D = shape
     else:
-        D_q = -1
-    if D_q != D:
         raise ValueError("Q must be [B, H_qo, D] or [B, q_len, H_qo, D]")
-    if output.shape != shape or lse.shape != shape[:-1] or lse.dtype != torch.float32:
+    vals, n_li = page_table_values, length_info.numel()
+    if (kv is None or len(pshape) != 5 or len(sshape) != 4 or pshape[1] != 2 or sshape[1] != 2
+            or sshape[0] != pshape[0] or sshape[2] != pshape[2] or scales.dtype != _F32
+            or sshape[3] < 1 or pshape[3] % sshape[3] or page_table_indptr.dtype != _I32
+            or length_info.dtype != _I32 or page_table_indptr.numel() != B + 1
+            or (n_li != B and n_li != 3 * B) or (vals is not None and vals.dtype != _I32)):
+        _bs_refuse(pages, scales, page_table_indptr, vals, length_info, B)
+    max_pages, _, H_kv, P, D_kv = pshape
+    if D_kv != D:
+        raise ValueError("Q must be [B, H_qo, D] or [B, q_len, H_qo, D]")
+    if output.shape != shape or lse.shape != shape[:-1] or lse.dtype != _F32:
         raise ValueError("output must be shaped like Q and lse float32 like its heads")
-    n_li = _bs_table(page_table_indptr, page_table_values, length_info, B)
-    dev = _device()
-    vals = page_table_values
-    desc = _PACK_DECODE(
-        B, H_qo, H_kv, D, P, DTYPE_CODES[Q.dtype], BS_DTYPE_CODES[pages.dtype],
-        DTYPE_CODES[output.dtype], length_info.dim() == 2, num_splits, max_pages,
-        0 if vals is None else vals.numel(), 0, 1.0, 1.0, DECODE_EARLY_INPUTS if early_inputs else 0,
-        0 if workspace is None else _addr(workspace, dev),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        0 if sink is None else _sink_ptr(sink, H_qo) and _addr(sink, dev),
-        0 if host_meta is None else _host_i32(host_meta[0], B + 1),
-        0 if host_meta is None else _host_i32(host_meta[1], n_li))
+    dev = _device(Q)
+    if not (pages.get_device() == scales.get_device()
+            == page_table_indptr.get_device() == length_info.get_device() == output.get_device()
+            == lse.get_device() == dev and Q.is_contiguous() and pages.is_contiguous()
+            and scales.is_contiguous() and page_table_indptr.is_contiguous()
+            and length_info.is_contiguous() and output.is_contiguous() and lse.is_contiguous()):
+        _refuse(dev, Q, pages, scales, page_table_indptr, length_info, output, lse)
+    vals_at = n_vals = ws_at = ws_bytes = sink_at = host_ip = host_li = 0
+    if vals is not None:
+        if vals.get_device() != dev or not vals.is_contiguous():
+            _refuse(dev, vals)
+        vals_at, n_vals = vals.data_ptr(), vals.numel()
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _refuse(dev, workspace)
+        ws_at, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if sink is not None:
+        sink_at = _sink_ptr(sink, H_qo)
+        if sink.get_device() != dev:
+            _refuse(dev, sink)
+    if host_meta is not None:
+        host_ip, host_li = _host_i32(host_meta[0], B + 1), _host_i32(host_meta[1], n_li)
+    desc = _PACK_DECODE(B, H_qo, H_kv, D, P, DTYPE_CODES[Q.dtype], kv, DTYPE_CODES[output.dtype],
+                        length_info.dim() == 2, num_splits, max_pages, n_vals, 0, 1.0, 1.0,
+                        DECODE_EARLY_INPUTS if early_inputs else 0, ws_at, ws_bytes, sink_at,
+                        host_ip, host_li)
     st = (_lib or lib()).pd_batch_decode_paged_kv_bs(
-        _addr(Q, dev), _addr(pages, dev), _addr(scales, dev), _addr(page_table_indptr, dev),
-        None if vals is None else _addr(vals, dev), _addr(length_info, dev), _addr(output, dev),
-        _addr(lse, dev), q_len, P // n_sb, D ** -0.5 if sm_scale is None else sm_scale, desc,
-        _stream(stream))
+        Q.data_ptr(), pages.data_ptr(), scales.data_ptr(), page_table_indptr.data_ptr(),
+        vals_at or None, length_info.data_ptr(), output.data_ptr(), lse.data_ptr(), q_len,
+        P // sshape[3], D ** -0.5 if sm_scale is None else sm_scale, desc,
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return output, lse
@@ -429,7 +469,17 @@ def append_paged_kv_bs(pages, scales, k_new, v_new, append_indptr, page_table_in
     tokens append_indptr[b] .. append_indptr[b+1] - 1, its last rows in the page table and
     length_info as they stand after the append.  k_new and v_new may be slices of a larger
     tensor along the heads (any token stride)."""
-    max_pages, H_kv, P, D, n_sb = _bs_shape(pages, scales)
+    pshape, sshape, kv = pages.shape, scales.shape, BS_DTYPE_CODES.get(pages.dtype)
+    B, n_li, vals = append_indptr.numel() - 1, length_info.numel(), page_table_values
+    if B < 0 or append_indptr.dtype != _I32:
+        raise ValueError("append_indptr must be int32 [B+1]")
+    if (kv is None or len(pshape) != 5 or len(sshape) != 4 or pshape[1] != 2 or sshape[1] != 2
+            or sshape[0] != pshape[0] or sshape[2] != pshape[2] or scales.dtype != _F32
+            or sshape[3] < 1 or pshape[3] % sshape[3] or page_table_indptr.dtype != _I32
+            or length_info.dtype != _I32 or page_table_indptr.numel() != B + 1
+            or (n_li != B and n_li != 3 * B) or vals.dtype != _I32):
+        _bs_refuse(pages, scales, page_table_indptr, vals, length_info, B)
+    max_pages, _, H_kv, P, D = pshape
     shape, dtype = k_new.shape, k_new.dtype
     if len(shape) != 3 or shape[1] != H_kv or shape[2] != D or v_new.shape != shape or v_new.dtype != dtype:
         raise ValueError("k_new and v_new must be [T, H_kv, D] of one dtype")
@@ -437,18 +487,22 @@ def append_paged_kv_bs(pages, scales, k_new, v_new, append_indptr, page_table_in
     (ks, kh, kd), (vs, vh, vd) = k_new.stride(), v_new.stride()
     if T and (kd != 1 or vd != 1 or (H_kv > 1 and (kh != D or vh != D))):
         raise ValueError("the heads of k_new and v_new must be contiguous")
-    B = append_indptr.numel() - 1
-    if append_indptr.dtype != torch.int32 or B < 0:
-        raise ValueError("append_indptr must be int32 [B+1]")
-    _bs_table(page_table_indptr, page_table_values, length_info, B)
     if T < 2:
         ks = vs = H_kv * D
-    dev = _device()
+    dev = _device(pages)
+    if not (scales.get_device() == k_new.get_device() == v_new.get_device()
+            == append_indptr.get_device() == page_table_indptr.get_device() == vals.get_device()
+            == length_info.get_device() == dev and pages.is_contiguous() and scales.is_contiguous()
+            and append_indptr.is_contiguous() and page_table_indptr.is_contiguous()
+            and vals.is_contiguous() and length_info.is_contiguous()):
+        _refuse(dev, pages, scales, k_new, v_new, append_indptr, page_table_indptr, vals, length_info)
+    desc = _PACK_APPEND(T, B, H_kv, D, P, P // sshape[3], DTYPE_CODES[dtype], kv, max_pages,
+                        vals.numel(), ks, vs, 0, 0)
     st = (_lib or lib()).pd_append_paged_kv_bs(
-        _addr(pages, dev), _addr(scales, dev), _addr(k_new, dev, False), _addr(v_new, dev, False),
-        _addr(append_indptr, dev), _addr(page_table_indptr, dev), _addr(page_table_values, dev),
-        _addr(length_info, dev), T, B, H_kv, D, P, P // n_sb, max_pages, page_table_values.numel(),
-        ks, vs, DTYPE_CODES[dtype], BS_DTYPE_CODES[pages.dtype], _stream(stream))
+        pages.data_ptr(), scales.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+        append_indptr.data_ptr(), page_table_indptr.data_ptr(), vals.data_ptr(),
+        length_info.data_ptr(), desc,
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return pages, scales
@@ -470,7 +524,7 @@ def rope_frequencies(rotary_dim, rope_theta=1e4, scaling=None, factor=1.0, origi
     return torch.tensor(list(out), dtype=torch.float64, device=device)
 
 
-def _heads(t, T, H, D, dtype, what, written=False):
+def _heads(t, T, H, D, dtype, dev, what, written=False):
     """(token stride, head stride) of rows [T, H, D], checked."""
     if t.shape != (T, H, D) or t.dtype != dtype:
         raise ValueError(f"{what} must be [T, heads, D] like the other rows")
@@ -479,6 +533,8 @@ def _heads(t, T, H, D, dtype, what, written=False):
         raise ValueError(f"the last dim of {what} must be contiguous")
     if written and ((a == 0 and T > 1) or (b == 0 and H > 1)):
         raise ValueError(f"{what} must not be an expanded tensor")
+    if t.get_device() != dev:
+        _refuse(dev, t)
     return a, b
 
 
@@ -490,43 +546,48 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out=None, k_ou
     k may be None.  q and k may be slices along the heads of a projection's output; q_out and
     k_out default to new tensors and may be q and k.  Returns (q_out, k_out)."""
     T, H_q, D = q.shape
-    dtype = q.dtype
+    dtype, dev = q.dtype, _device(q)
     if q_out is None:
         q_out = torch.empty((T, H_q, D), dtype=dtype, device=q.device)
-    qs, qh = _heads(q, T, H_q, D, dtype, "q")
-    qos, qoh = _heads(q_out, T, H_q, D, dtype, "q_out", True)
-    dev = _device()
+    qs, qh = _heads(q, T, H_q, D, dtype, dev, "q")
+    qos, qoh = _heads(q_out, T, H_q, D, dtype, dev, "q_out", True)
     H_k = ks = kh = kos = koh = 0
-    k_at = ko_at = None
+    k_at = ko_at = qw_at = kw_at = pos_at = freq_at = None
     if k is not None:
         H_k = k.shape[1]
         if k_out is None:
             k_out = torch.empty((T, H_k, D), dtype=dtype, device=k.device)
-        ks, kh = _heads(k, T, H_k, D, dtype, "k")
-        kos, koh = _heads(k_out, T, H_k, D, dtype, "k_out", True)
-        k_at, ko_at = _addr(k, dev, False), _addr(k_out, dev, False)
-    w = q_weight if q_weight is not None else k_weight
-    qw_at = kw_at = None
-    if w is not None:
-        if w.shape != (D,) or (k_weight is not None and (k_weight.shape != (D,) or k_weight.dtype != w.dtype)):
+        ks, kh = _heads(k, T, H_k, D, dtype, dev, "k")
+        kos, koh = _heads(k_out, T, H_k, D, dtype, dev, "k_out", True)
+        k_at, ko_at = k.data_ptr(), k_out.data_ptr()
+    wdt = 0
+    for w in (q_weight, k_weight):
+        if w is not None and (w.shape != (D,) or w.get_device() != dev or not w.is_contiguous()):
+            if w.shape != (D,):
+                raise ValueError("the weights must be [D], of one dtype")
+            _refuse(dev, w)
+    if q_weight is not None:
+        qw_at, wdt = q_weight.data_ptr(), DTYPE_CODES[q_weight.dtype]
+    if k_weight is not None:
+        if q_weight is not None and k_weight.dtype != q_weight.dtype:
             raise ValueError("the weights must be [D], of one dtype")
-        qw_at = None if q_weight is None else _addr(q_weight, dev)
-        kw_at = None if k_weight is None else _addr(k_weight, dev)
+        kw_at, wdt = k_weight.data_ptr(), DTYPE_CODES[k_weight.dtype]
     rd = 0
-    pos_at = freq_at = None
     if inv_freq is not None and rotary_mode:
         if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be float64 [rotary_dim / 2]")
-        if positions.dtype != torch.int32 or positions.shape != (T,):
+        if positions.dtype != _I32 or positions.shape != (T,):
             raise ValueError("positions must be int32 [T]")
+        if not (positions.get_device() == inv_freq.get_device() == dev
+                and positions.is_contiguous() and inv_freq.is_contiguous()):
+            _refuse(dev, positions, inv_freq)
         rd = 2 * inv_freq.numel()
-        pos_at, freq_at = _addr(positions, dev), _addr(inv_freq, dev)
-    desc = _PACK_QK(T, H_q, H_k, D, DTYPE_CODES[dtype], 0 if w is None else DTYPE_CODES[w.dtype],
-                    rotary_mode, rd, eps, weight_offset, attention_factor, qs, ks, qh, kh, qos, kos,
-                    qoh, koh)
+        pos_at, freq_at = positions.data_ptr(), inv_freq.data_ptr()
+    desc = _PACK_QK(T, H_q, H_k, D, DTYPE_CODES[dtype], wdt, rotary_mode, rd, eps, weight_offset,
+                    attention_factor, qs, ks, qh, kh, qos, kos, qoh, koh)
     st = (_lib or lib()).pd_qk_norm_rope(
-        _addr(q, dev, False), k_at, qw_at, kw_at, pos_at, freq_at, _addr(q_out, dev, False), ko_at,
-        desc, _stream(stream))
+        q.data_ptr(), k_at, qw_at, kw_at, pos_at, freq_at, q_out.data_ptr(), ko_at, desc,
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return q_out, k_out

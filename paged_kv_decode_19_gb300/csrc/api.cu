@@ -857,31 +857,34 @@ pd_status pd_append_paged_kv_rope(void* pages, const void* k_new, const void* v_
 pd_status pd_append_paged_kv_bs(void* pages, float* scales, const void* k_new, const void* v_new,
                                 const int32_t* append_indptr, const int32_t* page_table_indptr,
                                 const int32_t* page_table_values, const int32_t* length_info,
-                                int32_t T, int32_t B, int32_t H_kv, int32_t D, int32_t page_size,
-                                int32_t scale_rows, int64_t max_pages, int64_t nnz_pages,
-                                int64_t k_stride, int64_t v_stride, int32_t in_dtype,
-                                int32_t kv_dtype, pd_stream_t stream) {
-  if (T < 0 || B < 0 || H_kv <= 0 || max_pages <= 0 || nnz_pages < 0)
+                                const pd_append_bs_desc* desc, pd_stream_t stream) {
+  if (!desc) return fail(PD_ERR_INVALID_ARG, "desc is NULL");
+  const pd_append_bs_desc& d = *desc;
+  if (d.T < 0 || d.B < 0 || d.H_kv <= 0 || d.max_pages <= 0 || d.nnz_pages < 0)
     return fail(PD_ERR_INVALID_ARG, "bad T/B/H_kv/max_pages/nnz_pages");
-  if (D != 64 && D != 128 && D != 256) return fail(PD_ERR_UNSUPPORTED, "head dim must be 64, 128 or 256");
-  if (page_size <= 0 || page_size > 256) return fail(PD_ERR_INVALID_ARG, "page_size must be in [1, 256]");
-  if (scale_rows <= 0 || page_size % scale_rows != 0)
+  if (d.D != 64 && d.D != 128 && d.D != 256) return fail(PD_ERR_UNSUPPORTED, "head dim must be 64, 128 or 256");
+  if (d.page_size <= 0 || d.page_size > 256) return fail(PD_ERR_INVALID_ARG, "page_size must be in [1, 256]");
+  if (d.scale_rows <= 0 || d.page_size % d.scale_rows != 0)
     return fail(PD_ERR_INVALID_ARG, "scale_rows must divide page_size");
-  if (in_dtype != kF32 && in_dtype != kF16 && in_dtype != kBF16)
+  if (d.in_dtype != kF32 && d.in_dtype != kF16 && d.in_dtype != kBF16)
     return fail(PD_ERR_INVALID_ARG, "in_dtype must be F32, F16 or BF16");
-  if (kv_dtype != kE4M3 && kv_dtype != kI8) return fail(PD_ERR_INVALID_ARG, "a block-scaled cache is E4M3 or I8");
-  const long long row = (long long)H_kv * D;
-  if (T > 1 && (k_stride < row || v_stride < row))
+  if (d.kv_dtype != kE4M3 && d.kv_dtype != kI8) return fail(PD_ERR_INVALID_ARG, "a block-scaled cache is E4M3 or I8");
+  if (d.flags || d.reserved) return fail(PD_ERR_INVALID_ARG, "flags and reserved must be 0");
+  const long long row = (long long)d.H_kv * d.D;
+  if (d.T > 1 && (d.k_stride < row || d.v_stride < row))
     return fail(PD_ERR_INVALID_ARG, "k_stride and v_stride must be at least H_kv * D");
-  if (max_pages * 2 * H_kv > INT_MAX) return fail(PD_ERR_UNSUPPORTED, "max_pages * 2 * H_kv exceeds 2^31");
-  if ((long long)T / scale_rows + 2ll * B > INT_MAX || H_kv > 200000)
+  if (d.max_pages > INT_MAX || d.max_pages * 2 * d.H_kv > INT_MAX)
+    return fail(PD_ERR_UNSUPPORTED, "max_pages * 2 * H_kv exceeds 2^31");
+  if ((long long)d.T / d.scale_rows + 2ll * d.B > INT_MAX || d.H_kv > 200000)
     return fail(PD_ERR_UNSUPPORTED, "T, B or H_kv too large");
-  if (T == 0 || B == 0) return PD_OK;
+  if (d.T == 0 || d.B == 0) return PD_OK;
   if (!pages || !scales || !k_new || !v_new || !append_indptr || !page_table_indptr || !page_table_values ||
       !length_info)
     return fail(PD_ERR_INVALID_ARG, "NULL device pointer");
-  if ((reinterpret_cast<uintptr_t>(pages) % 16) != 0 || (reinterpret_cast<uintptr_t>(scales) % 4) != 0)
-    return fail(PD_ERR_INVALID_ARG, "pages must be 16-byte and scales 4-byte aligned");
+  const int eb = elem_bytes(d.in_dtype);
+  if ((reinterpret_cast<uintptr_t>(pages) % 16) != 0 || (reinterpret_cast<uintptr_t>(scales) % 4) != 0 ||
+      (reinterpret_cast<uintptr_t>(k_new) % eb) != 0 || (reinterpret_cast<uintptr_t>(v_new) % eb) != 0)
+    return fail(PD_ERR_INVALID_ARG, "pages must be 16-byte, scales 4-byte, k_new and v_new element aligned");
   DeviceState* ds = nullptr;
   pd_status st = device_state(&ds);
   if (st != PD_OK) return st;
@@ -895,16 +898,16 @@ pd_status pd_append_paged_kv_bs(void* pages, float* scales, const void* k_new, c
   a.values = page_table_values;
   a.length_info = length_info;
   a.err = ds->err;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.max_pages = max_pages;
-  a.nnz = nnz_pages;
-  a.T = T;
-  a.B = B;
-  a.H_kv = H_kv;
-  a.P = page_size;
-  a.S = scale_rows;
-  const cudaError_t e = launch_append_bs(a, D, in_dtype, kv_dtype, (cudaStream_t)stream);
+  a.k_stride = d.k_stride;
+  a.v_stride = d.v_stride;
+  a.max_pages = d.max_pages;
+  a.nnz = d.nnz_pages;
+  a.T = d.T;
+  a.B = d.B;
+  a.H_kv = d.H_kv;
+  a.P = d.page_size;
+  a.S = d.scale_rows;
+  const cudaError_t e = launch_append_bs(a, d.D, d.in_dtype, d.kv_dtype, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "append launch");
   return PD_OK;
 }

@@ -3,6 +3,7 @@ validation, the binding's own refusals, and the frequency tables against their f
 import ctypes
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -66,24 +67,27 @@ def test_decode_of_nothing_and_codes_elsewhere(L):
 
 
 def _append(L, **kw):
-    a = dict(pages=8192, scales=64, k=4096, v=4096, at=64, ip=64, vals=64, li=64, T=5, B=2, H=2, D=128, P=32, S=16,
-             max_pages=10, nnz=4, ks=256, vs=256, dt=2, kv=4)
+    a = dict(pages=8192, scales=64, k=4096, v=4096, at=64, ip=64, vals=64, li=64, T=5, B=2, H_kv=2, D=128,
+             page_size=32, scale_rows=16, max_pages=10, nnz_pages=4, k_stride=256, v_stride=256, in_dtype=2, kv_dtype=4,
+             flags=0, reserved=0)
     a.update(kw)
-    return _name(L.pd_append_paged_kv_bs(*(a[n] for n in ("pages", "scales", "k", "v", "at", "ip", "vals", "li", "T",
-                                                          "B", "H", "D", "P", "S", "max_pages", "nnz", "ks", "vs",
-                                                          "dt", "kv")), None))
+    d = _lib.AppendBsDesc(**{n: a[n] for n, _ in _lib.AppendBsDesc._fields_})
+    return _name(L.pd_append_paged_kv_bs(*(a[n] for n in ("pages", "scales", "k", "v", "at", "ip", "vals", "li")),
+                                         ctypes.byref(d), None))
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(T=-1), "PD_ERR_INVALID_ARG"), (dict(B=-1), "PD_ERR_INVALID_ARG"), (dict(H=0), "PD_ERR_INVALID_ARG"),
-    (dict(D=96), "PD_ERR_UNSUPPORTED"), (dict(P=0), "PD_ERR_INVALID_ARG"), (dict(P=512), "PD_ERR_INVALID_ARG"),
-    (dict(S=0), "PD_ERR_INVALID_ARG"), (dict(S=12), "PD_ERR_INVALID_ARG"), (dict(dt=3), "PD_ERR_INVALID_ARG"),
-    (dict(kv=2), "PD_ERR_INVALID_ARG"), (dict(ks=255), "PD_ERR_INVALID_ARG"), (dict(vs=0), "PD_ERR_INVALID_ARG"),
+    (dict(T=-1), "PD_ERR_INVALID_ARG"), (dict(B=-1), "PD_ERR_INVALID_ARG"), (dict(H_kv=0), "PD_ERR_INVALID_ARG"),
+    (dict(D=96), "PD_ERR_UNSUPPORTED"), (dict(page_size=0), "PD_ERR_INVALID_ARG"), (dict(page_size=512), "PD_ERR_INVALID_ARG"),
+    (dict(scale_rows=0), "PD_ERR_INVALID_ARG"), (dict(scale_rows=12), "PD_ERR_INVALID_ARG"), (dict(in_dtype=3), "PD_ERR_INVALID_ARG"),
+    (dict(kv_dtype=2), "PD_ERR_INVALID_ARG"), (dict(k_stride=255), "PD_ERR_INVALID_ARG"), (dict(v_stride=0), "PD_ERR_INVALID_ARG"),
     (dict(max_pages=0), "PD_ERR_INVALID_ARG"), (dict(max_pages=1 << 30), "PD_ERR_UNSUPPORTED"),
-    (dict(nnz=-1), "PD_ERR_INVALID_ARG"), (dict(B=(1 << 31) - 1), "PD_ERR_UNSUPPORTED"),
+    (dict(nnz_pages=-1), "PD_ERR_INVALID_ARG"), (dict(B=(1 << 31) - 1), "PD_ERR_UNSUPPORTED"),
     (dict(pages=None), "PD_ERR_INVALID_ARG"), (dict(pages=8200), "PD_ERR_INVALID_ARG"),
     (dict(scales=62), "PD_ERR_INVALID_ARG"), (dict(at=None), "PD_ERR_INVALID_ARG"),
     (dict(vals=None), "PD_ERR_INVALID_ARG"), (dict(T=0), "PD_OK"), (dict(B=0), "PD_OK"),
+    (dict(flags=1), "PD_ERR_INVALID_ARG"), (dict(reserved=1), "PD_ERR_INVALID_ARG"), (dict(k=4097), "PD_ERR_INVALID_ARG"),
+    (dict(max_pages=1 << 62), "PD_ERR_UNSUPPORTED"),
 ])
 def test_append_refusals(L, kw, status):
     assert _append(L, **kw) == status, L.pd_get_last_error_string()
@@ -117,9 +121,22 @@ def test_layouts():
     import struct
     assert struct.calcsize("@10i2qi2fi5Q") == ctypes.sizeof(_lib.DecodeDesc)
     assert struct.calcsize("@8i3f8q") == ctypes.sizeof(_lib.QkDesc)
+    for a in (np.arange(4, dtype=np.int32), np.arange(4, dtype=np.int32)[:0], np.arange(8, dtype=np.int32)[2:5]):
+        assert _lib._host_i32(a, a.size) == a.__array_interface__["data"][0]
+    a = np.arange(4, dtype=np.int32)
+    a.flags.writeable = False
+    assert _lib._host_i32(a, 4) == a.__array_interface__["data"][0]
+    for bad in (np.arange(4), np.arange(8, dtype=np.int32)[::2], np.arange(5, dtype=np.int32), [0, 1, 2, 3], None,
+                np.arange(4, dtype=np.uint32), np.arange(4, dtype=np.float32)):
+        with pytest.raises(ValueError):
+            _lib._host_i32(bad, 4)
     v = _lib._PACK_DECODE(*range(1, 11), 11, 12, 13, 14.0, 15.0, 16, 17, 18, 19, 20, 21)
     d = _lib.DecodeDesc.from_buffer_copy(v)
     assert [getattr(d, n) for n, _ in d._fields_] == list(range(1, 22))
+    v = _lib._PACK_APPEND(*range(1, 15))
+    assert len(v) == ctypes.sizeof(_lib.AppendBsDesc)
+    d = _lib.AppendBsDesc.from_buffer_copy(v)
+    assert [getattr(d, n) for n, _ in d._fields_] == list(range(1, 15))
     v = _lib._PACK_QK(*range(1, 9), 9.0, 10.0, 11.0, *range(12, 20))
     d = _lib.QkDesc.from_buffer_copy(v)
     assert [getattr(d, n) for n, _ in d._fields_] == list(range(1, 20))
