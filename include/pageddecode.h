@@ -335,10 +335,10 @@ pd_status pd_append_paged_kv_bs(void* pages, float* scales, const void* k_new, c
  * pd_workspace_size_bs(desc, q_len, scale_rows) bytes.  Q may be F32, F16 or BF16 whatever the
  * codes.  With PD_DECODE_EARLY_INPUTS the scales, like the pages, are read only after the
  * previous kernel.
- * Arithmetic: F16 and BF16 Q with D 64 or 128 and page_size and scale_rows multiples of 16 run
- * on tensor cores (Q and the codes enter exactly, the weights 2^(s - n) vs are rounded once to
- * f16 against their own running maximum n, sums in fp32); every other shape runs an fp32 kernel
- * without tensor cores, for q_len = 1 (q_len > 1: PD_ERR_UNSUPPORTED).
+ * Arithmetic: F16 and BF16 Q with D 64 or 128 run on tensor cores (Q and the codes enter
+ * exactly, the weights 2^(s - n) vs are rounded once to f16 against their own running maximum n,
+ * sums in fp32), fastest where page_size and scale_rows are multiples of 16; F32 Q and D 256 run
+ * an fp32 kernel without tensor cores, for q_len = 1 (q_len > 1: PD_ERR_UNSUPPORTED).
  */
 pd_status pd_batch_decode_paged_kv_bs(const void* Q, const void* pages, const float* scales,
                                       const int32_t* page_table_indptr,

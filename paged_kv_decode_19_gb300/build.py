@@ -23,7 +23,7 @@ SOURCES = ["api.cu", "decode_simt.cu", "decode_mma_bf16.cu", "decode_mma_f16.cu"
            "decode_mma_fp8.cu", "decode_mma_mq_bf16.cu", "decode_mma_mq_f16.cu",
            "decode_mma_mq_fp8.cu", "decode_mma_pair_bf16.cu", "decode_mma_pair_f16.cu",
            "decode_mma_pair_fp8.cu", "merge_append.cu", "decode_noalloc.cu", "decode_bs_e4m3.cu",
-           "decode_bs_int.cu", "decode_simt_bs.cu", "append_bs.cu", "qk_norm_rope.cu"]
+           "decode_bs_int.cu", "decode_bs_rows_e4m3.cu", "decode_bs_rows_int.cu", "decode_simt_bs.cu", "append_bs.cu", "qk_norm_rope.cu"]
 
 
 def _nvcc() -> str:

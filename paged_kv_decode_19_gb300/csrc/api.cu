@@ -63,8 +63,9 @@ struct DeviceState {
   // [mma][q_dtype][kv_dtype][D 64/128/256][kernel RoPE mode 0..4][single / multi-query /
   // pages of 8 rows]; 0 = not yet known
   int occupancy[2][4][4][3][5][3] = {};
-  // the same of the block-scaled kernels: [mma][q_dtype][e4m3 / int8][D][single / multi-query]
-  int bs_occupancy[2][4][2][3][2] = {};
+  // the same of the block-scaled kernels: [SIMT / mma / mma by rows][q_dtype][e4m3 / int8][D]
+  // [single / multi-query]
+  int bs_occupancy[3][4][2][3][2] = {};
 };
 constexpr int kMaxDevices = 64;
 static DeviceState g_dev[kMaxDevices];
@@ -210,14 +211,18 @@ static bool mma_path(const pd_decode_desc* d, const void* pages) {
   return false;
 }
 
-// The same for a block-scaled cache: 16-row tiles whose rows share a scale.
-static bool bs_mma_path(const pd_decode_desc* d, const BlockScales* bs) {
-  return d->page_size % 16 == 0 && bs->scale_rows % 16 == 0 && (d->D == 64 || d->D == 128) &&
-         (d->q_dtype == kBF16 || d->q_dtype == kF16);
+// The same for a block-scaled cache.
+static bool bs_mma_path(const pd_decode_desc* d) {
+  return (d->D == 64 || d->D == 128) && (d->q_dtype == kBF16 || d->q_dtype == kF16);
 }
+// Whether its tiles are 16 rows of one page under one scale (TMA boxes), or gathered row by row.
+static bool bs_boxes(int page_size, int scale_rows) { return page_size % 16 == 0 && scale_rows % 16 == 0; }
 
 static cudaError_t bs_mma_dispatch(const DecodeParams& p, const CUtensorMap& tm, int q_dtype, int kv_dtype,
                                    dim3 grid, cudaStream_t st, MmaConfig* cfg) {
+  if (!bs_boxes(p.P, p.scale_rows))
+    return kv_dtype == kE4M3 ? launch_bs_rows_e4m3(p, tm, q_dtype, grid, st, cfg)
+                             : launch_bs_rows_int(p, tm, q_dtype, grid, st, cfg);
   return kv_dtype == kE4M3 ? launch_bs_e4m3(p, tm, q_dtype, grid, st, cfg)
                            : launch_bs_int(p, tm, q_dtype, grid, st, cfg);
 }
@@ -308,14 +313,14 @@ static bool fill_host_plan(const pd_decode_desc& d, DecodeParams& p) {
 constexpr int kCrossTiles = 10;
 static bool block_per_segment(const pd_decode_desc& d, int n_z, int wave) {
   if (n_z != 1 || (long long)d.B * d.H_kv > wave) return false;
-  const int tiles_per_page = d.page_size / 16, B = d.B;
+  const int B = d.B;
   long long total = 0, most = 0;
   for (int b = 0; b < B; ++b) {
     const int32_t* li = d.host_length_info;
     bool bad = false;
     const SeqInfo s = seq_from(d.host_indptr[b], d.host_indptr[b + 1], li[b], d.sliding_window ? li[B + b] : 0,
                                d.sliding_window ? li[2 * B + b] : 0, d.page_size, d.sliding_window != 0, bad);
-    const long long n = (long long)units_of(s, d.page_size) * tiles_per_page;
+    const long long n = (s.L + 15) / 16;
     total += n;
     most = std::max(most, n);
   }
@@ -390,14 +395,17 @@ static pd_status occupancy_for(const pd_decode_desc* d, bool use_mma, int rm, in
   return PD_OK;
 }
 
-static pd_status bs_occupancy_for(const pd_decode_desc* d, bool use_mma, int* ctas, DeviceState* ds, int q_len) {
+static pd_status bs_occupancy_for(const pd_decode_desc* d, const BlockScales* bs, bool use_mma, int* ctas,
+                                  DeviceState* ds, int q_len) {
   const int di = d->D == 64 ? 0 : d->D == 128 ? 1 : 2;
-  int& cached = ds->bs_occupancy[use_mma ? 1 : 0][d->q_dtype & 3][d->kv_dtype == kI8 ? 1 : 0][di][q_len > 1 ? 1 : 0];
+  const int kind = !use_mma ? 0 : bs_boxes(d->page_size, bs->scale_rows) ? 1 : 2;
+  int& cached = ds->bs_occupancy[kind][d->q_dtype & 3][d->kv_dtype == kI8 ? 1 : 0][di][q_len > 1 ? 1 : 0];
   std::lock_guard<std::mutex> lk(g_mu);
   if (cached == 0) {
     DecodeParams p{};
     p.D = d->D;
     p.P = d->page_size;
+    p.scale_rows = bs->scale_rows;
     p.q_len = q_len;
     cudaError_t e;
     int n = 0;
@@ -447,9 +455,9 @@ size_t pd_workspace_size_bs(const pd_decode_desc* desc, int32_t q_len, int32_t s
   if (validate_desc(desc, &bs) != PD_OK || q_len < 1) return 0;
   DeviceState* ds = nullptr;
   if (device_state(&ds) != PD_OK) return 0;
-  const bool mma = bs_mma_path(desc, &bs);
+  const bool mma = bs_mma_path(desc);
   int ctas = 1, mode, grid;
-  if ((!mma && q_len > 1) || bs_occupancy_for(desc, mma, &ctas, ds, q_len) != PD_OK) return 0;
+  if ((!mma && q_len > 1) || bs_occupancy_for(desc, &bs, mma, &ctas, ds, q_len) != PD_OK) return 0;
   size_t ws;
   plan_impl(desc, ds->num_sms, ctas, mma ? kMmaWarps : 1, &mode, &grid, &ws, q_len);
   return ws;
@@ -502,10 +510,10 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   if (bs && (!bs->scales || (reinterpret_cast<uintptr_t>(bs->scales) % 4) != 0))
     return fail(PD_ERR_INVALID_ARG, "scales is NULL or not 4-byte aligned");
 
-  const bool use_mma = bs ? bs_mma_path(desc, bs) : mma_path(desc, pages);
+  const bool use_mma = bs ? bs_mma_path(desc) : mma_path(desc, pages);
   if (bs && q_len > 1 && !use_mma)
     return fail(PD_ERR_UNSUPPORTED, "several query tokens run on the tensor-core kernel only: f16/bf16 Q, "
-                                    "D 64 or 128, page_size and scale_rows multiples of 16");
+                                    "D 64 or 128");
   DeviceState* ds = nullptr;
   st = device_state(&ds);
   if (st != PD_OK) return st;
@@ -514,11 +522,11 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
                                     "f16/bf16 (D 64 or 128) or E4M3 (D 128) KV, page size a multiple of 16");
   int ctas = 1;
   const bool k_rotated = rotary_mode != 0 && (d.flags & PD_DECODE_K_ROTATED);
-  st = bs ? bs_occupancy_for(desc, use_mma, &ctas, ds, q_len)
+  st = bs ? bs_occupancy_for(desc, bs, use_mma, &ctas, ds, q_len)
           : occupancy_for(desc, use_mma, rotary_mode + (k_rotated ? 2 : 0), &ctas, ds, q_len);
   if (st != PD_OK) return st;
   CUtensorMap tm{};
-  if (bs && use_mma) {
+  if (bs && use_mma && bs_boxes(d.page_size, bs->scale_rows)) {
     st = page_boxes(d, pages, &tm);
     if (st != PD_OK) return st;
   }
@@ -536,8 +544,8 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
         ws_need = 0;
       }
     } else if ((long long)d.B * d.H_kv < grid_blocks &&
-               d.nnz_pages * (d.page_size / 16) / d.B / kMmaWarps <=
-                   d.nnz_pages * (d.page_size / 16) * d.H_kv / ((long long)wave * kMmaWarps) + kCrossTiles) {
+               d.nnz_pages * d.page_size / 16 / d.B / kMmaWarps <=
+                   d.nnz_pages * d.page_size / 16 * d.H_kv / ((long long)wave * kMmaWarps) + kCrossTiles) {
       // without: as many equal shares as segments, by the mean length alone (even sequences then
       // fall on block borders, and uneven ones are still shared equally)
       grid_blocks = d.B * d.H_kv;

@@ -93,6 +93,9 @@ __device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap* t
       "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %2, %5}], [%6];"
       ::"r"(dst), "l"(tm), "r"(0), "r"(y), "r"(head), "r"(page), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void cp_async_chunk(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_scale(uint32_t dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -170,7 +173,10 @@ struct PartEntry {
   int b, hz, mine, n, hk, c0, hcount;
 };
 // ----------------------------------------------------------------------------- kernel
-template <typename CT, typename QT, int D, bool MQ, int NW>
+// ROWS: tiles of 16 consecutive attended rows of any pages, gathered row by row, each row with its
+// own scales; else tiles are 16 rows of one page that share a scale (page size and rows per scale
+// multiples of 16).
+template <typename CT, typename QT, int D, bool MQ, bool ROWS, int NW>
 __global__ void __launch_bounds__(NW * 32, kBsBlocks)
     decode_bs_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tm) {
   using T = BsTile<D>;
@@ -183,6 +189,8 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
   __shared__ WorkerStart s_start[NW];
   __shared__ __align__(8) uint64_t s_bar[NW][NST];
   __shared__ float4 s_meta[NW][NST][NQ];  // of a tile: K and V scale, attended rows, first row's index
+  __shared__ float2 s_rowsc[ROWS ? NW : 1][ROWS ? NST : 1][ROWS ? NQ * 16 : 1];  // ROWS: each row's scales,
+  __shared__ unsigned s_rowok[ROWS ? NW : 1][ROWS ? NST : 1][ROWS ? NQ / 2 : 1];  // and which rows count
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint8_t* const rings = s_raw + (((smem_u32(s_raw) + 1023u) & ~1023u) - smem_u32(s_raw));
@@ -202,8 +210,9 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
     if (p.values) prefetch_l2_share(p.values, (size_t)p.nnz_pages * sizeof(int32_t), blockIdx.x, gridDim.x);
   }
   if (lane == 0) {
-    // per tile two arrivals: the issuing lane's (with the box's bytes) and its cp.async copies'
-    for (int i = 0; i < NST; ++i) mbar_init(bar0 + i * 8, 2 * NQ);
+    // per tile two arrivals: the issuing lane's (with the box's bytes) and its cp.async copies'; ROWS:
+    // per stage one of every lane's copies
+    for (int i = 0; i < NST; ++i) mbar_init(bar0 + i * 8, ROWS ? 32 : 2 * NQ);
     mbar_init_fence();
   }
   // With a host plan the start-up reads launch parameters alone and runs under the tail of the
@@ -287,8 +296,9 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
   // next 32 are loaded meanwhile.
   const int a_lo = max(pcs.ra0, (pcs.pa + min(ua, pcs.na)) * P), a_hi = min(pcs.ra1, (pcs.pa + min(pend, pcs.na)) * P);
   const int b_lo = max(pcs.ob0, (pcs.pb + max(ua - pcs.na, 0)) * P), b_hi = min(pcs.ob1, (pcs.pb + max(pend - pcs.na, 0)) * P);
-  const int n_a = a_hi > a_lo ? ((a_hi + 15) >> 4) - (a_lo >> 4) : 0;
-  int n_tiles = n_a + (b_hi > b_lo ? ((b_hi + 15) >> 4) - (b_lo >> 4) : 0);
+  const int n_a = a_hi <= a_lo ? 0 : ROWS ? a_hi - a_lo : ((a_hi + 15) >> 4) - (a_lo >> 4);
+  const int n_b = b_hi <= b_lo ? 0 : ROWS ? b_hi - b_lo : ((b_hi + 15) >> 4) - (b_lo >> 4);
+  const int n_tiles = ROWS ? (n_a + n_b + 15) >> 4 : n_a + n_b;  // (ROWS: n_a, n_b count rows)
   auto tile_at = [&](int k) { return k < n_a ? ((a_lo >> 4) + k) << 4 : ((b_lo >> 4) + k - n_a) << 4; };  // offset
   auto load_page = [&](int k) -> int {  // page id of tile k, unchecked; -1 out of the table
     if (k >= n_tiles) return -1;
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
     return pidx < sg.seq.npages && (long long)sg.seq.page_begin + pidx < p.nnz_pages
                ? __ldg(p.values + sg.seq.page_begin + pidx) : -1;
   };
-  int t_page = -1, t_row = 0, t_span = 0, t_r0 = 0, page_next = load_page(lane);
+  int t_page = -1, t_row = 0, t_span = 0, t_r0 = 0, page_next = ROWS ? -1 : load_page(lane);
   auto load_batch = [&](int k0) {  // tiles k0 .. k0 + 31
     const int k = k0 + lane, page = page_next;
     page_next = load_page(k + 32);
@@ -311,8 +321,62 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
       t_page = -1;  // no such tile, or its rows do not count
     }
   };
+  // ROWS: the page (unchecked; -1 out of the table) and slot of a lane's rows 32 h + lane of the
+  // stage that starts with tile k, loaded one stage ahead
+  int rw_page[NQ / 2], rw_slot[NQ / 2];
+  auto load_rows = [&](int k) {
+#pragma unroll
+    for (int h = 0; h < NQ / 2; ++h) {
+      const int i = k * 16 + 32 * h + lane;
+      rw_page[h] = rw_slot[h] = -1;
+      if (i < n_a + n_b) {
+        const int o = i < n_a ? a_lo + i : b_lo + i - n_a, pidx = o / P;
+        rw_slot[h] = o - pidx * P;
+        if (pidx < sg.seq.npages && (long long)sg.seq.page_begin + pidx < p.nnz_pages)
+          rw_page[h] = __ldg(p.values + sg.seq.page_begin + pidx);
+      }
+    }
+  };
+  if constexpr (ROWS) load_rows(0);
+  // its rows -> stage ist: D / 16 lanes copy a row's 16-byte chunks, the row's own lane its scales
+  auto issue_rows = [&](int k) {
+    constexpr int CPR = D / 16, RPI = 32 / CPR;  // chunks per row, rows per instruction
+    const size_t to_v = (size_t)p.H_kv * P * D;
+#pragma unroll
+    for (int h = 0; h < NQ / 2; ++h) {
+      const int page = rw_page[h], slot = rw_slot[h];
+      const bool ok = page >= 0 && page < p.max_pages;
+      if (slot >= 0 && !ok) set_error(p.err, kErrBadPage);  // its row does not count
+      const unsigned rows = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) s_rowok[warp][ist][h] = rows;
+      float2* const sc = &s_rowsc[warp][ist][32 * h + lane];
+      if (ok) {
+        const float* ks = p.scales + ((size_t)page * 2 * p.H_kv + hk) * p.n_sb + ((slot * p.sb_mul) >> 20);
+        cp_async_scale(smem_u32(&sc->x), ks);
+        cp_async_scale(smem_u32(&sc->y), ks + (size_t)p.H_kv * p.n_sb);
+      } else {
+        *sc = make_float2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int it = 0; it < CPR; ++it) {
+        const int r = it * RPI + lane / CPR, x = lane % CPR * 16;  // row of the 32, byte of it
+        const int pg = __shfl_sync(0xffffffffu, page, r), sl = __shfl_sync(0xffffffffu, slot, r);
+        if ((rows >> r) & 1) {
+          const uint8_t* src = reinterpret_cast<const uint8_t*>(p.pages) +
+                               (((size_t)pg * 2 * p.H_kv + hk) * P + sl) * D + x;
+          const uint32_t dst = ring + ist * T::kStage + (2 * h + (r >> 4)) * T::kPair + tile_off<D>(r & 15, x);
+          cp_async_chunk(dst, src);
+          cp_async_chunk(dst + T::kBytes, src + to_v);
+        }
+      }
+    }
+    mbar_arrive_cp_async(bar0 + ist * 8);
+    ist = ist + 1 == NST ? 0 : ist + 1;
+    load_rows(k + NQ);
+  };
   // tiles k .. k + NQ - 1 (the next in order; their lanes side by side) -> stage ist
   auto issue = [&](int k) {
+    if constexpr (ROWS) return issue_rows(k);
     if ((k & 31) == 0) load_batch(k);
     const int i = lane - (k & 31);
     if ((unsigned)i < (unsigned)NQ) {
@@ -340,6 +404,7 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
     pdl_release();
     waited = true;
   }
+  [[maybe_unused]] const int r_first = n_a ? a_lo : b_lo - pcs.shift;  // attended index of the share's first row
   // tiles are computed NQ at a time: the last few may be empty ones
   int k_issued = 0, k_end = dead ? 0 : (n_tiles + NQ - 1) / NQ * NQ;
 #pragma unroll 1
@@ -383,6 +448,7 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
 
   // NQ tiles from the ring: their chains of loads, products and exponentials are independent and
   // overlap in the warp, and share the vote and the rescale
+  __syncwarp();  // (what the issuing lanes wrote beside their copies)
 #pragma unroll 1
   for (int k = 0; k < k_end; k += NQ) {
     const bool ok = mbar_wait(bar0 + cst * 8, cph, dead ? 1024u : kWaitPolls);
@@ -391,7 +457,7 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
     float qacc[NQ][2][4];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      meta[i] = s_meta[warp][cst][i];
+      if constexpr (!ROWS) meta[i] = s_meta[warp][cst][i];
       const uint8_t* kt_base = stage + i * T::kPair;
       // -------------------------------------------------------------- S^T = C Q^T
       uint4 ka[2][KCH];
@@ -430,43 +496,55 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
         }
       }
     // ---------------------------------------------------------------- online softmax (log2)
-    float sc[NQ][4], lv[NQ];
+    float sc[NQ][4];
+    float2 vsc[NQ];  // V scales of rows kr and kr + 8
     float t0 = -INFINITY, t1 = -INFINITY, u0 = -INFINITY, u1 = -INFINITY;  // maxima of s, s + log2 vs
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const float f0 = cs0 * meta[i].x, f1 = cs1 * meta[i].x;
-      sc[i][0] = (qacc[i][0][0] + qacc[i][1][0]) * f0;  // row kr, columns 2 q4, 2 q4 + 1
-      sc[i][1] = (qacc[i][0][1] + qacc[i][1][1]) * f1;
-      sc[i][2] = (qacc[i][0][2] + qacc[i][1][2]) * f0;  // row kr + 8
-      sc[i][3] = (qacc[i][0][3] + qacc[i][1][3]) * f1;
-      const int span = __float_as_int(meta[i].z);
-      if (span != (16 << 8)) {  // (warp-uniform)
-        const int lo = span & 0xff, hi = span >> 8;
-        if (kr < lo || kr >= hi) sc[i][0] = sc[i][1] = -INFINITY;
-        if (kr + 8 < lo || kr + 8 >= hi) sc[i][2] = sc[i][3] = -INFINITY;
+      float ka = meta[i].x, kb = meta[i].x;
+      bool full;
+      unsigned rows;  // bit r: row r counts
+      if constexpr (ROWS) {
+        const float2 sa = s_rowsc[warp][cst][16 * i + kr], sb = s_rowsc[warp][cst][16 * i + kr + 8];
+        ka = sa.x;
+        kb = sb.x;
+        vsc[i] = make_float2(sa.y, sb.y);
+        rows = (s_rowok[warp][cst][i >> 1] >> (16 * (i & 1))) & 0xffffu;
+        full = rows == 0xffffu;
+      } else {
+        vsc[i] = make_float2(meta[i].y, meta[i].y);
+        const int span = __float_as_int(meta[i].z);
+        full = span == (16 << 8);
+        rows = ((1u << (span >> 8)) - 1) & ~((1u << (span & 0xff)) - 1);
+      }
+      sc[i][0] = (qacc[i][0][0] + qacc[i][1][0]) * (cs0 * ka);  // row kr, columns 2 q4, 2 q4 + 1
+      sc[i][1] = (qacc[i][0][1] + qacc[i][1][1]) * (cs1 * ka);
+      sc[i][2] = (qacc[i][0][2] + qacc[i][1][2]) * (cs0 * kb);  // row kr + 8
+      sc[i][3] = (qacc[i][0][3] + qacc[i][1][3]) * (cs1 * kb);
+      if (!full) {  // (warp-uniform)
+        if (!((rows >> kr) & 1)) sc[i][0] = sc[i][1] = -INFINITY;
+        if (!((rows >> (kr + 8)) & 1)) sc[i][2] = sc[i][3] = -INFINITY;
         // rows outside may hold any code (e4m3 NaN): their V bytes are zeroed
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int r = vr[j & 1] + 8 * (j >> 1);
-          if (r < lo || r >= hi) {
+          if (!((rows >> (vr[j & 1] + 8 * (j >> 1))) & 1)) {
 #pragma unroll
             for (int k = 0; k < RL / 4; ++k) va[i][j][k] = 0u;
           }
         }
       }
       if constexpr (MQ) {  // causal among the new tokens
-        const int r0 = __float_as_int(meta[i].w) + kr;
+        const int r0 = (ROWS ? r_first + (k + i) * 16 : __float_as_int(meta[i].w)) + kr;
         if (r0 >= lim0) sc[i][0] = -INFINITY;
         if (r0 >= lim1) sc[i][1] = -INFINITY;
         if (r0 + 8 >= lim0) sc[i][2] = -INFINITY;
         if (r0 + 8 >= lim1) sc[i][3] = -INFINITY;
       }
-      lv[i] = __log2f(meta[i].y);
-      const float x0 = fmaxf(sc[i][0], sc[i][2]), x1 = fmaxf(sc[i][1], sc[i][3]);
-      t0 = fmaxf(t0, x0);
-      t1 = fmaxf(t1, x1);
-      u0 = fmaxf(u0, x0 + lv[i]);
-      u1 = fmaxf(u1, x1 + lv[i]);
+      const float la = __log2f(vsc[i].x), lb = ROWS ? __log2f(vsc[i].y) : la;
+      t0 = fmaxf(t0, fmaxf(sc[i][0], sc[i][2]));
+      t1 = fmaxf(t1, fmaxf(sc[i][1], sc[i][3]));
+      u0 = fmaxf(u0, fmaxf(sc[i][0] + la, sc[i][2] + lb));
+      u1 = fmaxf(u1, fmaxf(sc[i][1] + la, sc[i][3] + lb));
     }
     const float over = fmaxf(fmaxf(t0 - st_m[0], t1 - st_m[1]), fmaxf(u0 - st_n[0], u1 - st_n[1]));
     if (__any_sync(0xffffffffu, over > kLazyMaxBs || !ok)) {
@@ -506,11 +584,10 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
       pr[3] = fast_exp2(sc[i][3] - st_m[1]);
       st_d[0] += pr[0] + pr[2];
       st_d[1] += pr[1] + pr[3];
-      const float w0 = meta[i].y * g0, w1 = meta[i].y * g1;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float w = pr[e] * (e & 1 ? w1 : w0);
-        pr[e] = MQ && pr[e] == 0.f ? 0.f : w;
+        const float w = pr[e] * ((e & 1 ? g1 : g0) * (e < 2 ? vsc[i].x : vsc[i].y));
+        pr[e] = (MQ || ROWS) && pr[e] == 0.f ? 0.f : w;
       }
       // P^T as a B fragment: fragment rows 2q, 2q + 1 | 2q + 8, 2q + 9 of column g_id
       const uint32_t x0 = pack2<__half>(pr[0], pr[2]);  // column 2q: rows of g_id, g_id + 8
@@ -736,12 +813,12 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
 }
 
 // ----------------------------------------------------------------------------- launch
-template <typename CT, typename QT, int D, bool MQ>
+template <typename CT, typename QT, int D, bool MQ, bool ROWS>
 static cudaError_t launch_bs_t(const DecodeParams& p, const CUtensorMap& tm, dim3 grid,
                                cudaStream_t st, MmaConfig* cfg) {
   constexpr int NW = kMmaWarps;
   constexpr int dyn = bs_smem_bytes<D, NW>();
-  auto kern = decode_bs_kernel<CT, QT, D, MQ, NW>;
+  auto kern = decode_bs_kernel<CT, QT, D, MQ, ROWS, NW>;
   // the dynamic shared memory above 48 KB is opted into on every query of the launch
   // configuration, which the host makes once per device and variant before the first launch
   if (cfg) {
@@ -757,18 +834,18 @@ static cudaError_t launch_bs_t(const DecodeParams& p, const CUtensorMap& tm, dim
   return launch_pdl(kern, grid, dim3(NW * 32), dyn, st, p, tm);
 }
 
-template <typename CT>
+template <typename CT, bool ROWS>
 static cudaError_t launch_bs_any(const DecodeParams& p, const CUtensorMap& tm, int q_dtype, dim3 grid,
                                  cudaStream_t st, MmaConfig* cfg) {
   const bool mq = p.q_len > 1;
   auto with_q = [&](auto q_tag) -> cudaError_t {
     using QT = decltype(q_tag);
     if (p.D == 128)
-      return mq ? launch_bs_t<CT, QT, 128, true>(p, tm, grid, st, cfg)
-                : launch_bs_t<CT, QT, 128, false>(p, tm, grid, st, cfg);
+      return mq ? launch_bs_t<CT, QT, 128, true, ROWS>(p, tm, grid, st, cfg)
+                : launch_bs_t<CT, QT, 128, false, ROWS>(p, tm, grid, st, cfg);
     if (p.D == 64)
-      return mq ? launch_bs_t<CT, QT, 64, true>(p, tm, grid, st, cfg)
-                : launch_bs_t<CT, QT, 64, false>(p, tm, grid, st, cfg);
+      return mq ? launch_bs_t<CT, QT, 64, true, ROWS>(p, tm, grid, st, cfg)
+                : launch_bs_t<CT, QT, 64, false, ROWS>(p, tm, grid, st, cfg);
     return cudaErrorInvalidValue;
   };
   if (q_dtype == kBF16) return with_q(__nv_bfloat16{});

@@ -5,7 +5,7 @@ namespace pd {
 
 cudaError_t launch_bs_e4m3(const DecodeParams& p, const CUtensorMap& tm, int q_dtype, dim3 grid,
                            cudaStream_t st, MmaConfig* cfg) {
-  return launch_bs_any<F8>(p, tm, q_dtype, grid, st, cfg);
+  return launch_bs_any<F8, false>(p, tm, q_dtype, grid, st, cfg);
 }
 
 }  // namespace pd

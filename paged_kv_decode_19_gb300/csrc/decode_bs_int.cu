@@ -4,8 +4,8 @@
 namespace pd {
 
 cudaError_t launch_bs_int(const DecodeParams& p, const CUtensorMap& tm, int q_dtype, dim3 grid,
-                           cudaStream_t st, MmaConfig* cfg) {
-  return launch_bs_any<I8>(p, tm, q_dtype, grid, st, cfg);
+                          cudaStream_t st, MmaConfig* cfg) {
+  return launch_bs_any<I8, false>(p, tm, q_dtype, grid, st, cfg);
 }
 
 }  // namespace pd

@@ -66,6 +66,11 @@ cudaError_t launch_bs_e4m3(const DecodeParams& p, const CUtensorMap& tm, int q_d
                            cudaStream_t st, MmaConfig* cfg);
 cudaError_t launch_bs_int(const DecodeParams& p, const CUtensorMap& tm, int q_dtype, dim3 grid,
                           cudaStream_t st, MmaConfig* cfg);
+// The same for any page size and rows per scale: tiles gathered row by row.
+cudaError_t launch_bs_rows_e4m3(const DecodeParams& p, const CUtensorMap& tm, int q_dtype, dim3 grid,
+                                cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_bs_rows_int(const DecodeParams& p, const CUtensorMap& tm, int q_dtype, dim3 grid,
+                               cudaStream_t st, MmaConfig* cfg);
 cudaError_t launch_decode_simt_bs(const DecodeParams& p, int q_dtype, int kv_dtype, dim3 grid,
                                   cudaStream_t st, int* ctas = nullptr);
 // Append to such a cache.

@@ -43,7 +43,6 @@ def _decode(L, d, q_len=1, scale_rows=16, Q=4096, pages=8192, scales=64, scale=0
     (dict(), dict(scale_rows=64), "PD_ERR_INVALID_ARG"), (dict(), dict(q_len=0), "PD_ERR_INVALID_ARG"),
     (dict(sliding_window=1), dict(q_len=2), "PD_ERR_UNSUPPORTED"),
     (dict(D=256), dict(q_len=2), "PD_ERR_UNSUPPORTED"), (dict(q_dtype=0), dict(q_len=2), "PD_ERR_UNSUPPORTED"),
-    (dict(), dict(q_len=2, scale_rows=8), "PD_ERR_UNSUPPORTED"),
     (dict(), dict(Q=4104), "PD_ERR_INVALID_ARG"), (dict(), dict(pages=8200), "PD_ERR_INVALID_ARG"),
     (dict(), dict(scales=66), "PD_ERR_INVALID_ARG"), (dict(), dict(scales=None), "PD_ERR_INVALID_ARG"),
     (dict(), dict(Q=None), "PD_ERR_INVALID_ARG"), (dict(flags=4), {}, "PD_ERR_INVALID_ARG"),

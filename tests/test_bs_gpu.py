@@ -75,15 +75,17 @@ def test_decode_tensor_core(kv, dt, D, P, S, Hq, H):
 @pytest.mark.parametrize("dt,D,P,S,Hq,H", [("bf16", 256, 16, 16, 4, 2), ("f16", 128, 8, 8, 8, 2),
                                            ("bf16", 64, 20, 5, 6, 2), ("f32", 128, 16, 16, 9, 1),
                                            ("bf16", 128, 1, 1, 4, 4), ("f16", 128, 32, 8, 4, 1),
-                                           ("f32", 64, 7, 7, 3, 3), ("f32", 256, 3, 1, 2, 1)])
+                                           ("f32", 64, 7, 7, 3, 3), ("f32", 256, 3, 1, 2, 1),
+                                           ("f16", 64, 255, 85, 8, 2), ("bf16", 128, 11, 11, 32, 2),
+                                           ("f16", 64, 32, 2, 7, 7), ("bf16", 128, 256, 8, 16, 1)])
 def test_decode_other_shapes(kv, dt, D, P, S, Hq, H):
-    _check(_case(SHORT, Hq, H, D, P, S, kv, dt, seed=D + P), "simt")
+    _check(_case(SHORT, Hq, H, D, P, S, kv, dt, seed=D + P), "simt" if D == 256 or dt == "f32" else "mma")
 
 
 @pytest.mark.parametrize("splits", [0, 1, 2, 7])
-@pytest.mark.parametrize("kv,D", [("e4m3", 128), ("int8", 64)])
-def test_decode_splits_and_lengths(splits, kv, D):
-    c = _case([3000, 0, 1, 4096, 517, 16], 8, 2, D, 32, 32, kv, "bf16", seed=7)
+@pytest.mark.parametrize("kv,D,P,S", [("e4m3", 128, 32, 32), ("int8", 64, 32, 32), ("int8", 128, 8, 8), ("e4m3", 64, 20, 4)])
+def test_decode_splits_and_lengths(splits, kv, D, P, S):
+    c = _case([3000, 0, 1, 4096, 517, 16], 8, 2, D, P, S, kv, "bf16", seed=7)
     _check(c, "mma", num_splits=splits)
     _check(c, "mma", num_splits=splits, out_dt=torch.float32)
 
@@ -91,7 +93,7 @@ def test_decode_splits_and_lengths(splits, kv, D):
 @pytest.mark.parametrize("lengths,Hq,H,n", [([300], 32, 8, 1), ([64, 1, 0, 70, 3], 8, 8, 1), ([5000, 30, 200], 8, 2, 1),
                                             ([40] * 37, 4, 4, 1), ([900, 3, 77], 8, 2, 2), ([700, 20], 32, 2, 1),
                                             ([100, 16, 4000, 0], 16, 4, 4)])
-@pytest.mark.parametrize("kv,D,P,S", [("int8", 128, 16, 16), ("e4m3", 64, 64, 32)])
+@pytest.mark.parametrize("kv,D,P,S", [("int8", 128, 16, 16), ("e4m3", 64, 64, 32), ("e4m3", 128, 8, 4)])
 def test_decode_planned_on_the_host(lengths, Hq, H, n, kv, D, P, S):
     """Host copies of the table: a block per segment for short or even sequences, else equal
     shares, at every warp count a segment can have."""
@@ -110,7 +112,7 @@ def test_decode_one_long_sequence():
     _check(_case([70001], 8, 1, 128, 64, 16, "int8", "bf16", seed=8), "mma")
 
 
-@pytest.mark.parametrize("P,D", [(16, 128), (64, 64), (8, 128)])
+@pytest.mark.parametrize("P,D", [(16, 128), (64, 64), (8, 128), (20, 64)])
 def test_decode_window_and_sinks(P, D):
     lengths = [5, 100, 333, 1000, 64]
     wins = [(0, 0), (50, 4), (301, 1), (999, 20), (17, 17)]
@@ -119,7 +121,8 @@ def test_decode_window_and_sinks(P, D):
 
 
 @pytest.mark.parametrize("n,Hq,H,D,P,S", [(2, 8, 2, 128, 16, 16), (3, 8, 8, 64, 32, 16), (5, 12, 2, 128, 32, 32),
-                                          (4, 16, 2, 64, 16, 16), (9, 4, 4, 128, 64, 16)])
+                                          (4, 16, 2, 64, 16, 16), (9, 4, 4, 128, 64, 16),
+                                             (2, 8, 2, 128, 8, 8), (3, 8, 8, 64, 20, 5), (5, 12, 2, 128, 1, 1)])
 @pytest.mark.parametrize("kv", ["e4m3", "int8"])
 def test_decode_several_queries(n, Hq, H, D, P, S, kv):
     # lengths below q_len leave the first tokens without a row
@@ -127,11 +130,11 @@ def test_decode_several_queries(n, Hq, H, D, P, S, kv):
 
 
 @pytest.mark.parametrize("pow2", [False, True])
-@pytest.mark.parametrize("kv,dt", [("e4m3", "bf16"), ("int8", "f16")])
-def test_decode_scales_far_apart(kv, dt, pow2):
+@pytest.mark.parametrize("kv,dt,S", [("e4m3", "bf16", 16), ("int8", "f16", 16), ("int8", "bf16", 4)])
+def test_decode_scales_far_apart(kv, dt, S, pow2):
     """V scales over 2^+-24 (K's tame, or every softmax would have one row), with zero and
     smallest scales among them: blocks of small weight and large scale count as much as others."""
-    c = _case([200, 1500, 40], 8, 2, 128, 16, 16, kv, dt, seed=11, spread=0.5, pow2=pow2)
+    c = _case([200, 1500, 40], 8, 2, 128, 16, S, kv, dt, seed=11, spread=0.5, pow2=pow2)
     g = torch.Generator().manual_seed(12)
     ok = ~torch.isnan(c["scales"][:, 1])
     f = torch.exp2(torch.randint(-24, 25, ok.shape, generator=g).float()).to(DEV)
@@ -219,21 +222,22 @@ def test_decode_is_the_same_every_time():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_decode_nonfinite_scale_stays_in_its_block():
+@pytest.mark.parametrize("S", [16, 8])
+def test_decode_nonfinite_scale_stays_in_its_block(S):
     for n, dt in ((1, "bf16"), (2, "f16")):
-        c = _case([100, 100, 40], 8, 2, 128, 16, 16, "e4m3", dt, n=n, seed=17)
+        c = _case([100, 100, 40], 8, 2, 128, 16, S, "e4m3", dt, n=n, seed=17)
         ref = _ref(c)
         ip = c["indptr"].tolist()
         # the last page of sequence 1, V of head 0: only heads 0-3 of sequence 1 are touched,
         # and of several queries only those that attend a row of the block
-        c["scales"][int(c["vals"][ip[2] - 1]), 1, 0, 0] = float("nan")
+        c["scales"][int(c["vals"][ip[2] - 1]), 1, 0, 0] = float("nan")  # (rows 96-99 of 100)
         out, lse = _run(c)
         out, lse = out.view(3, n, 8, 128), lse.view(3, n, 8)
         assert torch.isnan(out[1, :, :4]).all() and torch.isfinite(out[1, :, 4:]).all()
         keep = [0, 2]
         check_decode(out[keep], lse[keep], (ref[0][keep], ref[1][keep], tuple(x[keep] for x in ref[2])), 100)
     # a block that an earlier query token does not attend: 17 rows, 2 tokens, token 0 sees 16
-    c = _case([17], 4, 1, 128, 16, 16, "e4m3", "bf16", n=2, seed=18)
+    c = _case([17], 4, 1, 128, 16, S, "e4m3", "bf16", n=2, seed=18)
     ref = _ref(c)
     for side in (0, 1):
         d = dict(c, scales=c["scales"].clone())
@@ -253,7 +257,7 @@ def test_decode_bad_page_ids_are_skipped_and_reported():
         assert pd.check_device_errors() == "PD_ERR_BAD_PAGE"
         assert torch.isfinite(out.float()).all()
         check_decode(out[1:], lse[1:], (good[0][1:], good[1][1:], tuple(x[1:] for x in good[2])), 100,
-                     f16_weights=P == 16)
+                     f16_weights=True)
         assert pd.check_device_errors() == "PD_OK"
 
 
