@@ -64,9 +64,12 @@ def _dist():
 
 
 # Sources the tensor-core decode's launches depend on (its kernel, the shared device code
-# and the host planner); the SIMT kernel, merge/append kernels and the workspace arenas
-# do not change what it reads or writes.
-_TRAFFIC_EXCLUDE = ("decode_simt.cu", "merge_append.cu", "decode_noalloc.cu", "arena.h")
+# and the host planner); the SIMT kernel, merge/append kernels, the workspace arenas and the
+# block-scaled cache's kernels do not change what it reads or writes.
+_TRAFFIC_EXCLUDE = ("decode_simt.cu", "merge_append.cu", "decode_noalloc.cu", "arena.h",
+                    "decode_simt.cuh", "decode_simt_bs.cu", "decode_bs.cuh", "decode_bs_e4m3.cu",
+                    "decode_bs_int.cu", "decode_bs_rows_e4m3.cu", "decode_bs_rows_int.cu",
+                    "append_bs.cu", "qk_norm_rope.cu")
 
 
 def _sources_digest() -> str:
