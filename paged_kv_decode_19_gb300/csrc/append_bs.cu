@@ -19,9 +19,10 @@
 // loads (sequence search, table, rows) for one token per sequence.  One warp per (touched block,
 // K | V, head): the rows of a block are in registers when they fit (kKeep steps of 32 / (D / 8)
 // rows), so each is read once; the maximum is taken on the integer patterns (magnitude bits order
-// like the values, and a non-finite one shows as the largest).  Measured on one GB300: 9725 tokens
-// of 8 heads of 128 in five sequences 14.4 us (61 % of the copy rate on 60 MB, inputs from HBM),
-// 256 sequences of one token 6.6 us, of which the loads one after the other are most.
+// like the values, and a non-finite one shows as the largest).  Measured on one GB300: 9713 tokens
+// of 8 heads of 128 in five sequences 13.1 us (67 % of the copy rate on 60 MB, inputs from HBM;
+// 14.4 with three blocks of eight warps an SM instead of eight of four), 256 sequences of one
+// token 6.4 us, of which the loads one after the other are most.
 #include <type_traits>
 
 #include "common.cuh"
@@ -135,13 +136,13 @@ __device__ __forceinline__ void decode8(uint2 c, float (&x)[8]) {
   }
 }
 
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 4;
 
 // Slots: sequence b owns slots [append_indptr[b] / S + 2 b, append_indptr[b+1] / S + 2 b + 2),
 // at least as many as the blocks its new rows touch (n rows touch at most (n - 2) / S + 2);
 // blockIdx.x is the slot, a warp takes one (head, K | V) of its block.
 template <typename IT, typename CT, int D, bool VEC>
-__global__ void __launch_bounds__(kAppendWarps * 32)
+__global__ void __launch_bounds__(kAppendWarps * 32, 8)
     append_bs_kernel(const __grid_constant__ AppendBsParams a) {
   constexpr int LPR = D / 8;                  // lanes per row
   constexpr int RPS = 32 / LPR;               // rows per step of the warp

@@ -81,13 +81,13 @@ __device__ __forceinline__ void load_pairs(const float* a, const float* b, float
 // Rows in vectors: D a multiple of 8 (at most 8 LPR), 16-byte aligned rows, a rotated part that
 // is a multiple of 8.  MODE 0 no rotation, 1 rotate-half, 2 interleaved; a lane holds eight dims,
 // both of every rotated pair (rotate-half: four of each half, as two 8-byte accesses of a 16-bit
-// row; a 16-byte chunk and shuffles for the partner took 38 us instead of 36.5 for 8192 tokens of
-// 40 heads of 128, bf16).  A pass is 32 / LPR heads of one token, all queries or all keys; a warp takes
+// row; a 16-byte chunk and shuffles for the partner cost 1.5 us more for 8192 tokens of 40 heads of
+// 128, bf16).  A pass is 32 / LPR heads of one token, all queries or all keys; a warp takes
 // part `p` of the `parts` of a token's passes (grid stride over the T * parts tasks), GP passes
 // at a time, the next GP loaded while these are computed.  No block barrier after the start:
 // the warps drift apart, so that loads, products and stores of different tokens overlap (a block
-// per token with a barrier for its angles took 48 us).  36.5 us are 68 % of the copy rate; the
-// same kernel without norm and rotation takes 29 us, and of the rest half is the norm's shuffles.
+// per token with a barrier for its angles took 48 us).  33.2 us are 75 % of the copy rate; the same
+// kernel takes 28.3 us without norm and rotation, 30.1 with the norm alone, 31.0 with the rotation.
 //
 // With x' the rotation partner of x, an output is rs (x A + x' B), A = w cos and B = -+ w' sin:
 // A and B are the same for every query (key) head of a token, so a row costs two products per
@@ -206,14 +206,12 @@ __global__ void __launch_bounds__(kQkThreads, 3)
 #pragma unroll
         for (int i = 0; i < 4; ++i) A[i] = mul_f2(A[i], co[i]);
       }
-#pragma unroll 1
-      for (; n > 0; n -= GP) {
-        const int now = mine;
-        mine -= GP;
-        load(nxt);  // (none left: nothing)
+      // the passes of `cur`, of which the lane stores the first `now`; the full group has no branch, so
+      // that its passes' shuffles and products interleave (36.7 -> 33.2 us)
+      auto group = [&](int now, auto full) {
 #pragma unroll
         for (int u = 0; u < GP; ++u) {
-          if (u >= n) break;  // (warp-uniform)
+          if (!decltype(full)::value && u >= n) break;  // (warp-uniform)
           float2 x[4], y[4];
           unpack8<XT>(cur[u], x);
           float rs = 1.f;
@@ -243,10 +241,18 @@ __global__ void __launch_bounds__(kQkThreads, 3)
             }
           }
         }
+      };
+#pragma unroll 1
+      for (; n >= GP; n -= GP) {
+        const int now = mine;
+        mine -= GP;
+        load(nxt);  // (none left: nothing)
+        group(now, std::true_type{});
         dst += GP * step_to;
 #pragma unroll
         for (int u = 0; u < GP; ++u) cur[u] = nxt[u];
       }
+      if (n > 0) group(mine, std::false_type{});
     }
   }
 }
