@@ -674,13 +674,17 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
   // lane k < 2 NW of every warp holds entry k; `same`: the entries of its segment
   const PartEntry mine_e = s_part[(lane >> 1) % NW][lane & 1];
   const bool held = lane < 2 * NW && mine_e.b >= 0;
-  const long long key = held ? (long long)mine_e.b * p.H_kv * p.n_z + mine_e.hz : -1 - lane;
-  const unsigned same_l = __match_any_sync(0xffffffffu, key);
+  unsigned same_l = 0;
   int units = 0;  // of its segment in the block
+  const int key_b = held ? mine_e.b : -1;  // (a match instruction takes a turn per distinct value)
 #pragma unroll
   for (int k = 0; k < 2 * NW; ++k) {
+    const int b = __shfl_sync(0xffffffffu, key_b, k), hz = __shfl_sync(0xffffffffu, mine_e.hz, k);
     const int x = __shfl_sync(0xffffffffu, mine_e.mine, k);
-    if ((same_l >> k) & 1) units += x;
+    if (b >= 0 && b == key_b && hz == mine_e.hz) {
+      same_l |= 1u << k;
+      units += x;
+    }
   }
   const unsigned leaders = __ballot_sync(0xffffffffu, held && (same_l & ((1u << lane) - 1)) == 0);
   const unsigned whole_l = __ballot_sync(0xffffffffu, held && units == mine_e.n);
@@ -754,7 +758,7 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
   fence_acq_rel_gpu();
   __syncthreads();
   if (warp == 0 && (open >> lane) & 1) {
-    int* cnt = p.counters + key;
+    int* cnt = p.counters + (size_t)mine_e.b * p.H_kv * p.n_z + mine_e.hz;
     const int prev = atomicAdd(cnt, units);
     s_last[lane] = prev + units == mine_e.n;
     if (s_last[lane]) *cnt = 0;  // every other block's units have arrived: reset for reuse
