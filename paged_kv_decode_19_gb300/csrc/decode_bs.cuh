@@ -8,8 +8,8 @@
 // worker on its share of the pages.
 //
 // What bounds it: the codes, 2 D bytes per row and KV head, read once from HBM (DRAM traffic
-// 1.003 of them).  Each warp keeps a ring of two stages in shared memory, NQ 16-row tiles each (8
-// KB); a tile's K and V rows come by one 5-D TMA box and its two scales by 4-byte cp.async on the
+// 1.001 to 1.005 of them).  Each warp keeps a ring of two stages in shared memory, NQ 16-row
+// tiles each (8 KB); a tile's K and V rows come by one 5-D TMA box and its two scales by 4-byte cp.async on the
 // stage's mbarrier, issued by NQ lanes at once while the other stage is computed.  Eight warps an
 // SM then hold up to 128 KB in flight (the HBM rate times a 1 us latency needs about 45 KB of an
 // SM); more and smaller blocks, or deeper rings in fewer blocks, were slower (256 sequences: 197
@@ -20,7 +20,8 @@
 // together: their chains overlap and share the vote, the rescale and the wait (a tile alone in a
 // warp: 0.83 us one by one, 0.42 us now).  Short lists are padded with empty tiles; one copy of the
 // code for full stages only keeps the loop in reach of the instruction cache, whose misses are the
-// largest stall left (1.0 of 4.6 cycles an instruction).
+// largest stall left (int8: 1.0 of 5.2 cycles an instruction; e4m3: 1.4 of 7.0, level with the
+// fixed waits between dependent instructions).
 //   Measured on one GB300 (of the 6779 GB/s copy rate): eight contexts of 32K to 128K rows 194 us
 // (96 %; e4m3 in blocks of 64 rows 191 us, 98 %), 256 sequences of 300 to 4200 rows 184 us (92 %),
 // 32 of 512 to 4096 rows 34 us (55 %: about 3 us until the first tile, 3 us of uneven ends and 7 us
