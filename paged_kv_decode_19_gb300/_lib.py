@@ -410,12 +410,12 @@ def batch_decode_paged_kv_bs(Q, pages, scales, page_table_indptr, page_table_val
         B, q_len, H_qo, D = shape
     else:
         raise ValueError("Q must be [B, H_qo, D] or [B, q_len, H_qo, D]")
-    vals, n_li = page_table_values, length_info.numel()
+    vals, li_shape = page_table_values, length_info.shape
     if (kv is None or len(pshape) != 5 or len(sshape) != 4 or pshape[1] != 2 or sshape[1] != 2
             or sshape[0] != pshape[0] or sshape[2] != pshape[2] or scales.dtype != _F32
             or sshape[3] < 1 or pshape[3] % sshape[3] or page_table_indptr.dtype != _I32
             or length_info.dtype != _I32 or page_table_indptr.numel() != B + 1
-            or (n_li != B and n_li != 3 * B) or (vals is not None and vals.dtype != _I32)):
+            or (li_shape != (B,) and li_shape != (3, B)) or (vals is not None and vals.dtype != _I32)):
         _bs_refuse(pages, scales, page_table_indptr, vals, length_info, B)
     max_pages, _, H_kv, P, D_kv = pshape
     if D_kv != D:
@@ -443,9 +443,9 @@ def batch_decode_paged_kv_bs(Q, pages, scales, page_table_indptr, page_table_val
         if sink.get_device() != dev:
             _refuse(dev, sink)
     if host_meta is not None:
-        host_ip, host_li = _host_i32(host_meta[0], B + 1), _host_i32(host_meta[1], n_li)
+        host_ip, host_li = _host_i32(host_meta[0], B + 1), _host_i32(host_meta[1], length_info.numel())
     desc = _PACK_DECODE(B, H_qo, H_kv, D, P, DTYPE_CODES[Q.dtype], kv, DTYPE_CODES[output.dtype],
-                        length_info.dim() == 2, num_splits, max_pages, n_vals, 0, 1.0, 1.0,
+                        len(li_shape) == 2, num_splits, max_pages, n_vals, 0, 1.0, 1.0,
                         DECODE_EARLY_INPUTS if early_inputs else 0, ws_at, ws_bytes, sink_at,
                         host_ip, host_li)
     st = (_lib or lib()).pd_batch_decode_paged_kv_bs(
@@ -470,14 +470,14 @@ def append_paged_kv_bs(pages, scales, k_new, v_new, append_indptr, page_table_in
     length_info as they stand after the append.  k_new and v_new may be slices of a larger
     tensor along the heads (any token stride)."""
     pshape, sshape, kv = pages.shape, scales.shape, BS_DTYPE_CODES.get(pages.dtype)
-    B, n_li, vals = append_indptr.numel() - 1, length_info.numel(), page_table_values
+    B, li_shape, vals = append_indptr.numel() - 1, length_info.shape, page_table_values
     if B < 0 or append_indptr.dtype != _I32:
         raise ValueError("append_indptr must be int32 [B+1]")
     if (kv is None or len(pshape) != 5 or len(sshape) != 4 or pshape[1] != 2 or sshape[1] != 2
             or sshape[0] != pshape[0] or sshape[2] != pshape[2] or scales.dtype != _F32
             or sshape[3] < 1 or pshape[3] % sshape[3] or page_table_indptr.dtype != _I32
             or length_info.dtype != _I32 or page_table_indptr.numel() != B + 1
-            or (n_li != B and n_li != 3 * B) or vals.dtype != _I32):
+            or (li_shape != (B,) and li_shape != (3, B)) or vals.dtype != _I32):
         _bs_refuse(pages, scales, page_table_indptr, vals, length_info, B)
     max_pages, _, H_kv, P, D = pshape
     shape, dtype = k_new.shape, k_new.dtype

@@ -1,0 +1,42 @@
+"""Refusals of the block-scaled cache's calls, and of what they share with the other decodes, that
+need no GPU."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_decode_19_gb300 as pd
+
+
+def _cache(B=2, H=2, P=32, D=64):
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)  # noqa: E731
+    return dict(pages=torch.zeros(4, 2, H, P, D, dtype=torch.int8), scales=torch.ones(4, 2, H, 2),
+                page_table_indptr=i32(B + 1), page_table_values=i32(3), length_info=i32(B))
+
+
+def _decode_args(B=2):
+    Q = torch.zeros(B, 4, 64, dtype=torch.bfloat16)
+    return dict(_cache(B), Q=Q, output=Q.clone(), lse=torch.zeros(B, 4))
+
+
+def _append_args(B=2):
+    k = torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    return dict(_cache(B), k_new=k, v_new=k, append_indptr=torch.zeros(B + 1, dtype=torch.int32))
+
+
+CALLS = [(pd.batch_decode_paged_kv_bs, _decode_args), (pd.append_paged_kv_bs, _append_args)]
+
+
+@pytest.mark.parametrize("call,args", CALLS)
+@pytest.mark.parametrize("B", [1, 2, 3])
+def test_length_info_is_taken_by_its_shape(call, args, B):
+    """[B], or [3, B] of a windowed cache: a [1, B] or [B, 1] read as a window would be read past
+    its end, a flat [3 B] or a [B, 3] is not what its reader means."""
+    a = args(B)
+    for shape in ((1, B), (B, 1), (3 * B,), (B, 3), (2, B), (1, 3, B), (3, B, 1), (B + 1,), (3, B + 1), ()):
+        if shape in ((B,), (3, B)):  # (B = 1, 3: one of the two forms)
+            continue
+        with pytest.raises(ValueError, match="length_info"):
+            call(**{**a, "length_info": torch.zeros(shape, dtype=torch.int32)})
+    for shape in ((B,), (3, B)):  # taken: what is wrong then is the device
+        with pytest.raises(ValueError, match="current GPU"):
+            call(**{**a, "length_info": torch.zeros(shape, dtype=torch.int32)})
