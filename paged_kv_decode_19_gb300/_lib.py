@@ -243,6 +243,10 @@ def make_desc(Q, pages, indptr, values, length_info, out, *, num_splits=0, max_k
     max_pages, two, H_kv, P, D2 = pages.shape
     if two != 2 or D2 != D:
         raise ValueError(f"pages must be [max_pages, 2, H_kv, P, {D}], got {tuple(pages.shape)}")
+    # windowed: [3, B]; else the first B entries of a list (a flat window is no list of lengths)
+    n_li = length_info.numel()
+    if length_info.shape != (3, B) and (length_info.dim() != 1 or n_li < B or n_li == 3 * B > 0):
+        raise ValueError(f"length_info must be [{B}] or [3, {B}], got {tuple(length_info.shape)}")
     return DecodeDesc(
         B=B, H_qo=H_qo, H_kv=H_kv, D=D, page_size=P, q_dtype=DTYPE_CODES[Q.dtype],
         kv_dtype=DTYPE_CODES[pages.dtype], out_dtype=DTYPE_CODES[out.dtype],

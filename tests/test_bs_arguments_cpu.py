@@ -40,3 +40,21 @@ def test_length_info_is_taken_by_its_shape(call, args, B):
     for shape in ((B,), (3, B)):  # taken: what is wrong then is the device
         with pytest.raises(ValueError, match="current GPU"):
             call(**{**a, "length_info": torch.zeros(shape, dtype=torch.int32)})
+
+
+@pytest.mark.parametrize("B", [1, 2, 3])
+def test_length_info_of_the_other_decodes(B):
+    """The desc of the other entry points: windowed by a [3, B], else the first B of a list (a
+    longer buffer is taken as before, but no flat window)."""
+    Q = torch.zeros(B, 4, 64)
+    pages, ip = torch.zeros(4, 2, 2, 16, 64), torch.zeros(B + 1, dtype=torch.int32)
+
+    def desc(*shape):
+        return pd.make_desc(Q, pages, ip, ip, torch.zeros(shape, dtype=torch.int32), Q)
+    for shape in ((1, B), (B, 1), (B, 3), (2, B), (3, B + 1), (3 * B,), (B - 1,), (3, 1, B), ()):
+        if shape not in ((3, B), (B,)):
+            with pytest.raises(ValueError, match="length_info"):
+                desc(*shape)
+    assert desc(B).sliding_window == 0 and desc(3, B).sliding_window == 1 and desc(3 * B + 1).sliding_window == 0
+    none = torch.zeros(0, dtype=torch.int32)
+    assert pd.make_desc(Q[:0], pages, ip[:1], ip, none, Q[:0]).B == 0
