@@ -263,7 +263,7 @@ def make_desc(Q, pages, indptr, values, length_info, out, *, num_splits=0, max_k
 
 def _host_i32(a, n):
     try:
-        if a.size != n or a.dtype.char != "i":
+        if a.size != n or a.dtype.char != "i" or not a.dtype.isnative:
             raise ValueError
         return ctypes.addressof(ctypes.c_char.from_buffer(a))  # (a writable C-contiguous buffer)
     except (AttributeError, TypeError, ValueError):

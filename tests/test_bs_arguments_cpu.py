@@ -58,3 +58,16 @@ def test_length_info_of_the_other_decodes(B):
     assert desc(B).sliding_window == 0 and desc(3, B).sliding_window == 1 and desc(3 * B + 1).sliding_window == 0
     none = torch.zeros(0, dtype=torch.int32)
     assert pd.make_desc(Q[:0], pages, ip[:1], ip, none, Q[:0]).B == 0
+
+
+def test_host_copies_in_another_byte_order_are_refused():
+    from paged_kv_decode_19_gb300 import _lib
+    for writable in (True, False):
+        for dt in (">i4", ">u4", ">f4"):
+            a = np.arange(4).astype(dt)
+            a.flags.writeable = writable
+            with pytest.raises(ValueError):
+                _lib._host_i32(a, 4)
+        for a in (np.arange(4, dtype="<i4"), np.arange(4, dtype="=i4"), np.arange(4).astype(">i4").astype(np.int32)):
+            a.flags.writeable = writable
+            assert _lib._host_i32(a, 4) == a.__array_interface__["data"][0]
