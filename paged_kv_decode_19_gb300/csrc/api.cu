@@ -883,7 +883,7 @@ pd_status pd_append_paged_kv_bs(void* pages, float* scales, const void* k_new, c
     return fail(PD_ERR_INVALID_ARG, "k_stride and v_stride must be at least H_kv * D");
   if (d.max_pages > INT_MAX || d.max_pages * 2 * d.H_kv > INT_MAX)
     return fail(PD_ERR_UNSUPPORTED, "max_pages * 2 * H_kv exceeds 2^31");
-  if ((long long)d.T / d.scale_rows + 2ll * d.B > INT_MAX || d.H_kv > 200000)
+  if ((long long)d.T / d.scale_rows + 2ll * d.B > INT_MAX || append_bs_grid_y(d.H_kv) > 65535)
     return fail(PD_ERR_UNSUPPORTED, "T, B or H_kv too large");
   if (d.T == 0 || d.B == 0) return PD_OK;
   if (!pages || !scales || !k_new || !v_new || !append_indptr || !page_table_indptr || !page_table_values ||

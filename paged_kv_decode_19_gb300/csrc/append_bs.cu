@@ -136,8 +136,6 @@ __device__ __forceinline__ void decode8(uint2 c, float (&x)[8]) {
   }
 }
 
-constexpr int kAppendWarps = 4;
-
 // Slots: sequence b owns slots [append_indptr[b] / S + 2 b, append_indptr[b+1] / S + 2 b + 2),
 // at least as many as the blocks its new rows touch (n rows touch at most (n - 2) / S + 2);
 // blockIdx.x is the slot, a warp takes one (head, K | V) of its block.
@@ -314,7 +312,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 8)
 
 template <typename IT, typename CT, int D>
 static cudaError_t launch_d(const AppendBsParams& a, bool vec, cudaStream_t st) {
-  const dim3 grid((unsigned)(a.T / a.S + 2 * a.B), (unsigned)((2 * a.H_kv + kAppendWarps - 1) / kAppendWarps));
+  const dim3 grid((unsigned)(a.T / a.S + 2 * a.B), (unsigned)append_bs_grid_y(a.H_kv));
   const dim3 block(kAppendWarps * 32);
   return vec ? launch_pdl(append_bs_kernel<IT, CT, D, true>, grid, block, 0, st, a)
              : launch_pdl(append_bs_kernel<IT, CT, D, false>, grid, block, 0, st, a);

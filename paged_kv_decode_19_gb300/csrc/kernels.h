@@ -73,7 +73,10 @@ cudaError_t launch_bs_rows_int(const DecodeParams& p, const CUtensorMap& tm, int
                                cudaStream_t st, MmaConfig* cfg);
 cudaError_t launch_decode_simt_bs(const DecodeParams& p, int q_dtype, int kv_dtype, dim3 grid,
                                   cudaStream_t st, int* ctas = nullptr);
-// Append to such a cache.
+// Append to such a cache: grid x = slots of touched blocks, grid y = blocks of kAppendWarps (K | V,
+// head) pairs.
+constexpr int kAppendWarps = 4;
+inline long long append_bs_grid_y(int H_kv) { return (2ll * H_kv + kAppendWarps - 1) / kAppendWarps; }
 struct AppendBsParams {
   uint8_t* pages;
   float* scales;

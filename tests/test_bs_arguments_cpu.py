@@ -1,10 +1,14 @@
 """Refusals of the block-scaled cache's calls, and of what they share with the other decodes, that
 need no GPU."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
+import __graft_entry__
 import paged_kv_decode_19_gb300 as pd
+from paged_kv_decode_19_gb300 import _lib
 
 
 def _cache(B=2, H=2, P=32, D=64):
@@ -61,7 +65,6 @@ def test_length_info_of_the_other_decodes(B):
 
 
 def test_host_copies_in_another_byte_order_are_refused():
-    from paged_kv_decode_19_gb300 import _lib
     for writable in (True, False):
         for dt in (">i4", ">u4", ">f4"):
             a = np.arange(4).astype(dt)
@@ -71,3 +74,18 @@ def test_host_copies_in_another_byte_order_are_refused():
         for a in (np.arange(4, dtype="<i4"), np.arange(4, dtype="=i4"), np.arange(4).astype(">i4").astype(np.int32)):
             a.flags.writeable = writable
             assert _lib._host_i32(a, 4) == a.__array_interface__["data"][0]
+
+
+def test_append_takes_the_heads_that_its_grid_holds():
+    """Grid y, at most 65535, is (2 H_kv + 3) / 4 blocks of four (K | V, head) pairs: H_kv <= 131070."""
+    __graft_entry__.build()
+
+    def status(H):
+        # sizes alone are looked at before the pointers: with those NULL, accepted sizes say so
+        d = _lib.AppendBsDesc(T=1, B=1, H_kv=H, D=64, page_size=1, scale_rows=1, in_dtype=2, kv_dtype=4, max_pages=1,
+                              nnz_pages=1, k_stride=H * 64, v_stride=H * 64)
+        return _lib.STATUS[_lib.lib().pd_append_paged_kv_bs(*[None] * 8, ctypes.byref(d), None)]
+    for H in (1, 65535, 131070):
+        assert status(H) == "PD_ERR_INVALID_ARG"
+    for H in (131071, 150000, 200000, 200001, (1 << 30) - 1):
+        assert status(H) == "PD_ERR_UNSUPPORTED"
