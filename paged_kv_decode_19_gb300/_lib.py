@@ -386,6 +386,8 @@ def _bs_refuse(pages, scales, page_table_indptr, page_table_values, length_info,
     for t in (page_table_indptr, page_table_values, length_info):
         if t is not None and t.dtype != torch.int32:
             raise ValueError("the page table and length_info must be int32")
+    if page_table_values is None and page_table_indptr.numel() == B + 1 and length_info.shape in ((B,), (3, B)):
+        raise ValueError("page_table_values must be int32")
     raise ValueError(f"page_table_indptr [{B} + 1] and length_info [{B}] or [3, {B}]")
 
 
@@ -426,6 +428,9 @@ def batch_decode_paged_kv_bs(Q, pages, scales, page_table_indptr, page_table_val
         raise ValueError("Q must be [B, H_qo, D] or [B, q_len, H_qo, D]")
     if output.shape != shape or lse.shape != shape[:-1] or lse.dtype != _F32:
         raise ValueError("output must be shaped like Q and lse float32 like its heads")
+    q_code, out_code = DTYPE_CODES.get(Q.dtype), DTYPE_CODES.get(output.dtype)
+    if q_code is None or out_code is None:
+        raise ValueError("Q and output must be float32, float16 or bfloat16")
     dev = _device(Q)
     if not (pages.get_device() == scales.get_device()
             == page_table_indptr.get_device() == length_info.get_device() == output.get_device()
@@ -448,7 +453,7 @@ def batch_decode_paged_kv_bs(Q, pages, scales, page_table_indptr, page_table_val
             _refuse(dev, sink)
     if host_meta is not None:
         host_ip, host_li = _host_i32(host_meta[0], B + 1), _host_i32(host_meta[1], length_info.numel())
-    desc = _PACK_DECODE(B, H_qo, H_kv, D, P, DTYPE_CODES[Q.dtype], kv, DTYPE_CODES[output.dtype],
+    desc = _PACK_DECODE(B, H_qo, H_kv, D, P, q_code, kv, out_code,
                         len(li_shape) == 2, num_splits, max_pages, n_vals, 0, 1.0, 1.0,
                         DECODE_EARLY_INPUTS if early_inputs else 0, ws_at, ws_bytes, sink_at,
                         host_ip, host_li)
@@ -481,13 +486,15 @@ def append_paged_kv_bs(pages, scales, k_new, v_new, append_indptr, page_table_in
             or sshape[0] != pshape[0] or sshape[2] != pshape[2] or scales.dtype != _F32
             or sshape[3] < 1 or pshape[3] % sshape[3] or page_table_indptr.dtype != _I32
             or length_info.dtype != _I32 or page_table_indptr.numel() != B + 1
-            or (li_shape != (B,) and li_shape != (3, B)) or vals.dtype != _I32):
+            or (li_shape != (B,) and li_shape != (3, B)) or vals is None or vals.dtype != _I32):
         _bs_refuse(pages, scales, page_table_indptr, vals, length_info, B)
     max_pages, _, H_kv, P, D = pshape
     shape, dtype = k_new.shape, k_new.dtype
     if len(shape) != 3 or shape[1] != H_kv or shape[2] != D or v_new.shape != shape or v_new.dtype != dtype:
         raise ValueError("k_new and v_new must be [T, H_kv, D] of one dtype")
-    T = shape[0]
+    T, in_code = shape[0], DTYPE_CODES.get(dtype)
+    if in_code is None:
+        raise ValueError("k_new and v_new must be float32, float16 or bfloat16")
     (ks, kh, kd), (vs, vh, vd) = k_new.stride(), v_new.stride()
     if T and (kd != 1 or vd != 1 or (H_kv > 1 and (kh != D or vh != D))):
         raise ValueError("the heads of k_new and v_new must be contiguous")
@@ -500,7 +507,7 @@ def append_paged_kv_bs(pages, scales, k_new, v_new, append_indptr, page_table_in
             and append_indptr.is_contiguous() and page_table_indptr.is_contiguous()
             and vals.is_contiguous() and length_info.is_contiguous()):
         _refuse(dev, pages, scales, k_new, v_new, append_indptr, page_table_indptr, vals, length_info)
-    desc = _PACK_APPEND(T, B, H_kv, D, P, P // sshape[3], DTYPE_CODES[dtype], kv, max_pages,
+    desc = _PACK_APPEND(T, B, H_kv, D, P, P // sshape[3], in_code, kv, max_pages,
                         vals.numel(), ks, vs, 0, 0)
     st = (_lib or lib()).pd_append_paged_kv_bs(
         pages.data_ptr(), scales.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
@@ -549,8 +556,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out=None, k_ou
     (int32 [T]; rotary_mode 1 rotate-half, 2 interleaved; inv_freq None: no rotation).
     k may be None.  q and k may be slices along the heads of a projection's output; q_out and
     k_out default to new tensors and may be q and k.  Returns (q_out, k_out)."""
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q and k must be [T, heads, D]")
     T, H_q, D = q.shape
-    dtype, dev = q.dtype, _device(q)
+    dtype, dev = q.dtype, q.get_device()
+    code = DTYPE_CODES.get(dtype)
+    if code is None:
+        raise ValueError("q must be float32, float16 or bfloat16")
     if q_out is None:
         q_out = torch.empty((T, H_q, D), dtype=dtype, device=q.device)
     qs, qh = _heads(q, T, H_q, D, dtype, dev, "q")
@@ -571,23 +583,26 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out=None, k_ou
                 raise ValueError("the weights must be [D], of one dtype")
             _refuse(dev, w)
     if q_weight is not None:
-        qw_at, wdt = q_weight.data_ptr(), DTYPE_CODES[q_weight.dtype]
+        qw_at, wdt = q_weight.data_ptr(), DTYPE_CODES.get(q_weight.dtype)
     if k_weight is not None:
         if q_weight is not None and k_weight.dtype != q_weight.dtype:
             raise ValueError("the weights must be [D], of one dtype")
-        kw_at, wdt = k_weight.data_ptr(), DTYPE_CODES[k_weight.dtype]
+        kw_at, wdt = k_weight.data_ptr(), DTYPE_CODES.get(k_weight.dtype)
+    if wdt is None:
+        raise ValueError("the weights must be float32, float16 or bfloat16")
     rd = 0
     if inv_freq is not None and rotary_mode:
         if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be float64 [rotary_dim / 2]")
-        if positions.dtype != _I32 or positions.shape != (T,):
+        if positions is None or positions.dtype != _I32 or positions.shape != (T,):
             raise ValueError("positions must be int32 [T]")
         if not (positions.get_device() == inv_freq.get_device() == dev
                 and positions.is_contiguous() and inv_freq.is_contiguous()):
             _refuse(dev, positions, inv_freq)
         rd = 2 * inv_freq.numel()
         pos_at, freq_at = positions.data_ptr(), inv_freq.data_ptr()
-    desc = _PACK_QK(T, H_q, H_k, D, DTYPE_CODES[dtype], wdt, rotary_mode, rd, eps, weight_offset,
+    _device(q)
+    desc = _PACK_QK(T, H_q, H_k, D, code, wdt, rotary_mode, rd, eps, weight_offset,
                     attention_factor, qs, ks, qh, kh, qos, kos, qoh, koh)
     st = (_lib or lib()).pd_qk_norm_rope(
         q.data_ptr(), k_at, qw_at, kw_at, pos_at, freq_at, q_out.data_ptr(), ko_at, desc,

@@ -89,3 +89,30 @@ def test_append_takes_the_heads_that_its_grid_holds():
         assert status(H) == "PD_ERR_INVALID_ARG"
     for H in (131071, 150000, 200000, 200001, (1 << 30) - 1):
         assert status(H) == "PD_ERR_UNSUPPORTED"
+
+
+def _qk_args():
+    q = torch.zeros(5, 4, 64)
+    return dict(q=q, k=q, q_weight=torch.ones(64), k_weight=torch.ones(64),
+                positions=torch.zeros(5, dtype=torch.int32), inv_freq=torch.ones(32, dtype=torch.float64))
+
+
+@pytest.mark.parametrize("call,args,bad", [
+    (pd.batch_decode_paged_kv_bs, _decode_args, dict(Q=torch.zeros(2, 4, 64, dtype=torch.float64))),
+    (pd.batch_decode_paged_kv_bs, _decode_args, dict(Q=torch.zeros(2, 4, 64, dtype=torch.int32))),
+    (pd.batch_decode_paged_kv_bs, _decode_args, dict(output=torch.zeros(2, 4, 64, dtype=torch.float64))),
+    (pd.append_paged_kv_bs, _append_args, dict(k_new=torch.zeros(5, 2, 64).double(), v_new=torch.zeros(5, 2, 64).double())),
+    (pd.append_paged_kv_bs, _append_args, dict(page_table_values=None)),
+    (pd.qk_norm_rope, _qk_args, dict(q=torch.zeros(5, 4, 64).double(), k=None)),
+    (pd.qk_norm_rope, _qk_args, dict(q_weight=torch.ones(64).double(), k_weight=None)),
+    (pd.qk_norm_rope, _qk_args, dict(q_weight=None, k_weight=torch.ones(64).int())),
+    (pd.qk_norm_rope, _qk_args, dict(positions=None)),
+    (pd.qk_norm_rope, _qk_args, dict(k=torch.zeros(64))),
+    (pd.qk_norm_rope, _qk_args, dict(q=torch.zeros(4, 64))),
+])
+def test_types_and_missing_arguments_are_refused_as_such(call, args, bad):
+    """A ValueError that names the argument, before the device is looked at."""
+    with pytest.raises(ValueError) as e:
+        call(**{**args(), **bad})
+    assert any(name in str(e.value) for name in bad) or "weights" in str(e.value)
+    assert "current GPU" not in str(e.value)
