@@ -549,13 +549,25 @@ def _heads(t, T, H, D, dtype, dev, what, written=False):
     return a, b
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor for work on `stream`: memory of the current stream's, freed but still in use there,
+    is not taken for another."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        # (handles up to 2 name the default streams)
+        stream = torch.cuda.ExternalStream(stream, device) if stream > 2 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out=None, k_out=None, *,
                  rotary_mode=1, eps=1e-6, weight_offset=0.0, attention_factor=1.0, stream=None):
     """pd_qk_norm_rope: RMS norm of each head of q [T, H_q, D] and k [T, H_k, D] (weights [D],
     or None: no norm), then the rotation of the first 2 * len(inv_freq) dims at positions
     (int32 [T]; rotary_mode 1 rotate-half, 2 interleaved; inv_freq None: no rotation).
     k may be None.  q and k may be slices along the heads of a projection's output; q_out and
-    k_out default to new tensors and may be q and k.  Returns (q_out, k_out)."""
+    k_out default to new tensors (of `stream`'s memory) and may be q and k.  Returns (q_out, k_out)."""
     if q.dim() != 3 or (k is not None and k.dim() != 3):
         raise ValueError("q and k must be [T, heads, D]")
     T, H_q, D = q.shape
@@ -564,7 +576,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out=None, k_ou
     if code is None:
         raise ValueError("q must be float32, float16 or bfloat16")
     if q_out is None:
-        q_out = torch.empty((T, H_q, D), dtype=dtype, device=q.device)
+        q_out = _new((T, H_q, D), dtype, q.device, stream)
     qs, qh = _heads(q, T, H_q, D, dtype, dev, "q")
     qos, qoh = _heads(q_out, T, H_q, D, dtype, dev, "q_out", True)
     H_k = ks = kh = kos = koh = 0
@@ -572,7 +584,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out=None, k_ou
     if k is not None:
         H_k = k.shape[1]
         if k_out is None:
-            k_out = torch.empty((T, H_k, D), dtype=dtype, device=k.device)
+            k_out = _new((T, H_k, D), dtype, k.device, stream)
         ks, kh = _heads(k, T, H_k, D, dtype, dev, "k")
         kos, koh = _heads(k_out, T, H_k, D, dtype, dev, "k_out", True)
         k_at, ko_at = k.data_ptr(), k_out.data_ptr()
