@@ -771,7 +771,8 @@ __device__ void merge_segment(const DecodeParams& p, const BlockRange& br, const
     if (v < hcount * D4) {
       const int j = v / D4, d4 = v - j * D4;
       const int hq = hq0 + j;
-      const bool empty = !(s_M[j] > kEmptyM);
+      // (states that are all NaN or empty leave the maximum at kEmptyM)
+      const bool empty = !(s_M[j] > kEmptyM) && !(p.scales && s_den[j] != s_den[j]);
       const SinkAdj sa = p.sink ? apply_sink(p, hq, empty ? kEmptyM : s_M[j] + log2f(s_den[j]))
                                 : SinkAdj{1.f, empty ? kEmptyM : s_M[j] + log2f(s_den[j])};
       const float sc = empty ? 0.f : p.out_scale / s_den[j] * sa.scale;
@@ -815,7 +816,10 @@ __device__ void finish_share(const DecodeParams& p, const BlockRange& br, const 
       den += sm_d[s * 8 + j] * a;
       num += sm_o[(s * 8 + j) * D + d] * a;
     }
-    const bool empty = !(den > 0.f);
+    // Block scales: a NaN one, which the append writes for a block that received a non-finite row,
+    // makes den NaN, and the output with it.  Caches without keep a NaN row's output empty, as their
+    // tensor-core kernel does.
+    const bool empty = p.scales ? den == 0.f : !(den > 0.f);
     const float o = empty ? 0.f : num / den;
     const float l = empty ? kEmptyM : M + log2f(den);
     const int hq = hq0 + j;

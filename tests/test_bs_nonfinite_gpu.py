@@ -1,0 +1,92 @@
+"""What non-finite scales, and weights far below the largest, do to batch_decode_paged_kv_bs."""
+import pytest
+import torch
+
+from tests._bs import DT, KV, check_decode, decode_ref
+
+pd = pytest.importorskip("paged_kv_decode_19_gb300")
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+NAN = float("nan")
+# (D, type of Q, P, S, query tokens): SIMT by head dim and by Q, boxes, gathered rows
+SIMT = [(256, "bf16", 16, 16, 1), (128, "f32", 16, 8, 1), (64, "f32", 20, 5, 1), (256, "f32", 32, 32, 1)]
+MMA = [(128, "bf16", 16, 16, 1), (64, "f16", 32, 16, 1), (128, "f16", 8, 8, 1), (64, "bf16", 20, 5, 1),
+       (128, "bf16", 16, 16, 3), (64, "f16", 16, 8, 2)]
+
+
+def _case(D, dt, P, S, n, lengths, kv="int8", seed=0, Hq=4, H=2):
+    """Random codes in (0, 100], scales 0.02 and a positive Q: every score is positive."""
+    g = torch.Generator().manual_seed(seed)
+    counts = [-(-L // P) for L in lengths]
+    indptr = [0]
+    for c in counts:
+        indptr.append(indptr[-1] + c)
+    vals = torch.randperm(indptr[-1] + 2, generator=g)[: indptr[-1]]
+    codes = torch.randint(1, 101, (indptr[-1] + 2, 2, H, P, D), generator=g).to(torch.int8)
+    if kv == "e4m3":
+        codes = codes.float().to(torch.float8_e4m3fn).view(torch.int8)
+    Q = (0.5 + torch.rand(len(lengths), n, Hq, D, generator=g)).to(DT[dt])
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
+    return dict(Q=Q.to(DEV), codes=codes.to(DEV), scales=torch.full((indptr[-1] + 2, 2, H, P // S), 0.02, device=DEV),
+                indptr=t(indptr), vals=vals.to(torch.int32).to(DEV), lengths=lengths, P=P, S=S, kv=kv, n=n, D=D,
+                li=t([L - (c - 1) * P if c else 0 for L, c in zip(lengths, counts)]))
+
+
+def _at(c, b, row):
+    """(page, block) of a sequence's row."""
+    return int(c["vals"][int(c["indptr"][b]) + row // c["P"]]), row % c["P"] // c["S"]
+
+
+def _run(c, **kw):
+    Q = c["Q"] if c["n"] > 1 else c["Q"][:, 0].contiguous()
+    out = torch.full(Q.shape, 7.0, dtype=torch.float32, device=DEV)
+    lse = torch.full(Q.shape[:-1], 7.0, device=DEV)
+    pd.batch_decode_paged_kv_bs(Q, c["codes"].view(KV[c["kv"]]), c["scales"], c["indptr"], c["vals"], c["li"], out,
+                                lse, **kw)
+    assert pd.check_device_errors() == "PD_OK"
+    return out.view(c["Q"].shape), lse.view(c["Q"].shape[:-1])
+
+
+def _ref(c, **kw):
+    return decode_ref(c["Q"], c["codes"], c["scales"], c["kv"], c["indptr"], c["vals"], c["lengths"], c["P"],
+                      c["D"] ** -0.5, **kw)
+
+
+def _others_stand(c, out, lse, touched, f16_weights, sink=None):
+    """Heads outside `touched` ([B, n, Hq] bool) are what they are without the bad scale."""
+    d = dict(c, scales=torch.nan_to_num(c["scales"], 0.02, 0.02, 0.02))
+    o, l, (A, vmax, S) = _ref(d, sink=sink)
+    keep = ~touched
+    check_decode(out[keep], lse[keep], (o[keep], l[keep], (A[keep], vmax[keep], S[keep])), max(c["lengths"]),
+                 f16_weights=f16_weights)
+
+
+@pytest.mark.parametrize("shape", SIMT + MMA)
+@pytest.mark.parametrize("splits", [0, 1, 4])
+@pytest.mark.parametrize("side", [0, 1])
+def test_a_nan_scale_reaches_what_attends_it(shape, splits, side):
+    """And nothing else, on either kernel, whole or split."""
+    c = _case(*shape, [40, 700, 3], seed=1)
+    page, blk = _at(c, 1, 300)
+    c["scales"][page, side, 0, blk] = NAN
+    out, lse = _run(c, num_splits=splits)
+    touched = torch.zeros(3, c["n"], 4, dtype=torch.bool, device=DEV)
+    touched[1, :, :2] = True  # KV head 0 serves query heads 0 and 1
+    assert torch.isnan(out[touched]).all()
+    if side == 0:
+        assert torch.isnan(lse[touched]).all()
+    _others_stand(c, out, lse, touched, pd.last_decode_variant() == "mma")
+
+
+@pytest.mark.parametrize("shape", SIMT)
+@pytest.mark.parametrize("splits", [1, 7])
+def test_nothing_but_nan_is_not_nothing(shape, splits):
+    """Every K scale of a sequence NaN: its states are NaN, not empty."""
+    c = _case(*shape, [500, 20], seed=5)
+    page = c["vals"][int(c["indptr"][0]):int(c["indptr"][1])].long()
+    c["scales"][page, 0, 1] = NAN
+    out, lse = _run(c, num_splits=splits)
+    touched = torch.zeros(2, 1, 4, dtype=torch.bool, device=DEV)
+    touched[0, :, 2:] = True
+    assert torch.isnan(out[touched]).all() and torch.isnan(lse[touched]).all()
+    _others_stand(c, out, lse, touched, False)
