@@ -52,6 +52,10 @@ __device__ __forceinline__ float to_f32(F8 x) {
 
 __device__ __forceinline__ float to_f32(I8 x) { return (float)x.v; }
 
+// x, and NaN for an infinite x: a block's scale as the decodes use it, so that a row under an
+// infinite one is not taken for a row without weight (a score of -inf).
+__device__ __forceinline__ float nan_if_inf(float x) { return fmaf(x, 0.f, x); }
+
 // f32 -> one e4m3 code, round to nearest even, saturating to +-448.
 __device__ __forceinline__ uint8_t f32_to_e4m3(float x) {
   uint16_t r;

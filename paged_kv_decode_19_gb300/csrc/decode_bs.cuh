@@ -502,18 +502,20 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
     float t0 = -INFINITY, t1 = -INFINITY, u0 = -INFINITY, u1 = -INFINITY;  // maxima of s, s + log2 vs
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      float ka = meta[i].x, kb = meta[i].x;
+      float ka, kb;
       bool full;
       unsigned rows;  // bit r: row r counts
       if constexpr (ROWS) {
         const float2 sa = s_rowsc[warp][cst][16 * i + kr], sb = s_rowsc[warp][cst][16 * i + kr + 8];
-        ka = sa.x;
-        kb = sb.x;
-        vsc[i] = make_float2(sa.y, sb.y);
+        ka = nan_if_inf(sa.x);
+        kb = nan_if_inf(sb.x);
+        vsc[i] = make_float2(nan_if_inf(sa.y), nan_if_inf(sb.y));
         rows = (s_rowok[warp][cst][i >> 1] >> (16 * (i & 1))) & 0xffffu;
         full = rows == 0xffffu;
       } else {
-        vsc[i] = make_float2(meta[i].y, meta[i].y);
+        ka = kb = nan_if_inf(meta[i].x);
+        const float vs = nan_if_inf(meta[i].y);
+        vsc[i] = make_float2(vs, vs);
         const int span = __float_as_int(meta[i].z);
         full = span == (16 << 8);
         rows = ((1u << (span >> 8)) - 1) & ~((1u << (span & 0xff)) - 1);

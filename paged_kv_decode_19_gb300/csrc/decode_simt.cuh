@@ -401,7 +401,10 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_simt_kernel(const __grid_co
         for (int k = 1; k < LPR; k <<= 1) sc[j] += __shfl_xor_sync(0xffffffffu, sc[j], k);
       float2 row_sc = make_float2(1.f, 1.f);
       if constexpr (BS) {
-        if (off >= 0) row_sc = s_sc[buf][warp][trow];
+        if (off >= 0) {
+          row_sc = s_sc[buf][warp][trow];
+          row_sc = make_float2(nan_if_inf(row_sc.x), nan_if_inf(row_sc.y));
+        }
 #pragma unroll
         for (int j = 0; j < HM; ++j) sc[j] *= row_sc.x;
       }

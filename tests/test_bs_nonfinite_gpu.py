@@ -7,7 +7,7 @@ from tests._bs import DT, KV, check_decode, decode_ref
 pd = pytest.importorskip("paged_kv_decode_19_gb300")
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-NAN = float("nan")
+NAN, INF = float("nan"), float("inf")
 # (D, type of Q, P, S, query tokens): SIMT by head dim and by Q, boxes, gathered rows
 SIMT = [(256, "bf16", 16, 16, 1), (128, "f32", 16, 8, 1), (64, "f32", 20, 5, 1), (256, "f32", 32, 32, 1)]
 MMA = [(128, "bf16", 16, 16, 1), (64, "f16", 32, 16, 1), (128, "f16", 8, 8, 1), (64, "bf16", 20, 5, 1),
@@ -90,3 +90,35 @@ def test_nothing_but_nan_is_not_nothing(shape, splits):
     touched[0, :, 2:] = True
     assert torch.isnan(out[touched]).all() and torch.isnan(lse[touched]).all()
     _others_stand(c, out, lse, touched, False)
+
+
+@pytest.mark.parametrize("shape", SIMT + MMA)
+@pytest.mark.parametrize("splits", [0, 1, 4])
+@pytest.mark.parametrize("side", [0, 1])
+def test_an_infinite_scale_reaches_what_attends_it(shape, splits, side):
+    c = _case(*shape, [40, 700, 3], seed=1)
+    page, blk = _at(c, 1, 300)
+    c["scales"][page, side, 0, blk] = INF
+    out, lse = _run(c, num_splits=splits)
+    touched = torch.zeros(3, c["n"], 4, dtype=torch.bool, device=DEV)
+    touched[1, :, :2] = True
+    assert torch.isnan(out[touched]).all()
+    if side == 0:
+        assert torch.isnan(lse[touched]).all()
+    _others_stand(c, out, lse, touched, pd.last_decode_variant() == "mma")
+
+
+@pytest.mark.parametrize("shape", SIMT + MMA)
+@pytest.mark.parametrize("length,splits", [(16, 0), (400, 0), (400, 1), (400, 5)])
+def test_an_infinite_key_scale_with_scores_of_one_sign(shape, length, splits):
+    """Scores of -inf alone would look like rows that do not count."""
+    c = _case(*shape, [length, 50], seed=2)
+    c["Q"] = -c["Q"]
+    for row in range(0, length, c["S"]):
+        page, blk = _at(c, 0, row)
+        c["scales"][page, 0, 1, blk] = INF
+    out, lse = _run(c, num_splits=splits)
+    touched = torch.zeros(2, c["n"], 4, dtype=torch.bool, device=DEV)
+    touched[0, :, 2:] = True
+    assert not torch.isfinite(out[touched]).any() and not torch.isfinite(lse[touched]).any()
+    _others_stand(c, out, lse, touched, pd.last_decode_variant() == "mma")
