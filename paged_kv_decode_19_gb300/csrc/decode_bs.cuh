@@ -43,6 +43,7 @@
 
 #include <cuda.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "decode_mma.cuh"
@@ -130,6 +131,13 @@ __device__ __forceinline__ int tile_row(int g) { return (g & 6) ^ ((g & 1) * 5);
 template <int D>
 __device__ __forceinline__ int tile_off(int r, int x) {
   return r * D + (x ^ (D == 128 ? (r & 7) << 4 : ((r >> 1) & 3) << 4));
+}
+
+// The smaller of two, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 // four codes -> two f16x2 (codes 0, 1 and 2, 3), exact
@@ -573,9 +581,10 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
         oacc[mt][3] *= a1;
       }
     }
-    // weights of P.V: 2^(s - n) vs = p 2^(m - n) vs (the exponent is capped so that a zero
-    // scale stays zero); of several queries one that does not attend a row weighs it 0
-    // whatever the scale
+    // weights of P.V: 2^(s - n) vs = p 2^(m - n) vs (the exponent is capped so that a zero scale
+    // stays zero, and 2^(m - n) vs at the largest float so that a p of zero gives zero: it is above
+    // that only where p is under 2^-119); of several queries one that does not attend a row weighs
+    // it 0 whatever the scale
     const float g0 = fast_exp2(fminf(st_m[0] - st_n[0], 126.f)), g1 = fast_exp2(fminf(st_m[1] - st_n[1], 126.f));
     uint32_t pb[NQ][2];
 #pragma unroll
@@ -589,7 +598,7 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
       st_d[1] += pr[1] + pr[3];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float w = pr[e] * ((e & 1 ? g1 : g0) * (e < 2 ? vsc[i].x : vsc[i].y));
+        const float w = pr[e] * min_nan((e & 1 ? g1 : g0) * (e < 2 ? vsc[i].x : vsc[i].y), FLT_MAX);
         pr[e] = (MQ || ROWS) && pr[e] == 0.f ? 0.f : w;
       }
       // P^T as a B fragment: fragment rows 2q, 2q + 1 | 2q + 8, 2q + 9 of column g_id

@@ -122,3 +122,23 @@ def test_an_infinite_key_scale_with_scores_of_one_sign(shape, length, splits):
     touched[0, :, 2:] = True
     assert not torch.isfinite(out[touched]).any() and not torch.isfinite(lse[touched]).any()
     _others_stand(c, out, lse, touched, pd.last_decode_variant() == "mma")
+
+
+@pytest.mark.parametrize("shape", SIMT + MMA)
+@pytest.mark.parametrize("top", [0.0, 2.0 ** -126, 2.0 ** -100])
+@pytest.mark.parametrize("rest", [1.0, 4.0, 1e4, 1e30])
+def test_finite_scales_give_finite_outputs(shape, top, rest):
+    """The rows of by far the largest weight hold zeros under a tiny scale, the others, whose
+    weights underflow, large values: 0 * anything finite is 0."""
+    c = _case(*shape, [80], seed=4)
+    page, blk = _at(c, 0, 0)
+    c["scales"][:, 1] = rest
+    c["scales"][page, 0, :, blk] = 4.0
+    c["scales"][page, 1, :, blk] = top
+    c["codes"][page, 1, :, blk * c["S"]:(blk + 1) * c["S"]] = 0
+    out, lse = _run(c, num_splits=1)
+    ref = _ref(c)
+    # the first block's scores lead by thousands in log2 units: 1e30 * 100 * 2^-1000 counts as 0
+    assert torch.isfinite(out).all() and (out.double() - ref[0]).abs().max() <= 1e-30
+    # a score is off by at most 24 roundings of 2^-24 of its sum of magnitudes, here itself
+    assert ((lse.double() - ref[1]).abs() <= 2.0 ** -19 * ref[1].abs() + 1e-6).all()
