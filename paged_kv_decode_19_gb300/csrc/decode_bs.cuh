@@ -583,8 +583,9 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
     }
     // weights of P.V: 2^(s - n) vs = p 2^(m - n) vs (the exponent is capped so that a zero scale
     // stays zero, and 2^(m - n) vs at the largest float so that a p of zero gives zero: it is above
-    // that only where p is under 2^-119); of several queries one that does not attend a row weighs
-    // it 0 whatever the scale
+    // that only where p is under 2^-119).  Of several queries one that does not attend a row weighs
+    // it 0 whatever the scale; a weight of an attended row that underflowed still takes a NaN scale.
+    // (ROWS: a row that does not count has scales of 0.)
     const float g0 = fast_exp2(fminf(st_m[0] - st_n[0], 126.f)), g1 = fast_exp2(fminf(st_m[1] - st_n[1], 126.f));
     uint32_t pb[NQ][2];
 #pragma unroll
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float w = pr[e] * min_nan((e & 1 ? g1 : g0) * (e < 2 ? vsc[i].x : vsc[i].y), FLT_MAX);
-        pr[e] = (MQ || ROWS) && pr[e] == 0.f ? 0.f : w;
+        pr[e] = MQ && sc[i][e] == -INFINITY ? 0.f : w;
       }
       // P^T as a B fragment: fragment rows 2q, 2q + 1 | 2q + 8, 2q + 9 of column g_id
       const uint32_t x0 = pack2<__half>(pr[0], pr[2]);  // column 2q: rows of g_id, g_id + 8

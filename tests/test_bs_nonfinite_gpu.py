@@ -142,3 +142,40 @@ def test_finite_scales_give_finite_outputs(shape, top, rest):
     assert torch.isfinite(out).all() and (out.double() - ref[0]).abs().max() <= 1e-30
     # a score is off by at most 24 roundings of 2^-24 of its sum of magnitudes, here itself
     assert ((lse.double() - ref[1]).abs() <= 2.0 ** -19 * ref[1].abs() + 1e-6).all()
+
+
+@pytest.mark.parametrize("shape", SIMT + MMA)
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_a_bad_value_scale_under_a_weight_of_zero(shape, splits, bad):
+    """A peaked softmax: the block's weights underflow, its values are still attended."""
+    c = _case(*shape, [200, 60], seed=3)
+    page, blk = _at(c, 0, 0)
+    c["scales"][page, 0, 0, blk] = 4.0  # scores of the first block hundreds above the others'
+    page, blk = _at(c, 0, 100)
+    c["scales"][page, 1, 0, blk] = bad
+    out, lse = _run(c, num_splits=splits)
+    touched = torch.zeros(2, c["n"], 4, dtype=torch.bool, device=DEV)
+    touched[0, :, :2] = True
+    assert not torch.isfinite(out[touched]).any() and torch.isfinite(lse).all()
+    _others_stand(c, out, lse, touched, pd.last_decode_variant() == "mma")
+
+
+@pytest.mark.parametrize("shape", [x for x in MMA if x[-1] > 1])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_a_bad_value_scale_stays_from_earlier_tokens(shape, bad):
+    """Of several queries those whose limit lies before the block are untouched, whatever the others
+    weigh it with."""
+    n, S = shape[-1], shape[3]
+    L = 4 * S + 1  # the last row opens a block that the last token alone attends
+    for lead in (0.02, 4.0):
+        c = _case(*shape, [L], seed=6)
+        page, blk = _at(c, 0, 0)
+        c["scales"][page, 0, 0, blk] = lead
+        page, blk = _at(c, 0, L - 1)
+        c["scales"][page, 1, 0, blk] = bad
+        out, lse = _run(c)
+        touched = torch.zeros(1, n, 4, dtype=torch.bool, device=DEV)
+        touched[0, -1, :2] = True
+        assert not torch.isfinite(out[touched]).any()
+        _others_stand(c, out, lse, touched, True)
