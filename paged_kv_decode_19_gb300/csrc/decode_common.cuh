@@ -114,7 +114,7 @@ __device__ __forceinline__ SinkAdj apply_sink(const DecodeParams& p, int h, floa
   if (!p.sink) return {1.f, l};
   const float ls = __ldg(p.sink + h) * 1.4426950408889634f;
   const float m = fmaxf(l, ls);
-  const float a = l > kEmptyM ? exp2f(l - m) : 0.f;  // weight of the attended rows
+  const float a = l <= kEmptyM ? 0.f : exp2f(l - m);  // weight of the attended rows (NaN: NaN)
   const float den = a + exp2f(ls - m);
   return {a / den, m + log2f(den)};
 }

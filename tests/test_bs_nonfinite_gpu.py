@@ -179,3 +179,21 @@ def test_a_bad_value_scale_stays_from_earlier_tokens(shape, bad):
         touched[0, -1, :2] = True
         assert not torch.isfinite(out[touched]).any()
         _others_stand(c, out, lse, touched, True)
+
+
+@pytest.mark.parametrize("shape", SIMT + MMA)
+@pytest.mark.parametrize("splits", [0, 1, 4])
+@pytest.mark.parametrize("side", [0, 1])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_a_bad_scale_with_a_learned_sink(shape, splits, side, bad):
+    """The sink's weight joins a NaN denominator: lse is NaN beside the output."""
+    c = _case(*shape, [40, 700, 3], seed=1)
+    page, blk = _at(c, 1, 300)
+    c["scales"][page, side, 0, blk] = bad
+    sink = torch.tensor([0.0, 3.0, 60.0, -2.0], device=DEV)
+    out, lse = _run(c, num_splits=splits, sink=sink)
+    touched = torch.zeros(3, c["n"], 4, dtype=torch.bool, device=DEV)
+    touched[1, :, :2] = True
+    assert torch.isnan(out[touched]).all()
+    assert torch.isnan(lse[touched]).all() if side == 0 else torch.isfinite(lse[touched]).all()
+    _others_stand(c, out, lse, touched, pd.last_decode_variant() == "mma", sink)
