@@ -58,7 +58,8 @@ cudaError_t launch_merge_state(void* V, float* S, const void* V_other, const flo
 // merge_states: the merge formula over R partners at once (one warp per (n, h) row): the
 // R log-sum-exps are read by the lanes (r = lane, lane + 32, ...), M and the weight sum
 // come from warp reductions, then each lane accumulates its dims over the R fp32
-// partial rows and writes the output type.  All partners empty: out 0, lse -5e4.
+// partial rows and writes the output type.  All partners empty: out 0, lse -5e4; a NaN
+// partner makes the row NaN.
 template <typename OT, int DPL>
 __global__ void merge_states_kernel(OT* __restrict__ out, float* __restrict__ S_out,
                                     const float* __restrict__ Vp, const float* __restrict__ Sp,
@@ -79,9 +80,16 @@ __global__ void merge_states_kernel(OT* __restrict__ out, float* __restrict__ S_
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   OT* o = out + (size_t)row * D;
-  if (!(M > kEmptyM)) {
-    for (int d = lane; d < D; d += 32) o[d] = from_f32<OT>(0.f);
-    if (lane == 0) S_out[row] = kEmptyM;
+  if (!(M > kEmptyM)) {  // every partner empty, or NaN (which the maximum passes over)
+    bool nan = s_lane != s_lane;
+    for (int r = lane + 32; r < R; r += 32) {
+      const float s = Sp[r * sstride + row];
+      nan = nan || s != s;
+    }
+    nan = __any_sync(0xffffffffu, nan);
+    const float none = nan ? __int_as_float(0x7fc00000) : 0.f;
+    for (int d = lane; d < D; d += 32) o[d] = from_f32<OT>(none);
+    if (lane == 0) S_out[row] = nan ? none : kEmptyM;
     return;
   }
   // the partners' weights 2^(S_r - M), each computed once: lane r's for r < 32

@@ -197,3 +197,19 @@ def test_a_bad_scale_with_a_learned_sink(shape, splits, side, bad):
     assert torch.isnan(out[touched]).all()
     assert torch.isnan(lse[touched]).all() if side == 0 else torch.isfinite(lse[touched]).all()
     _others_stand(c, out, lse, touched, pd.last_decode_variant() == "mma", sink)
+
+
+def test_merge_states_keeps_a_nan():
+    """Partials of a decode split over ranks: one that is NaN shows, also beside empty ones only."""
+    D = 64
+    for R in (2, 5, 40):
+        V, S = torch.zeros(R, 3, 2, D, device=DEV), torch.full((R, 3, 2), -5e4, device=DEV)
+        S[R - 1, 0, 0], V[R - 1, 0, 0] = NAN, NAN      # among empty partners
+        S[R - 1, 1, 0], V[R - 1, 1, 0] = NAN, NAN      # beside one with rows
+        S[0, 1, 0], V[0, 1, 0] = 2.0, 1.0
+        S[0, 2, 1], V[0, 2, 1] = 3.0, 0.5
+        out, lse = torch.empty(3, 2, D, device=DEV), torch.empty(3, 2, device=DEV)
+        pd.merge_states(out, lse, V, S)
+        assert torch.isnan(out[:2, 0]).all() and torch.isnan(lse[:2, 0]).all()
+        assert (out[2, 1] == 0.5).all() and lse[2, 1] == 3.0
+        assert (out[:, 1][:2] == 0).all() and (lse[:, 1][:2] == -5e4).all() and (out[2, 0] == 0).all()
