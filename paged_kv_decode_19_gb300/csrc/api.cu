@@ -12,6 +12,7 @@
 #include <string>
 
 #include "arena.h"
+#include "bs_plan.h"
 #include "kernels.h"
 #include "pageddecode.h"
 
@@ -304,13 +305,12 @@ static bool fill_host_plan(const pd_decode_desc& d, DecodeParams& p) {
   return true;
 }
 
+// Slices of a KV head's columns whose warps walk the same pages side by side in one block.
+static int slices_side_by_side(int n_z) { return n_z == 2 || n_z == 4 ? n_z : 1; }
+
 // Block-scaled cache with host copies of the table: whether one block per (sequence, KV head)
-// beats equal shares of all pages.  A segment within a block is merged in shared memory; one
-// that crosses blocks costs about as much as kCrossTiles tiles of a warp more (a fence, an atomic
-// and two trips to L2: 64 rows alone took 6.8 us in one block and 11.9 us across four).  So the
-// longest segment's share of a warp may be that much larger than the equal share; all segments
-// must be resident at once, with a slice per KV head.
-constexpr int kCrossTiles = 10;
+// beats equal shares of all pages.  The longest segment's share of a warp may be kCrossTiles larger
+// than the equal share; all segments must be resident at once, with a slice per KV head.
 static bool block_per_segment(const pd_decode_desc& d, int n_z, int wave) {
   if (n_z != 1 || (long long)d.B * d.H_kv > wave) return false;
   const int B = d.B;
@@ -543,12 +543,10 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
         grid_blocks = d.B * d.H_kv;
         ws_need = 0;
       }
-    } else if ((long long)d.B * d.H_kv < grid_blocks &&
-               d.nnz_pages * d.page_size / 16 / d.B / kMmaWarps <=
-                   d.nnz_pages * d.page_size / 16 * d.H_kv / ((long long)wave * kMmaWarps) + kCrossTiles) {
-      // without: as many equal shares as segments, by the mean length alone (even sequences then
-      // fall on block borders, and uneven ones are still shared equally)
-      grid_blocks = d.B * d.H_kv;
+    } else {
+      const int n_z = (d.H_qo / d.H_kv * q_len + kMaxGroupPerCta - 1) / kMaxGroupPerCta;
+      grid_blocks = bs_device_grid(d.B, d.H_kv, n_z, slices_side_by_side(n_z), d.nnz_pages * d.page_size / 16, wave,
+                                   kMmaWarps, grid_blocks);
     }
   }
 
@@ -632,7 +630,7 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   p.n_z = n_z;
   // two or four slices of a KV head's query columns: their warps walk the same pages
   // side by side in one block, so the pages come from HBM once
-  p.zg = use_mma && mode == kSchedBalanced && (n_z == 2 || n_z == 4) ? n_z : 1;
+  p.zg = use_mma && mode == kSchedBalanced ? slices_side_by_side(n_z) : 1;
   p.q_len = q_len;
   p.ncol = ncol;
   p.precise = d.kv_dtype == kF32 ? 1 : 0;

@@ -1,6 +1,8 @@
 """Refusals of the block-scaled cache's calls, and of what they share with the other decodes, that
 need no GPU."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -116,3 +118,15 @@ def test_types_and_missing_arguments_are_refused_as_such(call, args, bad):
         call(**{**args(), **bad})
     assert any(name in str(e.value) for name in bad) or "weights" in str(e.value)
     assert "current GPU" not in str(e.value)
+
+
+def test_device_planned_grid(tmp_path):
+    """Blocks of a short batch planned on the device, for any number of column slices."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = tmp_path / "bs_plan_check"
+    subprocess.check_call(["g++", "-std=c++17", "-Wall", "-Werror", "-I",
+                           os.path.join(root, "paged_kv_decode_19_gb300", "csrc"),
+                           os.path.join(root, "tests", "c", "bs_plan_check.cpp"), "-o", str(exe)])
+    out = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert out.returncode == 0, out.stdout
+    assert out.stdout.strip() == "block-scaled plan ok"
