@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(NW * 32, kBsBlocks)
     return reinterpret_cast<float*>(side ? rings + w * NST * T::kStage : rings + NW * NST * T::kStage + w * T::kState);
   };
   if (threadIdx.x == 0) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm) : "memory");
+    if constexpr (!ROWS) asm volatile("prefetch.tensormap [%0];" ::"l"(&tm) : "memory");  // (ROWS: none)
     prefetch_l2_share(p.Q, (size_t)p.B * p.q_len * p.H_qo * D * sizeof(QT), blockIdx.x, gridDim.x);
     if (p.values) prefetch_l2_share(p.values, (size_t)p.nnz_pages * sizeof(int32_t), blockIdx.x, gridDim.x);
   }
