@@ -69,7 +69,7 @@ def _dist():
 _TRAFFIC_EXCLUDE = ("decode_simt.cu", "merge_append.cu", "decode_noalloc.cu", "arena.h",
                     "decode_simt.cuh", "decode_simt_bs.cu", "decode_bs.cuh", "decode_bs_e4m3.cu",
                     "decode_bs_int.cu", "decode_bs_rows_e4m3.cu", "decode_bs_rows_int.cu",
-                    "append_bs.cu", "qk_norm_rope.cu")
+                    "append_bs.cu", "qk_norm_rope.cu", "bs_plan.h")
 
 
 def _sources_digest() -> str:

@@ -278,8 +278,8 @@ pd_status pd_batch_decode_paged_kv_mq(const void* Q, const void* pages,
  *          V (1) block of a head stands for code * scales[page, K | V, head, slot / scale_rows].
  * scale_rows divides P; with scale_rows = P a page's head has one scale for K, one for V.
  * Codes of attended rows are numbers (no E4M3 NaN code; the append writes none).  Scales are
- * finite and >= 0; a NaN or infinite one makes the outputs that attend its block non-finite, and
- * nothing else.  The cache holds K as the decode uses it: rotate (and norm)
+ * finite and >= 0; a NaN or infinite one makes the outputs that attend its block NaN (a K scale:
+ * their lse too), and nothing else.  The cache holds K as the decode uses it: rotate (and norm)
  * the new K rows before the append, and Q before the decode, with pd_qk_norm_rope.
  *
  * pd_append_paged_kv_bs — quantises new tokens' K/V into such a cache.
@@ -426,7 +426,7 @@ pd_status pd_merge_state_inplace(void* V, float* S, const void* V_other, const f
  * For every (n, h):  M = max_r S_r;  w_r = 2^(S_r - M);
  *   V_out[n,h,:] = sum_r w_r V_r[n,h,:] / sum_r w_r;  S_out[n,h] = log2(sum_r w_r) + M.
  * If every partner is empty (S_r <= -5e4, the decode's empty-sequence state), V_out = 0
- * and S_out = -5e4.  Arithmetic in fp32.
+ * and S_out = -5e4; a NaN S_r makes its row NaN.  Arithmetic in fp32.
  * Arguments (device pointers):
  *   V_parts  float32 partner outputs; partner r's [N, H, D] rows at V_parts + r * v_rank_stride.
  *   S_parts  float32 partner lse (log2); partner r's [N, H] at S_parts + r * s_rank_stride.

@@ -37,8 +37,8 @@
 //     their own running maximum n of s + log2 vs, so blocks whose scales differ by any
 //     factor keep the same relative precision.  out = O 2^(n - m) / d.
 //   - both maxima are lazy: they move only when exceeded by more than 2^kLazyMaxBs.
-// A non-finite scale makes the outputs that attend the block non-finite, as a non-finite
-// row of an unquantised cache does; rows outside the attended ranges never count.
+// A NaN or infinite scale makes the outputs that attend the block NaN, whatever the weights;
+// rows outside the attended ranges never count.
 #pragma once
 
 #include <cuda.h>
