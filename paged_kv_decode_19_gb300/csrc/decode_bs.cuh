@@ -13,17 +13,17 @@
 // stage's mbarrier, issued by NQ lanes at once while the other stage is computed.  Eight warps an
 // SM then hold up to 128 KB in flight (the HBM rate times a 1 us latency needs about 45 KB of an
 // SM); more and smaller blocks, or deeper rings in fewer blocks, were slower (256 sequences: 197
-// us with 12 warps of one tile at a time, 184 us now).  The boxes are swizzled (128- or 64-byte
+// us with 12 warps of one tile at a time, 185 us now).  The boxes are swizzled (128- or 64-byte
 // rows) and the fragment rows permuted (tile_row) so that the fragment reads of K and V are free
 // of bank conflicts (D 64: two-way on V).
 //   A warp's time per tile is a chain of dependent steps, so a stage's NQ tiles are computed
 // together: their chains overlap and share the vote, the rescale and the wait (a tile alone in a
 // warp: 0.83 us one by one, 0.42 us now).  Short lists are padded with empty tiles; one copy of the
 // code for full stages only keeps the loop in reach of the instruction cache, whose misses are the
-// largest stall left (int8: 1.0 of 5.2 cycles an instruction; e4m3: 1.4 of 7.0, level with the
+// largest stall left (int8: 1.0 of 5.1 cycles an instruction; e4m3: 1.5 of 6.7, level with the
 // fixed waits between dependent instructions).
 //   Measured on one GB300 (of the 6779 GB/s copy rate): eight contexts of 32K to 128K rows 194 us
-// (96 %; e4m3 in blocks of 64 rows 191 us, 98 %), 256 sequences of 300 to 4200 rows 184 us (92 %),
+// (96 %; e4m3 in blocks of 64 rows 191 us, 98 %), 256 sequences of 300 to 4200 rows 185 us (91 %),
 // 32 of 512 to 4096 rows 34 us (55 %: about 3 us until the first tile, 3 us of uneven ends and 7 us
 // of merging stand beside 18.5 us of bytes), 300 rows alone 7.0 us.
 //
