@@ -555,8 +555,8 @@ def _new(shape, dtype, device, stream):
     if stream is None or device.type != "cuda":
         return torch.empty(shape, dtype=dtype, device=device)
     if not hasattr(stream, "cuda_stream"):
-        # (handles up to 2 name the default streams)
-        stream = torch.cuda.ExternalStream(stream, device) if stream > 2 else torch.cuda.default_stream(device)
+        handle = int(stream)  # (up to 2: the default streams)
+        stream = torch.cuda.ExternalStream(handle, device) if handle > 2 else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 

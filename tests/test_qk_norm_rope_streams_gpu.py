@@ -38,3 +38,21 @@ def test_new_outputs_on_the_default_stream():
         torch.cuda.synchronize()
         check_norm_rope(q, wq, pos, freq, qo)
         check_norm_rope(k, wk, pos, freq, ko)
+
+
+def test_new_outputs_on_a_stream_of_another_kind():
+    """Anything that turns into a handle, as the calls take it."""
+    class Handle:
+        def __init__(self, st):
+            self.st = st
+
+        def __int__(self):
+            return self.st.cuda_stream
+    q, k, wq, wk, pos = _inputs(5, 2, 1, 64, "f16", seed=3)
+    freq = pd.rope_frequencies(64, 1e4, device=DEV)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    qo, ko = pd.qk_norm_rope(q, k, wq, wk, pos, freq, stream=Handle(st))
+    torch.cuda.synchronize()
+    check_norm_rope(q, wq, pos, freq, qo)
+    check_norm_rope(k, wk, pos, freq, ko)
