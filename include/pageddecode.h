@@ -95,7 +95,8 @@ typedef struct {
                                 that joins the softmax as one more score with a zero value
                                 row -- out = sum_r e^(t_r) v_r / (e^sink + sum_r e^(t_r)),
                                 t_r = sm_scale q.k_r, and lse includes it (an empty
-                                sequence gives out = 0, lse = sink * log2(e)) */
+                                sequence gives out = 0, lse = sink * log2(e)); -inf: the
+                                head has none */
   const int32_t* host_indptr;       /* optional HOST copy of page_table_indptr [B+1], or NULL */
   const int32_t* host_length_info;  /* optional HOST copy of length_info ([B] or [3,B]), or NULL.
                                  Both or neither.  When given (and 2(B+1) plus the length_info

@@ -113,6 +113,7 @@ struct SinkAdj {
 __device__ __forceinline__ SinkAdj apply_sink(const DecodeParams& p, int h, float l) {
   if (!p.sink) return {1.f, l};
   const float ls = __ldg(p.sink + h) * 1.4426950408889634f;
+  if (ls == -INFINITY) return {1.f, l};  // (a head without one; of an empty sequence it would be 0 / 0)
   const float m = fmaxf(l, ls);
   const float a = l <= kEmptyM ? 0.f : exp2f(l - m);  // weight of the attended rows (NaN: NaN)
   const float den = a + exp2f(ls - m);
