@@ -48,12 +48,16 @@ typedef enum {
   PD_ERR_BAD_SLOT = 6,      /* device: an append slot lay beyond max_pages*page_size */
   PD_ERR_TIMEOUT = 7,       /* device: a kernel's bounded wait for its own copies ran out; the
                                outputs of that call are not valid */
-  PD_ERR_WORKSPACE = 8      /* caller workspace too small or misaligned */
+  PD_ERR_WORKSPACE = 8,     /* caller workspace too small or misaligned */
+  PD_ERR_NO_PAGES = 9       /* device: a step needed more pages than the pool had free */
 } pd_status;
 
 /* Element types.  PD_E4M3 = OCP float8 e4m3fn (bias 7, max 448, no inf); KV only.
- * PD_I8 = 8-bit integer codes; block-scaled KV only (pd_..._bs). */
-typedef enum { PD_F32 = 0, PD_F16 = 1, PD_BF16 = 2, PD_E4M3 = 3, PD_I8 = 4 } pd_dtype;
+ * PD_I8 = 8-bit integer codes; block-scaled KV only (pd_..._bs).  PD_MX_E4M3, PD_MX_E8M0 = 4-bit
+ * e2m1 codes under e4m3 scales of 16 dims, or power-of-two scales of 32; pd_..._mx only. */
+typedef enum {
+  PD_F32 = 0, PD_F16 = 1, PD_BF16 = 2, PD_E4M3 = 3, PD_I8 = 4, PD_MX_E4M3 = 5, PD_MX_E8M0 = 6
+} pd_dtype;
 
 /*
  * What [TVM] fixes when it builds a decode kernel (head counts, head dim, page
@@ -70,7 +74,8 @@ typedef struct {
                                 E4M3 KV (D 128, 16-bit Q); every other accepted shape
                                 runs on the SIMT kernel (pd_last_decode_variant) */
   int32_t q_dtype;           /* pd_dtype of Q: F32, F16 or BF16 */
-  int32_t kv_dtype;          /* pd_dtype of pages: F32, F16, BF16 or E4M3 (block-scaled: E4M3 or I8) */
+  int32_t kv_dtype;          /* pd_dtype of pages: F32, F16, BF16 or E4M3 (block-scaled: E4M3 or I8;
+                                4-bit: MX_E4M3 or MX_E8M0) */
   int32_t out_dtype;         /* pd_dtype of output: F32, F16 or BF16 */
   int32_t sliding_window;    /* 0: length_info is [B] = last_page_len.
                                 1: length_info is [3,B] = (last_page_len,
@@ -84,8 +89,8 @@ typedef struct {
   int64_t max_pages;         /* pages buffer holds [max_pages,2,H_kv,P,D] */
   int64_t nnz_pages;         /* entries in page_table_values (= indptr[B]) */
   int32_t max_kv_len_hint;   /* reserved (ignored); set to 0 */
-  float k_scale;             /* E4M3 KV only: K = code * k_scale (else ignored) */
-  float v_scale;             /* E4M3 KV only: V = code * v_scale (else ignored) */
+  float k_scale;             /* E4M3 KV and the 4-bit cache only: K = code * k_scale (else ignored) */
+  float v_scale;             /* the same: V = code * v_scale */
   int32_t flags;             /* 0, or PD_DECODE_EARLY_INPUTS | PD_DECODE_K_ROTATED (below) */
   void* workspace;           /* optional caller workspace (device, 256-byte aligned);
                                 NULL = library-managed */
@@ -349,6 +354,111 @@ pd_status pd_batch_decode_paged_kv_bs(const void* Q, const void* pages, const fl
                                       pd_stream_t stream);
 
 /*
+ * 4-bit (microscaled) cache — an addition of this library.
+ *   pages  [max_pages, 2, H_kv, P, D / 2] bytes: row `slot` of a page's K (0) or V (1), two dims a
+ *          byte, the even one in the low half; a code is a sign (bit 3) and a magnitude, one of 0,
+ *          0.5, 1, 1.5, 2, 3, 4, 6 (e2m1);
+ *   scales [max_pages, 2, H_kv, P, D / N] bytes: N = 16, e4m3 (PD_MX_E4M3); N = 32, powers of two
+ *          2^(byte - 127) (PD_MX_E8M0).  A dim stands for  code * scale * k_scale (v_scale).
+ * Both 16-byte aligned.  k_scale and v_scale are finite and positive, the same for every call on a
+ * cache.  A NaN scale makes the outputs that attend its block NaN (K: the head's whole output and lse;
+ * V: the block's dims), and nothing else.  Power-of-two scales lie in [2^-14, 2^13]: below, the
+ * decode takes 0, above, NaN.  The cache holds K as the decode uses it: rotate (and norm) the new K
+ * rows before the append, and Q before the decode, with pd_qk_norm_rope.
+ *
+ * pd_append_paged_kv_mx — quantises new tokens' K/V into their slots.  For each block of N dims of a
+ * row, with y = x / k_scale (v_scale; an IEEE fp32 quotient) and a = max |y|:
+ *   E4M3: scale = RN_e4m3(a / 6), at least 2^-9 and at most 448;
+ *   E8M0: scale = the smallest 2^k, -14 <= k <= 13, with a <= 6 * 2^k (k = 13 if there is none);
+ *   code  = RN_e2m1(y / scale), ties to even, saturating at 6.
+ * A block with a non-finite y gets a NaN scale and codes 0.  Rows are independent of one another: a
+ * sequence's cache does not depend on how it was cut into appends.
+ * Arguments (device pointers): k_new, v_new [T, H_kv, D] of in_dtype, token t at element t * k_stride
+ * (v_stride), heads contiguous; slot_mapping [T] int64 as in pd_append_paged_kv (negative: skipped; at
+ * or beyond max_pages * P: skipped, PD_ERR_BAD_SLOT; two tokens of one call on one slot leave it
+ * undefined).  The decode may follow with PD_DECODE_EARLY_INPUTS.
+ */
+typedef struct {
+  int32_t T;                  /* new tokens */
+  int32_t H_kv;
+  int32_t D;                  /* head dim: 64, 128 or 256 */
+  int32_t page_size;          /* 1 to 256 */
+  int32_t in_dtype;           /* pd_dtype of k_new, v_new: F32, F16 or BF16 */
+  int32_t kv_dtype;           /* MX_E4M3 or MX_E8M0 */
+  int64_t max_pages;
+  int64_t k_stride, v_stride; /* elements from token to token, at least H_kv * D */
+  float k_scale, v_scale;
+  int32_t flags, reserved;    /* 0 */
+} pd_append_mx_desc;
+pd_status pd_append_paged_kv_mx(void* pages, void* scales, const void* k_new, const void* v_new,
+                                const int64_t* slot_mapping, const pd_append_mx_desc* desc,
+                                pd_stream_t stream);
+
+/*
+ * pd_batch_decode_paged_kv_mx — pd_batch_decode_paged_kv (q_len = 1) and pd_batch_decode_paged_kv_mq
+ * (q_len > 1) over a 4-bit cache.  Shapes, page table, windows and sinks, desc->sink, the host copies,
+ * splits, workspaces and capture are those of the two entry points; there are no RoPE arguments (see
+ * above), desc->kv_dtype is PD_MX_E4M3 or PD_MX_E8M0, desc->k_scale and v_scale the cache's, and a
+ * caller workspace holds pd_workspace_size_mx(desc, q_len) bytes.  Q may be F32, F16 or BF16; any page
+ * size with one or several query tokens.
+ * Arithmetic: tensor cores; codes times scales are exact in f16.  F16 and BF16 Q enter exactly (scaled
+ * per head by a power of two; elements under 2^-28 of the head's largest lose bits), and the weights
+ * 2^(s - n) are rounded once to f16; F32 Q and its weights go as sums of two f16 parts (22 bits).  Sums
+ * in fp32.  Fastest where page_size is a multiple of 16, Q 16-bit and D 64 or 128.
+ */
+pd_status pd_batch_decode_paged_kv_mx(const void* Q, const void* pages, const void* scales,
+                                      const int32_t* page_table_indptr,
+                                      const int32_t* page_table_values, const int32_t* length_info,
+                                      void* output, float* lse, int32_t q_len, float sm_scale,
+                                      const pd_decode_desc* desc, pd_stream_t stream);
+
+/*
+ * pd_build_page_tables — the tables that a step's append and decode read, built on the device from
+ * the requests' lengths.  Request b holds lengths[b] rows in the pages page_table[b, 0 ..] and the
+ * step adds new_tokens[b] rows, or, if that is negative, drops its last -new_tokens[b] (drafted tokens
+ * that were rejected; -lengths[b]: the request is over).  With len' = lengths[b] + new_tokens[b],
+ * pages(x) = ceil(x / page_size), b in order:
+ *   lengths[b] = len';  pages(len') - pages(len) pages are taken from the pool into page_table[b], or
+ *   given back to it (their entries of page_table stay as they were);
+ *   page_table_indptr [B+1] = sums of pages(len');  page_table_values: the requests' pages, packed;
+ *   append_indptr [B+1] = sums of max(new_tokens, 0);
+ *   length_info [B] = rows in the last page (0: no rows);  with window > 0 [3, B]: that, and for len'
+ *   > window + sinks (len' - window, sinks), else (0, 0): the last `window` rows and the first `sinks`
+ *   are attended;
+ *   slot_mapping and positions: of each new token, its row in the cache (page * page_size + offset) and
+ *   in its sequence; entries behind the last new token: slot -1 (an append skips it), position 0.
+ * page_table_values behind the last page is left as it was.  append_indptr, slot_mapping and positions
+ * may be NULL.
+ * The pool is a ring of page ids, free_pages [free_capacity], that holds room for every page; state[0]
+ * and state[1] count the pages ever taken from and given to it: those at state[0] .. state[1] - 1 (mod
+ * free_capacity) are free, taken in order.  state [4] int64 starts as (0, free pages, 0, 0).  Pages that
+ * requests share must not be given back here.  free_pages NULL: page_table already holds the pages.
+ * Nothing is changed, and the tables describe B empty sequences without new tokens, if the pool has
+ * too few pages or no room (PD_ERR_NO_PAGES on the device), or if values_capacity or T is too small
+ * (PD_ERR_BAD_LENGTH).  A request whose old or new length is outside [0, max_pages_per_seq *
+ * page_size] is left as it is and described as empty (PD_ERR_BAD_LENGTH).  A new token in a page with
+ * a negative id gets slot -1 (PD_ERR_BAD_PAGE).
+ * Calls that share `state`, lengths or page_table must not overlap on the GPU.  The call may be
+ * captured: a replay reads the lengths, tokens and pool that it finds.
+ */
+typedef struct {
+  int32_t B;                  /* requests, at most 8192 */
+  int32_t page_size;          /* 1 to 256 */
+  int32_t max_pages_per_seq;  /* entries of a row of page_table */
+  int32_t T;                  /* entries of slot_mapping and positions; 0 without both */
+  int32_t window, sinks;      /* 0: length_info is [B]; else [3, B] */
+  int32_t flags, reserved;    /* 0 */
+  int64_t table_stride;       /* entries from row to row of page_table */
+  int64_t values_capacity;    /* entries of page_table_values */
+  int64_t free_capacity;      /* entries of free_pages */
+} pd_tables_desc;
+pd_status pd_build_page_tables(int32_t* page_table, int32_t* lengths, const int32_t* new_tokens,
+                               int64_t* state, int32_t* free_pages, int32_t* page_table_indptr,
+                               int32_t* page_table_values, int32_t* length_info,
+                               int32_t* append_indptr, int64_t* slot_mapping, int32_t* positions,
+                               const pd_tables_desc* desc, pd_stream_t stream);
+
+/*
  * pd_qk_norm_rope — the per-head RMS norm of queries and keys and the position rotation, in one
  * pass (the order norm, rotation, cache update).  For token t, head h, x the head's D values:
  *   y_d = x_d / sqrt(mean(x^2) + eps) * (w_d + weight_offset); without weights y = x (no norm;
@@ -522,6 +632,9 @@ size_t pd_workspace_size_mq(const pd_decode_desc* desc, int32_t q_len);
 /* The same for pd_batch_decode_paged_kv_bs. */
 size_t pd_workspace_size_bs(const pd_decode_desc* desc, int32_t q_len, int32_t scale_rows);
 
+/* The same for pd_batch_decode_paged_kv_mx. */
+size_t pd_workspace_size_mx(const pd_decode_desc* desc, int32_t q_len);
+
 /* Zero-fill a caller-provided workspace before its first use (enqueued on stream). */
 pd_status pd_workspace_init(void* workspace, size_t bytes, pd_stream_t stream);
 
@@ -539,7 +652,7 @@ pd_status pd_plan(const pd_decode_desc* desc, int32_t num_sms, int32_t ctas_per_
                   int32_t* schedule, int32_t* grid_blocks, size_t* workspace_bytes);
 
 /* Synchronises `stream`, then reads and clears the current device's error word.
- * Returns PD_OK, PD_ERR_BAD_PAGE, PD_ERR_BAD_LENGTH, PD_ERR_BAD_SLOT or
+ * Returns PD_OK, PD_ERR_BAD_PAGE, PD_ERR_BAD_LENGTH, PD_ERR_BAD_SLOT, PD_ERR_NO_PAGES or
  * PD_ERR_TIMEOUT (the first that is set, in that order), or PD_ERR_CUDA. */
 pd_status pd_check_device_errors(pd_stream_t stream);
 

@@ -8,11 +8,14 @@ from ._lib import (  # noqa: F401
     PDError,
     append_paged_kv,
     append_paged_kv_bs,
+    append_paged_kv_mx,
     append_paged_kv_rope,
     batch_decode_paged_kv,
     batch_decode_paged_kv_noalloc,
     batch_decode_paged_kv_bs,
     batch_decode_paged_kv_mq,
+    batch_decode_paged_kv_mx,
+    build_page_tables,
     check_device_errors,
     host_meta_of,
     last_decode_variant,
@@ -20,6 +23,7 @@ from ._lib import (  # noqa: F401
     merge_state_inplace,
     merge_states,
     merge_states_packed,
+    page_pool,
     cp_shard_plan,
     plan,
     qk_norm_rope,
@@ -29,4 +33,5 @@ from ._lib import (  # noqa: F401
     workspace_init,
     workspace_size,
     workspace_size_bs,
+    workspace_size_mx,
 )

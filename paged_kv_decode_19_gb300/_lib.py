@@ -31,6 +31,7 @@ STATUS = {
     6: "PD_ERR_BAD_SLOT",
     7: "PD_ERR_TIMEOUT",
     8: "PD_ERR_WORKSPACE",
+    9: "PD_ERR_NO_PAGES",
 }
 DTYPE_CODES = {
     torch.float32: 0,
@@ -40,6 +41,8 @@ DTYPE_CODES = {
 }
 # codes of a block-scaled cache (the _bs entry points)
 BS_DTYPE_CODES = {torch.float8_e4m3fn: 3, torch.int8: 4}
+# a 4-bit cache, by the type of its scales, and the dims that share one (the _mx entry points)
+MX_DTYPE_CODES = {torch.float8_e4m3fn: (5, 16), torch.float8_e8m0fnu: (6, 32)}
 DTYPE_NAMES = {"f32": 0, "f16": 1, "bf16": 2, "e4m3": 3}
 
 # Every entry point declared in include/pageddecode.h.
@@ -60,6 +63,10 @@ EXPORTS = (
     "pd_append_paged_kv_bs",
     "pd_batch_decode_paged_kv_bs",
     "pd_workspace_size_bs",
+    "pd_append_paged_kv_mx",
+    "pd_batch_decode_paged_kv_mx",
+    "pd_workspace_size_mx",
+    "pd_build_page_tables",
     "pd_qk_norm_rope",
     "pd_rope_frequencies",
     "pd_check_device_errors",
@@ -145,6 +152,40 @@ class AppendBsDesc(ctypes.Structure):
     ]
 
 
+class AppendMxDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int32),
+        ("H_kv", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("max_pages", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class TablesDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("T", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("sinks", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("table_stride", ctypes.c_int64),
+        ("values_capacity", ctypes.c_int64),
+        ("free_capacity", ctypes.c_int64),
+    ]
+
+
 def lib():
     """Load libpageddecode.so (raises if it has not been built)."""
     global _lib
@@ -184,6 +225,14 @@ def lib():
             L.pd_batch_decode_paged_kv_bs.restype = i32
             L.pd_workspace_size_bs.argtypes = [ctypes.POINTER(DecodeDesc), i32, i32]
             L.pd_workspace_size_bs.restype = ctypes.c_size_t
+            L.pd_append_paged_kv_mx.argtypes = [P] * 7
+            L.pd_append_paged_kv_mx.restype = i32
+            L.pd_batch_decode_paged_kv_mx.argtypes = [P] * 8 + [i32, f32, P, P]
+            L.pd_batch_decode_paged_kv_mx.restype = i32
+            L.pd_workspace_size_mx.argtypes = [ctypes.POINTER(DecodeDesc), i32]
+            L.pd_workspace_size_mx.restype = ctypes.c_size_t
+            L.pd_build_page_tables.argtypes = [P] * 13
+            L.pd_build_page_tables.restype = i32
             L.pd_qk_norm_rope.argtypes = [P] * 8 + [P, P]
             L.pd_qk_norm_rope.restype = i32
             f64 = ctypes.c_double
@@ -517,6 +566,208 @@ def append_paged_kv_bs(pages, scales, k_new, v_new, append_indptr, page_table_in
     if st:
         _check(st)
     return pages, scales
+
+
+# ----------------------------------------------------------------------------- 4-bit cache
+_PACK_APPEND_MX = struct.Struct("@6i3q2f2i").pack
+_PACK_TABLES = struct.Struct("@8i3q").pack
+_U8, _I64 = torch.uint8, torch.int64
+# bytes of two codes: uint8, or torch's own type of two e2m1 values where it has one
+_MX_PAGES = (_U8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
+
+
+def _mx_refuse(pages, scales):
+    """What is wrong with a 4-bit cache."""
+    if pages.dim() != 5 or pages.shape[1] != 2 or pages.dtype not in _MX_PAGES:
+        raise ValueError("pages must be [max_pages, 2, H_kv, P, D / 2] of uint8 (two codes a byte)")
+    if scales.dtype not in MX_DTYPE_CODES:
+        raise ValueError("scales must be float8_e4m3fn (of 16 dims) or float8_e8m0fnu (of 32)")
+    n = MX_DTYPE_CODES[scales.dtype][1]
+    raise ValueError(f"scales must be [max_pages, 2, H_kv, P, D / {n}] for these pages")
+
+
+def batch_decode_paged_kv_mx(Q, pages, scales, page_table_indptr, page_table_values, length_info,
+                             output, lse, sm_scale=None, *, k_scale=1.0, v_scale=1.0, num_splits=0,
+                             workspace=None, early_inputs=False, sink=None, host_meta=None, stream=None):
+    """pd_batch_decode_paged_kv_mx: decode over 4-bit pages [max_pages, 2, H_kv, P, D / 2] (uint8,
+    two e2m1 codes a byte) with scales [max_pages, 2, H_kv, P, D / 16] float8_e4m3fn or
+    [..., D / 32] float8_e8m0fnu, times k_scale and v_scale.  Q [B, H_qo, D], or [B, q_len, H_qo, D]
+    for several query tokens per sequence (causal among them); output like Q, lse [B, H_qo] or
+    [B, q_len, H_qo].  K is used as stored and Q as given: rotate both with qk_norm_rope."""
+    shape, pshape, sshape = Q.shape, pages.shape, scales.shape
+    kv, block = MX_DTYPE_CODES.get(scales.dtype, (None, 1))
+    rank = len(shape)
+    if rank == 3:
+        (B, H_qo, D), q_len = shape, 1
+    elif rank == 4:
+        B, q_len, H_qo, D = shape
+    else:
+        raise ValueError("Q must be [B, H_qo, D] or [B, q_len, H_qo, D]")
+    vals, li_shape = page_table_values, length_info.shape
+    if (kv is None or len(pshape) != 5 or pshape[1] != 2 or pages.dtype not in _MX_PAGES
+            or len(sshape) != 5 or sshape[:4] != pshape[:4] or sshape[4] * block != 2 * pshape[4]):
+        _mx_refuse(pages, scales)
+    if (page_table_indptr.dtype != _I32 or length_info.dtype != _I32 or page_table_indptr.numel() != B + 1
+            or (li_shape != (B,) and li_shape != (3, B)) or (vals is not None and vals.dtype != _I32)):
+        _table_refuse(page_table_indptr, vals, length_info, B)
+    max_pages, _, H_kv, P, half = pshape
+    if 2 * half != D:
+        raise ValueError("Q must be [B, H_qo, D] or [B, q_len, H_qo, D]")
+    if output.shape != shape or lse.shape != shape[:-1] or lse.dtype != _F32:
+        raise ValueError("output must be shaped like Q and lse float32 like its heads")
+    q_code, out_code = DTYPE_CODES.get(Q.dtype), DTYPE_CODES.get(output.dtype)
+    if q_code is None or out_code is None:
+        raise ValueError("Q and output must be float32, float16 or bfloat16")
+    dev = _device(Q)
+    if not (pages.get_device() == scales.get_device()
+            == page_table_indptr.get_device() == length_info.get_device() == output.get_device()
+            == lse.get_device() == dev and Q.is_contiguous() and pages.is_contiguous()
+            and scales.is_contiguous() and page_table_indptr.is_contiguous()
+            and length_info.is_contiguous() and output.is_contiguous() and lse.is_contiguous()):
+        _refuse(dev, Q, pages, scales, page_table_indptr, length_info, output, lse)
+    vals_at = n_vals = ws_at = ws_bytes = sink_at = host_ip = host_li = 0
+    if vals is not None:
+        if vals.get_device() != dev or not vals.is_contiguous():
+            _refuse(dev, vals)
+        vals_at, n_vals = vals.data_ptr(), vals.numel()
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _refuse(dev, workspace)
+        ws_at, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if sink is not None:
+        sink_at = _sink_ptr(sink, H_qo)
+        if sink.get_device() != dev:
+            _refuse(dev, sink)
+    if host_meta is not None:
+        host_ip, host_li = _host_i32(host_meta[0], B + 1), _host_i32(host_meta[1], length_info.numel())
+    desc = _PACK_DECODE(B, H_qo, H_kv, D, P, q_code, kv, out_code,
+                        len(li_shape) == 2, num_splits, max_pages, n_vals, 0, k_scale, v_scale,
+                        DECODE_EARLY_INPUTS if early_inputs else 0, ws_at, ws_bytes, sink_at,
+                        host_ip, host_li)
+    st = (_lib or lib()).pd_batch_decode_paged_kv_mx(
+        Q.data_ptr(), pages.data_ptr(), scales.data_ptr(), page_table_indptr.data_ptr(),
+        vals_at or None, length_info.data_ptr(), output.data_ptr(), lse.data_ptr(), q_len,
+        D ** -0.5 if sm_scale is None else sm_scale, desc,
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
+    return output, lse
+
+
+def _table_refuse(page_table_indptr, page_table_values, length_info, B):
+    """What is wrong with a page table."""
+    for t in (page_table_indptr, page_table_values, length_info):
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError("page_table_indptr, page_table_values and length_info must be int32")
+    raise ValueError(f"page_table_indptr must be [{B} + 1] and length_info [{B}] or [3, {B}]")
+
+
+def workspace_size_mx(desc: DecodeDesc, q_len: int) -> int:
+    return int(lib().pd_workspace_size_mx(ctypes.byref(desc), q_len))
+
+
+def append_paged_kv_mx(pages, scales, k_new, v_new, slot_mapping, k_scale=1.0, v_scale=1.0, stream=None):
+    """pd_append_paged_kv_mx: quantises new tokens' K/V [T, H_kv, D] into the slots (int64 [T],
+    negative: skipped) of 4-bit pages with scales (both updated in place).  k_new and v_new may be
+    slices of a larger tensor along the heads (any token stride)."""
+    pshape, sshape = pages.shape, scales.shape
+    kv, block = MX_DTYPE_CODES.get(scales.dtype, (None, 1))
+    if (kv is None or len(pshape) != 5 or pshape[1] != 2 or pages.dtype not in _MX_PAGES
+            or len(sshape) != 5 or sshape[:4] != pshape[:4] or sshape[4] * block != 2 * pshape[4]):
+        _mx_refuse(pages, scales)
+    max_pages, _, H_kv, P, half = pshape
+    D, shape, dtype = 2 * half, k_new.shape, k_new.dtype
+    if len(shape) != 3 or shape[1] != H_kv or shape[2] != D or v_new.shape != shape or v_new.dtype != dtype:
+        raise ValueError("k_new and v_new must be [T, H_kv, D] of one dtype")
+    T, in_code = shape[0], DTYPE_CODES.get(dtype)
+    if in_code is None:
+        raise ValueError("k_new and v_new must be float32, float16 or bfloat16")
+    if slot_mapping.dtype != _I64 or slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be int64 [T]")
+    (ks, kh, kd), (vs, vh, vd) = k_new.stride(), v_new.stride()
+    if T and (kd != 1 or vd != 1 or (H_kv > 1 and (kh != D or vh != D))):
+        raise ValueError("the heads of k_new and v_new must be contiguous")
+    if T < 2:
+        ks = vs = H_kv * D
+    dev = _device(pages)
+    if not (scales.get_device() == k_new.get_device() == v_new.get_device() == slot_mapping.get_device() == dev
+            and pages.is_contiguous() and scales.is_contiguous() and slot_mapping.is_contiguous()):
+        _refuse(dev, pages, scales, k_new, v_new, slot_mapping)
+    desc = _PACK_APPEND_MX(T, H_kv, D, P, in_code, kv, max_pages, ks, vs, k_scale, v_scale, 0, 0)
+    st = (_lib or lib()).pd_append_paged_kv_mx(
+        pages.data_ptr(), scales.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), desc,
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
+    return pages, scales
+
+
+def page_pool(num_pages, device="cuda"):
+    """(free_pages, state) of a pool of pages 0 .. num_pages - 1, all free, for build_page_tables."""
+    return (torch.arange(num_pages, dtype=_I32, device=device),
+            torch.tensor([0, num_pages, 0, 0], dtype=_I64, device=device))
+
+
+def build_page_tables(page_table, lengths, new_tokens, state, page_size, page_table_indptr, page_table_values,
+                      length_info, append_indptr=None, slot_mapping=None, positions=None, *, free_pages=None,
+                      window=0, sinks=0, stream=None):
+    """pd_build_page_tables: the tables of a step, on the device, from the requests' lengths.
+    page_table int32 [B, pages] (each request's pages; rows may be strided), lengths int32 [B] and
+    state int64 [4] are moved on in place; new_tokens int32 [B] (negative: rows dropped).  Written:
+    page_table_indptr [B+1], page_table_values, length_info ([B], with a window [3, B]), append_indptr
+    [B+1] (all int32), slot_mapping int64 [T] and positions int32 [T], as the appends and decodes take
+    them.  free_pages int32: the ring of free pages (page_pool); None: page_table holds its pages."""
+    if page_table.dim() != 2 or page_table.dtype != _I32:
+        raise ValueError("page_table must be int32 [B, pages]")
+    B, width = page_table.shape
+    if lengths.dtype != _I32 or new_tokens.dtype != _I32 or lengths.shape != (B,) or new_tokens.shape != (B,):
+        raise ValueError("lengths and new_tokens must be int32 [B]")
+    if state.dtype != _I64 or state.shape != (4,):
+        raise ValueError("state must be int64 [4]")
+    if page_table_values.dtype != _I32 or page_table_values.dim() != 1:
+        raise ValueError("page_table_values must be int32 [capacity]")
+    if page_table_indptr.dtype != _I32 or page_table_indptr.shape != (B + 1,):
+        raise ValueError("page_table_indptr must be int32 [B+1]")
+    if length_info.dtype != _I32 or length_info.shape != ((3, B) if window else (B,)):
+        raise ValueError("length_info must be int32 [B], with a window [3, B]")
+    if append_indptr is not None and (append_indptr.dtype != _I32 or append_indptr.shape != (B + 1,)):
+        raise ValueError("append_indptr must be int32 [B+1]")
+    T = 0
+    if slot_mapping is not None:
+        T = slot_mapping.numel()
+        if slot_mapping.dtype != _I64 or slot_mapping.dim() != 1:
+            raise ValueError("slot_mapping must be int64 [T]")
+    if positions is not None:
+        if positions.dtype != _I32 or positions.dim() != 1 or (slot_mapping is not None and positions.numel() != T):
+            raise ValueError("positions must be int32 [T]")
+        T = positions.numel()
+    if free_pages is not None and (free_pages.dtype != _I32 or free_pages.dim() != 1 or not free_pages.numel()):
+        raise ValueError("free_pages must be int32 [pages]")
+    dev = _device(state)
+    stride, last = page_table.stride()
+    if B > 1 and width and (last != 1 and width > 1 or stride < width):
+        raise ValueError("the rows of page_table must be contiguous, and apart")
+    if B == 1 and width > 1 and last != 1:
+        raise ValueError("the rows of page_table must be contiguous, and apart")
+    at = []
+    for t in (lengths, new_tokens, state, free_pages, page_table_indptr, page_table_values, length_info,
+              append_indptr, slot_mapping, positions):
+        if t is None:
+            at.append(None)
+            continue
+        if t.get_device() != dev or not t.is_contiguous():
+            _refuse(dev, t)
+        at.append(t.data_ptr())
+    if page_table.get_device() != dev:
+        _refuse(dev, page_table)
+    desc = _PACK_TABLES(B, page_size, width, T, window, sinks, 0, 0, stride, page_table_values.numel(),
+                        0 if free_pages is None else free_pages.numel())
+    st = (_lib or lib()).pd_build_page_tables(
+        page_table.data_ptr(), *at, desc,
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
+    return page_table_indptr, page_table_values, length_info
 
 
 ROPE_SCALINGS = {None: 0, "linear": 1, "theta": 2, "parts": 3}

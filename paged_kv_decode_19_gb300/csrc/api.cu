@@ -33,6 +33,11 @@ constexpr int kSegCostTiles = PD_SEG_COST_TILES;
 #define PD_BS_SEG_COST_TILES 8
 #endif
 constexpr int kBsSegCostTiles = PD_BS_SEG_COST_TILES;
+// And of the 4-bit one.
+#ifndef PD_MX_SEG_COST_TILES
+#define PD_MX_SEG_COST_TILES 8
+#endif
+constexpr int kMxSegCostTiles = PD_MX_SEG_COST_TILES;
 constexpr size_t kWsAlign = 256;
 
 static thread_local std::string t_last_error;
@@ -67,6 +72,8 @@ struct DeviceState {
   // the same of the block-scaled kernels: [SIMT / mma / mma by rows][q_dtype][e4m3 / int8][D]
   // [single / multi-query]
   int bs_occupancy[3][4][2][3][2] = {};
+  // of the 4-bit kernels: [e4m3 / e8m0 scales][16-bit / F32 Q][whole tiles / rows][D][single / multi-query]
+  int mx_occupancy[2][2][2][3][2] = {};
 };
 constexpr int kMaxDevices = 64;
 static DeviceState g_dev[kMaxDevices];
@@ -120,9 +127,15 @@ struct BlockScales {
   int scale_rows;
 };
 
+// A 4-bit cache's scales [max_pages, 2, H_kv, page_size, D / 16 (PD_MX_E4M3) or D / 32 (PD_MX_E8M0)], a byte each.
+struct MxScales {
+  const uint8_t* scales;
+};
+static bool mx_dtype(int dt) { return dt == PD_MX_E4M3 || dt == PD_MX_E8M0; }
+
 // ---------------------------------------------------------------------------- validation
-// bs: the desc is of a block-scaled cache (its k_scale, v_scale are not read).
-static pd_status validate_desc(const pd_decode_desc* d, const BlockScales* bs = nullptr) {
+// bs: the desc is of a block-scaled cache (its k_scale, v_scale are not read); mx: of a 4-bit one.
+static pd_status validate_desc(const pd_decode_desc* d, const BlockScales* bs = nullptr, const MxScales* mx = nullptr) {
   if (!d) return fail(PD_ERR_INVALID_ARG, "desc is NULL");
   if (d->B < 0) return fail(PD_ERR_INVALID_ARG, "B < 0");
   if (d->H_kv <= 0 || d->H_qo <= 0 || d->H_qo % d->H_kv != 0)
@@ -135,6 +148,8 @@ static pd_status validate_desc(const pd_decode_desc* d, const BlockScales* bs = 
   if (bs) {
     if (d->kv_dtype != kE4M3 && d->kv_dtype != kI8)
       return fail(PD_ERR_INVALID_ARG, "a block-scaled cache is E4M3 or I8");
+  } else if (mx) {
+    if (!mx_dtype(d->kv_dtype)) return fail(PD_ERR_INVALID_ARG, "a 4-bit cache is MX_E4M3 or MX_E8M0");
   } else if (d->kv_dtype < kF32 || d->kv_dtype > kE4M3) {
     return fail(PD_ERR_INVALID_ARG, "bad kv_dtype");
   }
@@ -150,6 +165,11 @@ static pd_status validate_desc(const pd_decode_desc* d, const BlockScales* bs = 
   if (bs) {
     if (bs->scale_rows <= 0 || d->page_size % bs->scale_rows != 0)
       return fail(PD_ERR_INVALID_ARG, "scale_rows must divide page_size");
+    return PD_OK;
+  }
+  if (mx) {
+    if (!(d->k_scale > 0.f && d->v_scale > 0.f && std::isfinite(d->k_scale) && std::isfinite(d->v_scale)))
+      return fail(PD_ERR_INVALID_ARG, "a 4-bit cache needs finite positive k_scale and v_scale");
     return PD_OK;
   }
   if (d->kv_dtype == kE4M3 && !(d->k_scale > 0.f && d->v_scale > 0.f && std::isfinite(d->k_scale) &&
@@ -226,6 +246,20 @@ static cudaError_t bs_mma_dispatch(const DecodeParams& p, const CUtensorMap& tm,
                              : launch_bs_rows_int(p, tm, q_dtype, grid, st, cfg);
   return kv_dtype == kE4M3 ? launch_bs_e4m3(p, tm, q_dtype, grid, st, cfg)
                            : launch_bs_int(p, tm, q_dtype, grid, st, cfg);
+}
+
+// Whether the tiles of a 4-bit decode are gathered row by row: copied whole they are 16 rows of a page.
+// (F32 Q and D 256 are bound by their products: one kernel, which takes any page.)
+static bool mx_rows(const pd_decode_desc* d) {
+  return d->page_size % 16 != 0 || d->q_dtype == kF32 || d->D == 256;
+}
+
+static cudaError_t mx_dispatch(const DecodeParams& p, int q_dtype, int kv_dtype, bool rows, dim3 grid,
+                               cudaStream_t st, MmaConfig* cfg) {
+  const bool e4m3 = kv_dtype == PD_MX_E4M3;
+  if (q_dtype == kF32) return e4m3 ? launch_mx_f32_e4m3(p, grid, st, cfg) : launch_mx_f32_e8m0(p, grid, st, cfg);
+  if (rows) return e4m3 ? launch_mx_rows_e4m3(p, grid, st, cfg) : launch_mx_rows_e8m0(p, grid, st, cfg);
+  return e4m3 ? launch_mx_e4m3(p, grid, st, cfg) : launch_mx_e8m0(p, grid, st, cfg);
 }
 
 // The pages of an 8-bit cache as TMA boxes of 16 rows of a head, K and V: [max_pages, 2, H_kv, P, D]
@@ -423,6 +457,24 @@ static pd_status bs_occupancy_for(const pd_decode_desc* d, const BlockScales* bs
   return PD_OK;
 }
 
+static pd_status mx_occupancy_for(const pd_decode_desc* d, int* ctas, DeviceState* ds, int q_len) {
+  const int di = d->D == 64 ? 0 : d->D == 128 ? 1 : 2;
+  const bool rows = mx_rows(d);
+  int& cached = ds->mx_occupancy[d->kv_dtype == PD_MX_E8M0][d->q_dtype == kF32][rows][di][q_len > 1];
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (cached == 0) {
+    DecodeParams p{};
+    p.D = d->D;
+    p.q_len = q_len;
+    MmaConfig cfg{};
+    const cudaError_t e = mx_dispatch(p, d->q_dtype, d->kv_dtype, rows, dim3(1), nullptr, &cfg);
+    if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
+    cached = std::max(cfg.ctas_per_sm, 1);
+  }
+  *ctas = cached;
+  return PD_OK;
+}
+
 static size_t workspace_size_q(const pd_decode_desc* desc, int q_len) {
   if (validate_desc(desc) != PD_OK || q_len < 1) return 0;
   DeviceState* ds = nullptr;
@@ -463,6 +515,18 @@ size_t pd_workspace_size_bs(const pd_decode_desc* desc, int32_t q_len, int32_t s
   return ws;
 }
 
+size_t pd_workspace_size_mx(const pd_decode_desc* desc, int32_t q_len) {
+  const MxScales mx{};
+  if (validate_desc(desc, nullptr, &mx) != PD_OK || q_len < 1) return 0;
+  DeviceState* ds = nullptr;
+  if (device_state(&ds) != PD_OK) return 0;
+  int ctas = 1, mode, grid;
+  if (mx_occupancy_for(desc, &ctas, ds, q_len) != PD_OK) return 0;
+  size_t ws;
+  plan_impl(desc, ds->num_sms, ctas, kMmaWarps, &mode, &grid, &ws, q_len);
+  return ws;
+}
+
 pd_status pd_workspace_init(void* workspace, size_t bytes, pd_stream_t stream) {
   if (!workspace && bytes) return fail(PD_ERR_INVALID_ARG, "workspace is NULL");
   cudaError_t e = cudaMemsetAsync(workspace, 0, bytes, (cudaStream_t)stream);
@@ -473,15 +537,15 @@ pd_status pd_workspace_init(void* workspace, size_t bytes, pd_stream_t stream) {
 }  // extern "C"
 
 // All decode entry points: q_len query tokens per sequence (1: batch_decode_paged_kv);
-// bs: the cache's block scales (nullptr: a cache without).
+// bs: the cache's block scales, mx: a 4-bit cache's (both nullptr: a cache without).
 static pd_status decode_call(const void* Q, const void* pages, const int32_t* page_table_indptr,
                              const int32_t* page_table_values, const int32_t* length_info,
                              const int32_t* k_rope_pos_offset, const int32_t* q_rope_position,
                              void* output, float* lse, int q_len, int32_t rotary_mode,
                              float rope_scale, float rope_theta, float sm_scale,
                              const pd_decode_desc* desc, pd_stream_t stream,
-                             const BlockScales* bs = nullptr) {
-  pd_status st = validate_desc(desc, bs);
+                             const BlockScales* bs = nullptr, const MxScales* mx = nullptr) {
+  pd_status st = validate_desc(desc, bs, mx);
   if (st != PD_OK) return st;
   const pd_decode_desc& d = *desc;
   if (rotary_mode < 0 || rotary_mode > 2) return fail(PD_ERR_INVALID_ARG, "rotary_mode must be 0, 1 or 2");
@@ -510,19 +574,23 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   if (bs && (!bs->scales || (reinterpret_cast<uintptr_t>(bs->scales) % 4) != 0))
     return fail(PD_ERR_INVALID_ARG, "scales is NULL or not 4-byte aligned");
 
-  const bool use_mma = bs ? bs_mma_path(desc) : mma_path(desc, pages);
+  if (mx && (!mx->scales || (reinterpret_cast<uintptr_t>(mx->scales) % 16) != 0))
+    return fail(PD_ERR_INVALID_ARG, "scales is NULL or not 16-byte aligned");
+
+  const bool use_mma = mx || (bs ? bs_mma_path(desc) : mma_path(desc, pages));
   if (bs && q_len > 1 && !use_mma)
     return fail(PD_ERR_UNSUPPORTED, "several query tokens run on the tensor-core kernel only: f16/bf16 Q, "
                                     "D 64 or 128");
   DeviceState* ds = nullptr;
   st = device_state(&ds);
   if (st != PD_OK) return st;
-  if (!bs && q_len > 1 && (!use_mma || d.page_size % 16 != 0))
+  if (!bs && !mx && q_len > 1 && (!use_mma || d.page_size % 16 != 0))
     return fail(PD_ERR_UNSUPPORTED, "multi-query decode runs on the tensor-core kernel only: "
                                     "f16/bf16 (D 64 or 128) or E4M3 (D 128) KV, page size a multiple of 16");
   int ctas = 1;
   const bool k_rotated = rotary_mode != 0 && (d.flags & PD_DECODE_K_ROTATED);
-  st = bs ? bs_occupancy_for(desc, bs, use_mma, &ctas, ds, q_len)
+  st = mx ? mx_occupancy_for(desc, &ctas, ds, q_len)
+     : bs ? bs_occupancy_for(desc, bs, use_mma, &ctas, ds, q_len)
           : occupancy_for(desc, use_mma, rotary_mode + (k_rotated ? 2 : 0), &ctas, ds, q_len);
   if (st != PD_OK) return st;
   CUtensorMap tm{};
@@ -535,7 +603,7 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   const int wpb = use_mma ? kMmaWarps : 1;
   plan_impl(desc, ds->num_sms, ctas, wpb, &mode, &grid_blocks, &ws_need, q_len);
   if (grid_blocks == 0) return PD_OK;
-  if (bs && use_mma && mode == kSchedBalanced && d.num_splits == 0) {
+  if ((bs || mx) && use_mma && mode == kSchedBalanced && d.num_splits == 0) {
     const int wave = ds->num_sms * ctas;
     if (d.host_indptr) {
       if (block_per_segment(d, (d.H_qo / d.H_kv * q_len + kMaxGroupPerCta - 1) / kMaxGroupPerCta, wave)) {
@@ -638,7 +706,7 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   p.rotary = rotary_mode;
   p.mode = mode;
   // tensor-core schedule: a segment's set-up and finish cost about kSegCostTiles tiles
-  const int seg_tiles = bs ? kBsSegCostTiles : kSegCostTiles;
+  const int seg_tiles = mx ? kMxSegCostTiles : bs ? kBsSegCostTiles : kSegCostTiles;
   p.seg_cost = use_mma && mode == kSchedBalanced && seg_tiles > 0
                    ? std::max(1, seg_tiles * 16 / d.page_size) : 0;
   p.out_dtype = d.out_dtype;
@@ -647,10 +715,15 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   p.k_rotated = k_rotated ? 1 : 0;
   p.sink = d.sink;
   const double log2e = 1.4426950408889634073599246810019;
-  const double kdeq = d.kv_dtype == kE4M3 && !bs ? (double)d.k_scale : 1.0;
+  const bool tensor_scales = mx || (d.kv_dtype == kE4M3 && !bs);
+  const double kdeq = tensor_scales ? (double)d.k_scale : 1.0;
   p.score_scale = (float)((double)sm_scale * log2e * kdeq);
   p.q_prescale = p.score_scale;
-  p.out_scale = d.kv_dtype == kE4M3 && !bs ? d.v_scale : 1.f;
+  p.out_scale = tensor_scales ? d.v_scale : 1.f;
+  if (mx) {
+    p.mx_scales = mx->scales;
+    p.q_bf16 = d.q_dtype == kBF16;
+  }
   if (bs) {
     p.scales = bs->scales;
     p.scale_rows = bs->scale_rows;
@@ -662,7 +735,10 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
 
   const dim3 grid((unsigned)grid_blocks);
   cudaError_t e;
-  if (bs) {
+  if (mx) {
+    e = mx_dispatch(p, d.q_dtype, d.kv_dtype, mx_rows(desc), grid, s, nullptr);
+    t_last_variant = "mma";
+  } else if (bs) {
     e = use_mma ? bs_mma_dispatch(p, tm, d.q_dtype, d.kv_dtype, grid, s, nullptr)
                 : launch_decode_simt_bs(p, d.q_dtype, d.kv_dtype, grid, s);
     t_last_variant = use_mma ? "mma" : "simt";
@@ -724,6 +800,20 @@ pd_status pd_batch_decode_paged_kv_bs(const void* Q, const void* pages, const fl
   const BlockScales bs{scales, scale_rows};
   return decode_call(Q, pages, page_table_indptr, page_table_values, length_info, nullptr, nullptr,
                      output, lse, q_len, 0, 1.f, 1e4f, sm_scale, desc, stream, &bs);
+}
+
+pd_status pd_batch_decode_paged_kv_mx(const void* Q, const void* pages, const void* scales,
+                                      const int32_t* page_table_indptr,
+                                      const int32_t* page_table_values, const int32_t* length_info,
+                                      void* output, float* lse, int32_t q_len, float sm_scale,
+                                      const pd_decode_desc* desc, pd_stream_t stream) {
+  if (q_len < 1) return fail(PD_ERR_INVALID_ARG, "q_len must be >= 1");
+  if (desc && q_len > 1 && desc->sliding_window)
+    return fail(PD_ERR_UNSUPPORTED, "multi-query decode has no sliding-window form");
+  if (desc && (long long)desc->B * q_len > INT_MAX) return fail(PD_ERR_UNSUPPORTED, "B * q_len exceeds 2^31");
+  const MxScales mx{(const uint8_t*)scales};
+  return decode_call(Q, pages, page_table_indptr, page_table_values, length_info, nullptr, nullptr,
+                     output, lse, q_len, 0, 1.f, 1e4f, sm_scale, desc, stream, nullptr, &mx);
 }
 
 pd_status pd_merge_state_inplace(void* V, float* S, const void* V_other, const float* S_other,
@@ -918,6 +1008,113 @@ pd_status pd_append_paged_kv_bs(void* pages, float* scales, const void* k_new, c
   return PD_OK;
 }
 
+pd_status pd_append_paged_kv_mx(void* pages, void* scales, const void* k_new, const void* v_new,
+                                const int64_t* slot_mapping, const pd_append_mx_desc* desc,
+                                pd_stream_t stream) {
+  if (!desc) return fail(PD_ERR_INVALID_ARG, "desc is NULL");
+  const pd_append_mx_desc& d = *desc;
+  if (d.T < 0 || d.H_kv <= 0 || d.max_pages <= 0) return fail(PD_ERR_INVALID_ARG, "bad T/H_kv/max_pages");
+  if (d.D != 64 && d.D != 128 && d.D != 256) return fail(PD_ERR_UNSUPPORTED, "head dim must be 64, 128 or 256");
+  if (d.page_size <= 0 || d.page_size > 256) return fail(PD_ERR_INVALID_ARG, "page_size must be in [1, 256]");
+  if (d.in_dtype != kF32 && d.in_dtype != kF16 && d.in_dtype != kBF16)
+    return fail(PD_ERR_INVALID_ARG, "in_dtype must be F32, F16 or BF16");
+  if (!mx_dtype(d.kv_dtype)) return fail(PD_ERR_INVALID_ARG, "a 4-bit cache is MX_E4M3 or MX_E8M0");
+  if (!(d.k_scale > 0.f && d.v_scale > 0.f && std::isfinite(d.k_scale) && std::isfinite(d.v_scale)))
+    return fail(PD_ERR_INVALID_ARG, "a 4-bit cache needs finite positive k_scale and v_scale");
+  if (d.flags || d.reserved) return fail(PD_ERR_INVALID_ARG, "flags and reserved must be 0");
+  const long long row = (long long)d.H_kv * d.D;
+  if (d.T > 1 && (d.k_stride < row || d.v_stride < row))
+    return fail(PD_ERR_INVALID_ARG, "k_stride and v_stride must be at least H_kv * D");
+  if (d.max_pages > INT_MAX || d.max_pages * 2 * d.H_kv > INT_MAX)
+    return fail(PD_ERR_UNSUPPORTED, "max_pages * 2 * H_kv exceeds 2^31");
+  if ((long long)d.T * d.H_kv > INT_MAX || d.T > (1 << 30) || row > INT_MAX)
+    return fail(PD_ERR_UNSUPPORTED, "T or H_kv too large");
+  if (d.T == 0) return PD_OK;
+  if (!pages || !scales || !k_new || !v_new || !slot_mapping) return fail(PD_ERR_INVALID_ARG, "NULL device pointer");
+  const int eb = elem_bytes(d.in_dtype);
+  if ((reinterpret_cast<uintptr_t>(pages) % 16) != 0 || (reinterpret_cast<uintptr_t>(scales) % 16) != 0 ||
+      (reinterpret_cast<uintptr_t>(k_new) % eb) != 0 || (reinterpret_cast<uintptr_t>(v_new) % eb) != 0)
+    return fail(PD_ERR_INVALID_ARG, "pages and scales must be 16-byte, k_new and v_new element aligned");
+  DeviceState* ds = nullptr;
+  pd_status st = device_state(&ds);
+  if (st != PD_OK) return st;
+  AppendMxParams a{};
+  a.pages = (uint8_t*)pages;
+  a.scales = (uint8_t*)scales;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.slots = slot_mapping;
+  a.err = ds->err;
+  a.k_stride = d.k_stride;
+  a.v_stride = d.v_stride;
+  a.n_slots = d.max_pages * d.page_size;
+  a.k_scale = d.k_scale;
+  a.v_scale = d.v_scale;
+  a.T = d.T;
+  a.H_kv = d.H_kv;
+  a.P = d.page_size;
+  const cudaError_t e = launch_append_mx(a, d.D, d.kv_dtype == PD_MX_E4M3 ? 16 : 32, d.in_dtype, ds->num_sms,
+                                         (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "append launch");
+  return PD_OK;
+}
+
+pd_status pd_build_page_tables(int32_t* page_table, int32_t* lengths, const int32_t* new_tokens, int64_t* state,
+                               int32_t* free_pages, int32_t* page_table_indptr, int32_t* page_table_values,
+                               int32_t* length_info, int32_t* append_indptr, int64_t* slot_mapping,
+                               int32_t* positions, const pd_tables_desc* desc, pd_stream_t stream) {
+  if (!desc) return fail(PD_ERR_INVALID_ARG, "desc is NULL");
+  const pd_tables_desc& d = *desc;
+  if (d.B < 0 || d.max_pages_per_seq <= 0 || d.T < 0 || d.values_capacity < 0 || d.free_capacity < 0)
+    return fail(PD_ERR_INVALID_ARG, "bad B/max_pages_per_seq/T/values_capacity/free_capacity");
+  if (d.page_size <= 0 || d.page_size > 256) return fail(PD_ERR_INVALID_ARG, "page_size must be in [1, 256]");
+  if (d.window < 0 || d.sinks < 0 || (d.sinks && !d.window))
+    return fail(PD_ERR_INVALID_ARG, "window and sinks must be >= 0, sinks 0 without a window");
+  if (d.flags || d.reserved) return fail(PD_ERR_INVALID_ARG, "flags and reserved must be 0");
+  if (d.B > 1 && d.table_stride < d.max_pages_per_seq)
+    return fail(PD_ERR_INVALID_ARG, "table_stride must be at least max_pages_per_seq");
+  if (d.B > kMaxTableB) return fail(PD_ERR_UNSUPPORTED, "B exceeds 8192");
+  if ((long long)d.B * d.max_pages_per_seq > INT_MAX || d.values_capacity > INT_MAX || d.free_capacity > INT_MAX ||
+      d.T > (1 << 30) - 1)
+    return fail(PD_ERR_UNSUPPORTED, "B * max_pages_per_seq, values_capacity, free_capacity or T too large");
+  if (!state || !page_table_indptr || (d.values_capacity && !page_table_values) ||
+      (d.B && (!page_table || !lengths || !new_tokens || !length_info)))
+    return fail(PD_ERR_INVALID_ARG, "NULL device pointer");
+  if (!free_pages != !d.free_capacity) return fail(PD_ERR_INVALID_ARG, "free_pages and free_capacity go together");
+  if (d.T && !slot_mapping && !positions)
+    return fail(PD_ERR_INVALID_ARG, "T is the length of slot_mapping and positions: 0 without both");
+  DeviceState* ds = nullptr;
+  pd_status st = device_state(&ds);
+  if (st != PD_OK) return st;
+  TableParams a{};
+  a.table = page_table;
+  a.lengths = lengths;
+  a.new_tokens = new_tokens;
+  a.state = (long long*)state;
+  a.ring = free_pages;
+  a.indptr = page_table_indptr;
+  a.values = page_table_values;
+  a.length_info = length_info;
+  a.append_indptr = append_indptr;
+  a.slots = slot_mapping;
+  a.positions = positions;
+  a.err = ds->err;
+  a.table_stride = d.table_stride;
+  a.B = d.B;
+  a.P = d.page_size;
+  a.max_pages = d.max_pages_per_seq;
+  a.max_rows = (int)std::min<long long>((long long)d.max_pages_per_seq * d.page_size, INT_MAX - 256);
+  a.window = d.window;
+  a.sinks = d.sinks;
+  a.values_cap = (int)d.values_capacity;
+  a.C = (int)d.free_capacity;
+  a.T = d.T;
+  a.most_tokens = slot_mapping || positions ? d.T : (1 << 30) - 1;
+  const cudaError_t e = launch_page_tables(a, ds->num_sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "page tables launch");
+  return PD_OK;
+}
+
 pd_status pd_rope_frequencies(int32_t rotary_dim, double rope_theta, int32_t scaling, double factor,
                               double original_context, double low_turns, double high_turns,
                               double* inv_freq) {
@@ -1045,6 +1242,7 @@ pd_status pd_check_device_errors(pd_stream_t stream) {
   if (word & kErrBadPage) return fail(PD_ERR_BAD_PAGE, "a page id or sequence offset was out of range");
   if (word & kErrBadLength) return fail(PD_ERR_BAD_LENGTH, "inconsistent length_info or split-plan overflow");
   if (word & kErrBadSlot) return fail(PD_ERR_BAD_SLOT, "an append slot was beyond the cache");
+  if (word & kErrNoPages) return fail(PD_ERR_NO_PAGES, "a step needed more pages than the pool had free");
   if (word & kErrTimeout) return fail(PD_ERR_TIMEOUT, "a pipeline wait timed out");
   return PD_OK;
 }

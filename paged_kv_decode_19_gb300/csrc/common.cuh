@@ -22,7 +22,8 @@ enum : int { kF32 = 0, kF16 = 1, kBF16 = 2, kE4M3 = 3, kI8 = 4 };
 
 // device error word bits
 // (kErrTimeout: a bounded wait for a kernel's own copies ran out; decode_bs.cuh)
-enum : unsigned { kErrBadPage = 1u, kErrBadLength = 2u, kErrBadSlot = 4u, kErrTimeout = 8u };
+// (kErrNoPages: a step needed more pages than the pool had free; page_tables.cu)
+enum : unsigned { kErrBadPage = 1u, kErrBadLength = 2u, kErrBadSlot = 4u, kErrTimeout = 8u, kErrNoPages = 16u };
 
 // Initial running max of the online softmax (the TVM decode kernel's -5e4 sentinel);
 // together with d = 0 it is the empty state and the merge identity.

@@ -67,6 +67,8 @@ struct DecodeParams {
   const float* scales;  // 8-bit cache with a scale per block of rows: [max_pages, 2, H_kv, n_sb]
   int scale_rows, n_sb; // rows per block, blocks per page (scale_rows * n_sb = P)
   int sb_mul;           // ceil(2^20 / scale_rows): row r < 256 of a page is in block (r * sb_mul) >> 20
+  const uint8_t* mx_scales;  // 4-bit cache: [max_pages, 2, H_kv, P, D / block] scale bytes
+  int q_bf16;                // 4-bit cache, 16-bit Q: BF16, else F16
   unsigned long long rope_F[kMaxHalfDim];  // fixed-point turns/position per frequency
   // Host plan: when hp_B > 0 the caller gave host copies of page_table_indptr and
   // length_info, and the launch carries them: hp[0 .. B] = prefix sums over the

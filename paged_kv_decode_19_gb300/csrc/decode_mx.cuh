@@ -1,0 +1,713 @@
+// Tensor-core decode of a 4-bit KV cache: e2m1 codes, two dims a byte, with a scale per row and block
+// of SB dims: e4m3 (SB 16) or a power of two, e8m0 (SB 32).
+//
+//   K_rd = c_rd ks_r,d/SB k_scale,  s_r = sm_scale log2(e) q.K_r,  out = sum_r 2^(s_r) V_r / sum_r 2^(s_r)
+//
+// The work split, the schedule and the merge are those of the other tensor-core decodes
+// (decode_common.cuh, decode_parts.cuh): every warp is an independent worker on its share of the pages.
+#pragma once
+
+#include <cfloat>
+
+#include "decode_mma.cuh"
+#include "decode_parts.cuh"
+
+namespace pd {
+
+constexpr float kLazyMaxMx = 8.f;   // the running maximum moves when exceeded by more than 2^8 ...
+constexpr float kWeightUp = 7.f;    // ... and a weight is held times 2^7: at most 2^15 in f16
+
+// ----------------------------------------------------------------------------- geometry
+template <int SB, int D, bool ROWS>
+struct MxTile {
+  static constexpr int RB = D / 2;                  // code bytes per row
+  static constexpr int NB = D / SB;                 // scale bytes per row
+  static constexpr int SR = ROWS && NB < 4 ? 4 : NB;  // of a row in shared memory (ROWS: whole words are copied)
+  static constexpr int KT = D / 16;                 // k-tiles of QK, m-tiles of PV
+  static constexpr int KB = D == 64 ? 8 : 16;       // K bytes a thread reads at once
+  static constexpr int KCH = RB / (4 * KB);         // times per row
+  static constexpr int VB = RB / 8;                 // V bytes per row and thread
+  static constexpr int RL = D / 8;                  // V dims per row and thread
+  static constexpr int kCodes = 16 * RB;            // one tile of K (or V) codes
+  static constexpr int kScales = 16 * SR;           // and of its scales
+  static constexpr int kPair = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
+  static constexpr int NQ = D == 64 ? 4 : 2;        // tiles computed together
+  static constexpr int NST = 2;                     // ring stages per warp, of NQ tiles each
+  static constexpr int kStage = NQ * kPair;
+  static constexpr int kState = kMaxGroupPerCta * D * 4;  // a partial state's outputs, fp32
+  static constexpr int kRing = (NST * kStage > kState ? NST * kStage : kState);
+  static_assert(D == 64 || D == 128 || D == 256, "head dim");
+};
+template <int SB, int D, bool ROWS, int NW>
+constexpr int mx_smem_bytes() { return NW * (MxTile<SB, D, ROWS>::kRing + MxTile<SB, D, ROWS>::kState) + 128; }
+
+// Row of the tile that fragment row g (0..7; g + 8: the row + 8) holds.  Rows 2i and 2i + 1 of K, read
+// by one phase of lanes, lie in both halves of a 128-byte line (D 128); of the four rows of V that the
+// quad lanes read, two do.
+__device__ __forceinline__ int mx_row(int g) { return g ^ ((g >> 1) & 1); }
+
+// A scale's f16 pair from two bytes in the low half of w.
+template <int SB>
+__device__ __forceinline__ uint32_t mx_scales(uint32_t w) {
+  if constexpr (SB == 16) return e4m3x2_to_f16x2((uint16_t)w);
+  // 2^(b - 127) as f16: exponent b - 112 for 2^-14 to 2^15; 0 below, NaN above 2^13 (where a code
+  // times it would overflow)
+  const int a = (int)(w & 255u) - 112, b = (int)((w >> 8) & 255u) - 112;
+  const uint32_t x = a > 28 ? 0x7e00u : (uint32_t)max(a, 0) << 10, y = b > 28 ? 0x7e00u : (uint32_t)max(b, 0) << 10;
+  return x | (y << 16);
+}
+
+// eight codes (four bytes) -> f16x2 of each byte, exact
+__device__ __forceinline__ void mx_codes(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// 8x8 transpose of 16-bit elements across the warp: from row lane / 4, columns 2 (lane % 4) + {0, 1}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// N bytes (a multiple of 16) from global to shared memory, counted on `bar`
+__device__ __forceinline__ void bulk_load(uint32_t dst, const uint8_t* src, uint32_t n, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(n), "r"(bar) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_n(uint32_t dst, const uint8_t* src) {
+  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+template <int N>  // N bytes of shared memory as words
+__device__ __forceinline__ void lds_words(const uint8_t* src, uint32_t (&w)[N / 4]) {
+  if constexpr (N == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(src);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(src);
+  }
+}
+
+// ----------------------------------------------------------------------------- kernel
+// SPLIT: F32 Q; Q and the weights then go as a sum of two f16 parts, each product twice.  Else Q is
+// F16 or BF16 (p.q_bf16).
+// ROWS: tiles of 16 consecutive attended rows of any pages, gathered row by row; else tiles are 16
+// rows of one page (page size a multiple of 16), copied whole.
+template <int SB, bool SPLIT, int D, bool MQ, bool ROWS, int NW, int BLOCKS>
+__global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid_constant__ DecodeParams p) {
+  using T = MxTile<SB, D, ROWS>;
+  constexpr int NT = NW * 32;
+  constexpr int KT = T::KT, KCH = T::KCH, KB = T::KB, VB = T::VB, RL = T::RL, NQ = T::NQ, NST = T::NST;
+  constexpr int RB = T::RB, NB = T::NB, SR = T::SR;
+  constexpr int KW = KB / 4;  // words
+  extern __shared__ uint8_t s_raw[];
+  __shared__ PartEntry s_part[NW][2];              // each warp's partial states: first, last segment
+  __shared__ float s_plse[NW][2][kMaxGroupPerCta]; // their lse
+  __shared__ int s_last[2 * NW];
+  __shared__ WorkerStart s_start[NW];
+  __shared__ __align__(8) uint64_t s_bar[NW][NST];
+  __shared__ int2 s_meta[NW][NST][NQ];  // of a tile: attended rows [lo, hi) (bits 0-7, 8-15), first row's index
+  // ROWS: which rows of a stage count; of rows with two scale bytes, which half of the copied word
+  // holds K's and V's
+  constexpr int NH = NQ > 1 ? NQ / 2 : 1;
+  __shared__ unsigned s_rowok[ROWS ? NW : 1][ROWS ? NST : 1][ROWS ? NH : 1][3];
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint8_t* const rings = s_raw + (((smem_u32(s_raw) + 127u) & ~127u) - smem_u32(s_raw));
+  const uint32_t bar0 = smem_u32(&s_bar[warp][0]);
+  uint8_t* const my_ring = rings + warp * T::kRing;
+  const uint32_t ring = smem_u32(my_ring);
+  // the rings' space before the first fill: scratch of the start-up scan; after a warp's last
+  // tile, its part: the state of its last segment
+  static_assert(NW * T::kRing >= kStartCacheB * 4, "scratch");
+  int* const s_units = reinterpret_cast<int*>(rings);
+  auto state_of = [&](int w, int side) -> float* {
+    return reinterpret_cast<float*>(side ? rings + w * T::kRing : rings + NW * T::kRing + w * T::kState);
+  };
+  if (threadIdx.x == 0) {
+    prefetch_l2_share(p.Q, (size_t)p.B * p.q_len * p.H_qo * D * (SPLIT ? 4 : 2), blockIdx.x, gridDim.x);
+    if (p.values) prefetch_l2_share(p.values, (size_t)p.nnz_pages * sizeof(int32_t), blockIdx.x, gridDim.x);
+  }
+  if (lane == 0) {
+    // arrivals: of a stage's tiles, one each (with the bytes of its copies); ROWS: of every lane's copies
+    for (int i = 0; i < NST; ++i) mbar_init(bar0 + i * 8, ROWS ? 32 : NQ);
+    mbar_init_fence();
+  }
+  // With a host plan the start-up reads launch parameters alone and runs under the tail of the
+  // kernel before; otherwise, as everywhere, nothing of the caller's is read before it completes.
+  bool waited = false;
+  if (!p.early_inputs && !p.hp_B) {
+    pdl_wait();
+    pdl_release();
+    waited = true;
+  }
+  worker_starts<NT, NW>(p, s_start, s_units);
+  // the scan's shared memory accesses before the fills that overwrite its scratch
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  if (lane < 2) s_part[warp][lane].b = -1;
+  __syncthreads();  // no block-wide barrier until every warp has finished its range
+
+  const int g_id = lane >> 2, q4 = lane & 3;
+  const WorkerStart ws = s_start[warp];
+  const int P = p.P;
+  const int zg = p.mode == kSchedBalanced ? p.zg : 1;
+
+  Segment sg;
+  sg.b = max(ws.b, 0);  // (ws.b < 0: no units for this worker)
+  sg.hz = ws.hz;
+  sg.off = ws.off;
+  sg.seq = load_seq(p, sg.b);
+  sg.n = units_of(sg.seq, P);
+  const int C = p.mode == kSchedBalanced ? p.seg_cost : 0;
+  const long long cx1 = p.mode != kSchedPerSegment ? ws.x1 : sg.off + sg.n;
+
+  // this thread's fragment rows (+ 8: the second half)
+  const int kr = mx_row(g_id);
+  const int vr[2] = {mx_row(2 * q4), mx_row(2 * q4 + 1)};
+
+  // The ring: NQ tiles at a time are filled into stage `ist` and read from stage `cst`, in order.
+  int ist = 0, cst = 0;
+  uint32_t cph = 0;   // parity of the fill that stage cst waits for
+  bool dead = false;  // a wait ran out: no further fills
+  if (!p.early_inputs && !waited) {
+    pdl_wait();
+    pdl_release();
+    waited = true;
+  }
+
+  while (ws.b >= 0) {
+  const int ua = (int)min(max(ws.x0 - sg.off - C, 0ll), (long long)sg.n);
+  const int ub = (int)min(max(cx1 - sg.off - C, 0ll), (long long)sg.n);
+  if (ua < ub) {
+  const int hk = sg.hz / p.n_z, z = sg.hz - (sg.hz / p.n_z) * p.n_z;
+  const Pieces pcs = make_pieces(0, sg.seq.L, sg.seq, P);
+  const int pend = min(ub, sg.seq.L > 0 ? pcs.count() : 0);
+  const int c0 = z * kMaxGroupPerCta;
+  const int hcount = min(kMaxGroupPerCta, p.ncol - c0);
+
+  // Raw Q of column g_id at this lane's B-fragment dims (2 KB of them from 2 KB (4 c + q4)), loaded first
+  const bool have_q = g_id < hcount;
+  constexpr int QV = SPLIT ? KB / 2 : KB / 4;  // 16-byte loads per chunk
+  uint4 qraw[KCH][QV];
+  {
+    constexpr int QB = SPLIT ? 4 : 2;
+    const uint8_t* qrow = reinterpret_cast<const uint8_t*>(p.Q) +
+                          col_row<MQ>(p, sg.b, hk, c0 + (have_q ? g_id : 0)) * (D * QB);
+#pragma unroll
+    for (int c = 0; c < KCH; ++c)
+#pragma unroll
+      for (int i = 0; i < QV; ++i)
+        qraw[c][i] = have_q ? __ldg(reinterpret_cast<const uint4*>(qrow + 2 * KB * QB * (4 * c + q4)) + i)
+                            : make_uint4(0u, 0u, 0u, 0u);
+  }
+  int lim0 = 0, lim1 = 0, lim_all = INT_MAX;  // attended-row limits of this lane's score columns, and the least
+  if constexpr (MQ) {
+    const int cc = c0 + 2 * q4;
+    lim_all = sg.seq.L - p.q_len + 1;
+    lim0 = lim_all + cc / p.group;
+    lim1 = lim_all + (cc + 1) / p.group;
+  }
+
+  // ---------------------------------------------------------------- tile stream
+  // The share's pieces are whole pages of at most two runs of attended offsets (A: the sinks,
+  // or every row; B: the window), so its tiles are the multiples of 16 of each run in order.
+  // Tiles come 32 at a time: lane i holds tile 32 m + i and issues it; the page ids of the
+  // next 32 are loaded meanwhile.
+  const int a_lo = max(pcs.ra0, (pcs.pa + min(ua, pcs.na)) * P), a_hi = min(pcs.ra1, (pcs.pa + min(pend, pcs.na)) * P);
+  const int b_lo = max(pcs.ob0, (pcs.pb + max(ua - pcs.na, 0)) * P), b_hi = min(pcs.ob1, (pcs.pb + max(pend - pcs.na, 0)) * P);
+  const int n_a = a_hi <= a_lo ? 0 : ROWS ? a_hi - a_lo : ((a_hi + 15) >> 4) - (a_lo >> 4);
+  const int n_b = b_hi <= b_lo ? 0 : ROWS ? b_hi - b_lo : ((b_hi + 15) >> 4) - (b_lo >> 4);
+  const int n_tiles = ROWS ? (n_a + n_b + 15) >> 4 : n_a + n_b;  // (ROWS: n_a, n_b count rows)
+  auto tile_at = [&](int k) { return k < n_a ? ((a_lo >> 4) + k) << 4 : ((b_lo >> 4) + k - n_a) << 4; };  // offset
+  auto load_page = [&](int k) -> int {  // page id of tile k, unchecked; -1 out of the table
+    if (k >= n_tiles) return -1;
+    const int pidx = tile_at(k) / P;
+    return pidx < sg.seq.npages && (long long)sg.seq.page_begin + pidx < p.nnz_pages
+               ? __ldg(p.values + sg.seq.page_begin + pidx) : -1;
+  };
+  int t_page = -1, t_row = 0, t_span = 0, t_r0 = 0, page_next = ROWS ? -1 : load_page(lane);
+  auto load_batch = [&](int k0) {  // tiles k0 .. k0 + 31
+    const int k = k0 + lane, page = page_next;
+    page_next = load_page(k + 32);
+    const int o = tile_at(k);
+    const bool in_a = k < n_a;
+    t_row = o % P;
+    t_span = max((in_a ? a_lo : b_lo) - o, 0) | (min((in_a ? a_hi : b_hi) - o, 16) << 8);
+    t_r0 = in_a ? o : o - pcs.shift;
+    t_page = page;
+    if (page < 0 || page >= p.max_pages) {
+      if (k < n_tiles) set_error(p.err, kErrBadPage);
+      t_page = -1;  // no such tile, or its rows do not count
+    }
+  };
+  // ROWS: the page (unchecked; -1 out of the table) and slot of a lane's rows 32 h + lane of the
+  // stage that starts with tile k, loaded one stage ahead (NQ 1: 16 rows, of the first 16 lanes)
+  int rw_page[NH], rw_slot[NH];
+  auto load_rows = [&](int k) {
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const int i = k * 16 + 32 * h + lane;
+      rw_page[h] = rw_slot[h] = -1;
+      if (i < n_a + n_b && (NQ > 1 || lane < 16)) {
+        const int o = i < n_a ? a_lo + i : b_lo + i - n_a, pidx = o / P;
+        rw_slot[h] = o - pidx * P;
+        if (pidx < sg.seq.npages && (long long)sg.seq.page_begin + pidx < p.nnz_pages)
+          rw_page[h] = __ldg(p.values + sg.seq.page_begin + pidx);
+      }
+    }
+  };
+  if constexpr (ROWS) load_rows(0);
+  // its rows -> stage ist: RB / 16 lanes copy a row's 16-byte chunks, the row's own lane its scales
+  auto issue_rows = [&](int k) {
+    constexpr int CPR = RB / 16, RPI = 32 / CPR;  // chunks per row, rows per instruction
+    const long long to_v = (long long)p.H_kv * P;  // rows
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const int page = rw_page[h], slot = rw_slot[h];
+      const bool ok = page >= 0 && page < p.max_pages;
+      if (slot >= 0 && !ok) set_error(p.err, kErrBadPage);  // its row does not count
+      const unsigned rows = __ballot_sync(0xffffffffu, ok);
+      const long long row = ((long long)page * 2 * p.H_kv + hk) * P + slot;  // of K
+      const uint32_t tile = ring + ist * T::kStage + (2 * h + (lane >> 4)) * T::kPair;
+      unsigned kpar = 0, vpar = 0;
+      if constexpr (NB < 4) {  // the aligned word that holds the row's two bytes
+        kpar = __ballot_sync(0xffffffffu, ok && (row & 1));
+        vpar = __ballot_sync(0xffffffffu, ok && ((row + to_v) & 1));
+      }
+      if (lane == 0) {
+        s_rowok[warp][ist][h][0] = rows;
+        s_rowok[warp][ist][h][1] = kpar;
+        s_rowok[warp][ist][h][2] = vpar;
+      }
+      if (ok) {
+        const uint32_t dst = tile + 2 * T::kCodes + (lane & 15) * SR;
+        const long long kw = NB < 4 ? row >> 1 : row, vw = NB < 4 ? (row + to_v) >> 1 : row + to_v;
+        cp_async_n<SR>(dst, p.mx_scales + kw * SR);
+        cp_async_n<SR>(dst + T::kScales, p.mx_scales + vw * SR);
+      }
+#pragma unroll
+      for (int it = 0; it < (NQ > 1 ? CPR : CPR / 2); ++it) {
+        const int r = it * RPI + lane / CPR, x = lane % CPR * 16;  // row of the 32, byte of it
+        const long long src_row = __shfl_sync(0xffffffffu, row, r);
+        if ((rows >> r) & 1) {
+          const uint8_t* src = reinterpret_cast<const uint8_t*>(p.pages) + src_row * RB + x;
+          const uint32_t dst = ring + ist * T::kStage + (2 * h + (r >> 4)) * T::kPair + (r & 15) * RB + x;
+          cp_async_chunk(dst, src);
+          cp_async_chunk(dst + T::kCodes, src + to_v * RB);
+        }
+      }
+    }
+    mbar_arrive_cp_async(bar0 + ist * 8);
+    ist = ist + 1 == NST ? 0 : ist + 1;
+    load_rows(k + NQ);
+  };
+  // tiles k .. k + NQ - 1 (the next in order; their lanes side by side) -> stage ist
+  auto issue = [&](int k) {
+    if constexpr (ROWS) return issue_rows(k);
+    if ((k & 31) == 0) load_batch(k);
+    const int i = lane - (k & 31);
+    if ((unsigned)i < (unsigned)NQ) {
+      const uint32_t bar = bar0 + ist * 8, dst = ring + ist * T::kStage + i * T::kPair;
+      s_meta[warp][ist][i] = t_page >= 0 ? make_int2(t_span, t_r0) : make_int2(0, 0);
+      if (t_page >= 0) {
+        const long long row = ((long long)t_page * 2 * p.H_kv + hk) * P + t_row, to_v = (long long)p.H_kv * P;
+        const uint8_t* codes = reinterpret_cast<const uint8_t*>(p.pages) + row * RB;
+        const uint8_t* scales = p.mx_scales + row * NB;
+        mbar_arrive_expect_tx(bar, T::kPair);
+        bulk_load(dst, codes, T::kCodes, bar);
+        bulk_load(dst + T::kCodes, codes + to_v * RB, T::kCodes, bar);
+        bulk_load(dst + 2 * T::kCodes, scales, T::kScales, bar);
+        bulk_load(dst + 2 * T::kCodes + T::kScales, scales + to_v * NB, T::kScales, bar);
+      } else {  // no attended row
+        mbar_arrive(bar);
+      }
+    }
+    ist = ist + 1 == NST ? 0 : ist + 1;
+  };
+
+  if (!waited) {  // pages and scales may still be written by the previous kernel until here
+    pdl_wait();
+    pdl_release();
+    waited = true;
+  }
+  [[maybe_unused]] const int r_first = n_a ? a_lo : b_lo - pcs.shift;  // attended index of the share's first row
+  // tiles are computed NQ at a time: the last few may be empty ones
+  int k_issued = 0, k_end = dead ? 0 : (n_tiles + NQ - 1) / NQ * NQ;
+#pragma unroll 1
+  for (; k_issued < min(NST * NQ, k_end); k_issued += NQ) issue(k_issued);
+
+  // ---------------------------------------------------------------- Q^T B fragments
+  // k-tile kt = 2 (KW c + w) + h: dims 2 KB (4 c + q4) + 8 w + 4 h + {0, 1} and + {2, 3} of column g_id,
+  // times 2^(14 - e), e the exponent of the column's largest magnitude, and the sign of sm_scale
+  uint32_t qf[KT][2];
+  [[maybe_unused]] uint32_t ql[SPLIT ? KT : 1][2];
+  float cs0, cs1;  // column factors of this lane's score columns: 2^(e - 14) |sm_scale| log2(e) k_scale
+  {
+    auto four = [&](int kt) -> float4 {  // this lane's four dims of k-tile kt
+      const int c = kt / (2 * KW), i = kt % (2 * KW);
+      if constexpr (SPLIT) {
+        const uint4 v = qraw[c][i];
+        return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+      } else {
+        const uint32_t x = comp(qraw[c][i >> 1], 2 * (i & 1)), y = comp(qraw[c][i >> 1], 2 * (i & 1) + 1);
+        const float2 a = p.q_bf16 ? unpack2<__nv_bfloat16>(x) : unpack2<__half>(x);
+        const float2 b = p.q_bf16 ? unpack2<__nv_bfloat16>(y) : unpack2<__half>(y);
+        return make_float4(a.x, a.y, b.x, b.y);
+      }
+    };
+    float amax = 0.f;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      const float4 f = four(kt);
+      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // 2^(14 - e) and its inverse, both normal: e is kept in [-100, 126]
+    const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255) - 127, -100), 126);
+    const float up = copysignf(__uint_as_float((unsigned)(127 + 14 - e) << 23), p.score_scale);
+    const float cs = __uint_as_float((unsigned)(127 - 14 + e) << 23) * fabsf(p.score_scale);
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      const float4 f = four(kt);
+      if constexpr (SPLIT) {
+        split2<__half>(f.x * up, f.y * up, qf[kt][0], ql[kt][0]);
+        split2<__half>(f.z * up, f.w * up, qf[kt][1], ql[kt][1]);
+      } else {
+        qf[kt][0] = pack2<__half>(f.x * up, f.y * up);
+        qf[kt][1] = pack2<__half>(f.z * up, f.w * up);
+      }
+    }
+    cs0 = __shfl_sync(0xffffffffu, cs, 8 * q4);      // column 2 q4
+    cs1 = __shfl_sync(0xffffffffu, cs, 8 * q4 + 4);  // column 2 q4 + 1
+  }
+
+  // The running maxima m are of the products before the column's factor cs (>= 0); weights are
+  // 2^(cs s + nm) with nm = kWeightUp - cs m
+  float st_m[2] = {-FLT_MAX, -FLT_MAX}, nm[2] = {0.f, 0.f}, st_d[2] = {0.f, 0.f};
+  const float over0 = kLazyMaxMx / cs0, over1 = kLazyMaxMx / cs1;  // (cs 0: the maximum never moves)
+  float oacc[KT][4];
+#pragma unroll
+  for (int i = 0; i < KT; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
+
+  // NQ tiles from the ring: their chains of loads, products and exponentials are independent and
+  // overlap in the warp, and share the vote and the rescale
+  __syncwarp();  // (what the issuing lanes wrote beside their copies)
+#pragma unroll 1
+  for (int k = 0; k < k_end; k += NQ) {
+    const bool ok = mbar_wait(bar0 + cst * 8, cph, dead ? 1024u : kWaitPolls);
+    const uint8_t* const stage = my_ring + cst * T::kStage;
+    float sc[NQ][4];
+    // a row's scale bytes in shared memory (v: of V)
+    auto scales_at = [&](int i, int r, bool v) -> const uint8_t* {
+      const uint8_t* at = stage + i * T::kPair + 2 * T::kCodes + (v ? T::kScales : 0) + r * SR;
+      if constexpr (ROWS && NB < 4) at += ((s_rowok[warp][cst][i >> 1][v ? 2 : 1] >> (16 * (i & 1) + r)) & 1) * NB;
+      return at;
+    };
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      // -------------------------------------------------------------- S^T = K Q^T
+      const uint8_t* kt_base = stage + i * T::kPair + kr * RB + KB * q4;
+      const uint8_t* sa = scales_at(i, kr, false);
+      const uint8_t* sb = scales_at(i, kr + 8, false);
+      sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < KCH; ++c) {
+        uint32_t ka[KW], kb[KW];
+        lds_words<KB>(kt_base + 4 * KB * c, ka);
+        lds_words<KB>(kt_base + 8 * RB + 4 * KB * c, kb);
+        constexpr int BPC = 2 * KB > SB ? 2 * KB / SB : 1;  // blocks of a chunk
+        const int blk = 2 * KB * (4 * c + q4) / SB;
+        uint32_t fa[2], fb[2];  // their scales, twice each
+        if constexpr (BPC == 2) {
+          const uint32_t a = mx_scales<SB>(*reinterpret_cast<const uint16_t*>(sa + blk));
+          const uint32_t b = mx_scales<SB>(*reinterpret_cast<const uint16_t*>(sb + blk));
+          fa[0] = __byte_perm(a, a, 0x1010), fa[1] = __byte_perm(a, a, 0x3232);
+          fb[0] = __byte_perm(b, b, 0x1010), fb[1] = __byte_perm(b, b, 0x3232);
+        } else {
+          const uint32_t ab = mx_scales<SB>(sa[blk] | ((uint32_t)sb[blk] << 8));
+          fa[0] = fa[1] = __byte_perm(ab, ab, 0x1010);
+          fb[0] = fb[1] = __byte_perm(ab, ab, 0x3232);
+        }
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint32_t ra[4], rb[4];
+          mx_codes(ka[w], ra);
+          mx_codes(kb[w], rb);
+          const int f = BPC == 2 ? 2 * w / KW : 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int kt = 2 * (KW * c + w) + h;
+            const uint32_t a[4] = {mul_h2(ra[2 * h], fa[f]), mul_h2(rb[2 * h], fb[f]),
+                                   mul_h2(ra[2 * h + 1], fa[f]), mul_h2(rb[2 * h + 1], fb[f])};
+            Mma<__half>::run(sc[i], a, qf[kt][0], qf[kt][1]);
+            if constexpr (SPLIT) Mma<__half>::run(sc[i], a, ql[kt][0], ql[kt][1]);
+          }
+        }
+      }
+    }
+    // ---------------------------------------------------------------- online softmax (log2)
+    unsigned rows[NQ];  // bit r: row r counts
+    int r0[NQ];         // MQ: attended index of the tile's first row
+    bool whole = true;  // every row of the stage counts for every column
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      if constexpr (ROWS) {
+        rows[i] = (s_rowok[warp][cst][i >> 1][0] >> (16 * (i & 1))) & 0xffffu;
+        r0[i] = r_first + (k + i) * 16;
+      } else {
+        const int2 m = s_meta[warp][cst][i];
+        rows[i] = ((1u << (m.x >> 8)) - 1) & ~((1u << (m.x & 0xff)) - 1);
+        r0[i] = m.y;
+      }
+      whole = whole && rows[i] == 0xffffu && (!MQ || r0[i] + 16 <= lim_all);
+    }
+    // whether row r of tile i counts for this lane's column 2 q4 + h
+    auto counts = [&](int i, int r, int h) {
+      return ((rows[i] >> r) & 1) && (!MQ || r0[i] + r < (h ? lim1 : lim0));
+    };
+    float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      if (!whole) {  // (warp-uniform)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!counts(i, kr + (e >> 1) * 8, e & 1)) sc[i][e] = -INFINITY;
+      }
+      t0 = fmaxf(t0, fmaxf(sc[i][0], sc[i][2]));
+      t1 = fmaxf(t1, fmaxf(sc[i][1], sc[i][3]));
+    }
+    if (__any_sync(0xffffffffu, t0 - st_m[0] > over0 || t1 - st_m[1] > over1 || !ok)) {
+      if (__any_sync(0xffffffffu, !ok)) {
+        dead = true;  // the tiles in flight are still waited for; the error word says the rest
+        k_end = k_issued;
+        if (lane == 0) set_error(p.err, kErrTimeout);
+      }
+      const float mn0 = fmaxf(st_m[0], max_over_groups(t0)), mn1 = fmaxf(st_m[1], max_over_groups(t1));
+      const float a0 = fast_exp2((st_m[0] - mn0) * cs0), a1 = fast_exp2((st_m[1] - mn1) * cs1);
+      st_d[0] *= a0;
+      st_d[1] *= a1;
+      st_m[0] = mn0;
+      st_m[1] = mn1;
+      nm[0] = fmaf(-mn0, cs0, kWeightUp);
+      nm[1] = fmaf(-mn1, cs1, kWeightUp);
+#pragma unroll
+      for (int mt = 0; mt < KT; ++mt) {
+        oacc[mt][0] *= a0;
+        oacc[mt][1] *= a1;
+        oacc[mt][2] *= a0;
+        oacc[mt][3] *= a1;
+      }
+    }
+    uint32_t pb[NQ][2];
+    [[maybe_unused]] uint32_t pl[SPLIT ? NQ : 1][2];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      float pr[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        pr[e] = fast_exp2(fmaf(sc[i][e], e & 1 ? cs1 : cs0, nm[e & 1]));
+        if (!whole && sc[i][e] == -INFINITY) pr[e] = 0.f;  // (whatever cs and nm are)
+      }
+      st_d[0] += pr[0] + pr[2];
+      st_d[1] += pr[1] + pr[3];
+      // P^T as a B fragment: rows 2 q4, 2 q4 + 1 (+ 8) of column g_id
+      if constexpr (SPLIT) {
+        uint32_t hi, lo;
+        split2<__half>(pr[0], pr[1], hi, lo);
+        pb[i][0] = transpose8(hi);
+        pl[i][0] = transpose8(lo);
+        split2<__half>(pr[2], pr[3], hi, lo);
+        pb[i][1] = transpose8(hi);
+        pl[i][1] = transpose8(lo);
+      } else {
+        pb[i][0] = transpose8(pack2<__half>(pr[0], pr[1]));
+        pb[i][1] = transpose8(pack2<__half>(pr[2], pr[3]));
+      }
+    }
+    // ---------------------------------------------------------------- O^T += V^T P^T
+    // m-tile mt: rows g_id / g_id + 8 are dims RL g_id + 2 mt / + 1
+    constexpr int VBL = RL > SB ? RL / SB : 1;  // blocks of a thread's dims
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const uint8_t* vt = stage + i * T::kPair + T::kCodes + VB * g_id;
+      uint32_t v[4][VB / 4];  // rows vr[0], vr[1], vr[0] + 8, vr[1] + 8
+      uint32_t sv[2][VBL];    // scales of rows (vr[0], vr[1]) and of the same + 8
+#pragma unroll
+      for (int j = 0; j < 4; ++j) lds_words<VB>(vt + (vr[j & 1] + 8 * (j >> 1)) * RB, v[j]);
+#pragma unroll
+      for (int b = 0; b < VBL; ++b)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int blk = RL * g_id / SB + b;
+          uint32_t x = mx_scales<SB>(scales_at(i, vr[0] + 8 * j, true)[blk] |
+                                     ((uint32_t)scales_at(i, vr[1] + 8 * j, true)[blk] << 8));
+          if (!whole) {
+            // rows outside may have any scale (NaN): 0
+            if (!((rows[i] >> (vr[0] + 8 * j)) & 1)) x &= 0xffff0000u;
+            if (!((rows[i] >> (vr[1] + 8 * j)) & 1)) x &= 0x0000ffffu;
+          }
+          sv[j][b] = x;
+        }
+      if constexpr (MQ) {
+        if (!whole) {
+          // A row that some of the queries do not attend must not reach them by a NaN scale: such
+          // scales go to 0 here, and to the outputs of the queries that do attend the row
+          auto is_nan = [](uint32_t s) { return (s & 0x7fffu) > 0x7c00u || (s & 0x7fff0000u) > 0x7c000000u; };
+          bool any = false;
+#pragma unroll
+          for (int b = 0; b < VBL; ++b) any = any || is_nan(sv[0][b]) || is_nan(sv[1][b]);
+          if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+            for (int b = 0; b < VBL; ++b) {
+              const int blk = RL * g_id / SB + b;
+              bool bad0 = false, bad1 = false;
+#pragma unroll 1
+              for (int r = 0; r < 16; ++r) {
+                if (!is_nan(mx_scales<SB>(scales_at(i, r, true)[blk]) & 0xffffu)) continue;
+                bad0 = bad0 || counts(i, r, 0);
+                bad1 = bad1 || counts(i, r, 1);
+              }
+#pragma unroll
+              for (int mt = b * KT / VBL; mt < (b + 1) * KT / VBL; ++mt) {
+                if (bad0) oacc[mt][0] = oacc[mt][2] = __int_as_float(0x7fc00000);
+                if (bad1) oacc[mt][1] = oacc[mt][3] = __int_as_float(0x7fc00000);
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                if (is_nan(sv[j][b] & 0xffffu)) sv[j][b] &= 0xffff0000u;
+                if (is_nan(sv[j][b] & 0xffff0000u)) sv[j][b] &= 0x0000ffffu;
+              }
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < VB / 4; ++w) {
+        // codes of rows (0, 1) and (2, 3) side by side in a byte: even dims, odd dims
+        constexpr uint32_t M = 0x0f0f0f0fu;
+        uint32_t ev[2][4], od[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t x = v[2 * j][w], y = v[2 * j + 1][w];
+          mx_codes((x & M) | ((y << 4) & ~M), ev[j]);
+          mx_codes(((x >> 4) & M) | (y & ~M), od[j]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int mt = 4 * w + u, b = mt * VBL / KT;
+          const uint32_t a[4] = {mul_h2(ev[0][u], sv[0][b]), mul_h2(od[0][u], sv[0][b]),
+                                 mul_h2(ev[1][u], sv[1][b]), mul_h2(od[1][u], sv[1][b])};
+          Mma<__half>::run(oacc[mt], a, pb[i][0], pb[i][1]);
+          if constexpr (SPLIT) Mma<__half>::run(oacc[mt], a, pl[i][0], pl[i][1]);
+        }
+      }
+    }
+    // every lane has its codes in registers: the stage takes the next tiles
+    cst = cst + 1 == NST ? 0 : cst + 1;
+    if (cst == 0) cph ^= 1;
+    __syncwarp();
+    if (k_issued < k_end) {
+      issue(k_issued);
+      k_issued += NQ;
+    }
+  }
+  st_d[0] = sum_over_groups(st_d[0]);
+  st_d[1] = sum_over_groups(st_d[1]);
+
+  // ---------------------------------------------------------------- finish the segment
+  // This thread holds columns 2 q4 (o0, o2) and 2 q4 + 1 (o1, o3), dims RL g_id .. + RL - 1.
+  // A segment within the range goes to out/lse; else its state (O / d, lse) waits in shared
+  // memory for the block's other warps.
+  const bool all = (ua == 0 && ub == sg.n);
+  const int side = sg.off <= ws.x0 ? 0 : 1;
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) {
+    const int j = 2 * q4 + hh;
+    if (j < hcount) {
+      const bool empty = st_d[hh] == 0.f;
+      float inv = empty ? 0.f : p.out_scale / st_d[hh];
+      float l = empty ? kEmptyM : log2f(st_d[hh]) - nm[hh];
+      const size_t row = col_row<MQ>(p, sg.b, hk, c0 + j);
+      if (all && p.sink) {
+        const SinkAdj sa = apply_sink(p, col_head<MQ>(p, hk, c0 + j), l);
+        inv *= sa.scale;
+        l = sa.lse;
+      }
+#pragma unroll
+      for (int o = 0; o < RL / 4; ++o) {
+        const float4 v = make_float4(oacc[2 * o][hh] * inv, oacc[2 * o][hh + 2] * inv,
+                                     oacc[2 * o + 1][hh] * inv, oacc[2 * o + 1][hh + 2] * inv);
+        if (all) store_four(p, row * D + RL * g_id + 4 * o, v);
+        else reinterpret_cast<float4*>(state_of(warp, side) + j * D + RL * g_id)[o] = v;
+      }
+      if (g_id == 0) {
+        if (all) p.lse[row] = l;
+        else s_plse[warp][side][j] = l;
+      }
+    }
+  }
+  if (!all && lane == 0) s_part[warp][side] = PartEntry{sg.off, sg.b, sg.hz, ub - ua, sg.n, hk, c0, hcount};
+  }  // ua < ub
+  if (sg.off + C + sg.n >= cx1 || !next_segment(p, sg, C)) break;
+  }  // segments
+  if (!waited) pdl_wait();  // (a worker without units: the block's partials still follow it)
+
+  merge_parts<D, MQ, NW>(p, s_part, s_plse, s_last, s_start[0], C, zg, state_of);
+}
+
+// ----------------------------------------------------------------------------- launch
+template <int SB, bool SPLIT, int D, bool MQ, bool ROWS>
+static cudaError_t launch_mx_t(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg) {
+  constexpr int NW = kMmaWarps;
+  constexpr int BLOCKS = SPLIT || D == 256 ? 2 : 3;
+  constexpr int dyn = mx_smem_bytes<SB, D, ROWS, NW>();
+  auto kern = decode_mx_kernel<SB, SPLIT, D, MQ, ROWS, NW, BLOCKS>;
+  // the dynamic shared memory above 48 KB is opted into on every query of the launch
+  // configuration, which the host makes once per device and variant before the first launch
+  if (cfg) {
+    cfg->threads = NW * 32;
+    cfg->smem_bytes = dyn;
+    int n = 0;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, NW * 32, dyn);
+    if (e != cudaSuccess) return e;
+    cfg->ctas_per_sm = n;
+    return cudaSuccess;
+  }
+  return launch_pdl(kern, grid, dim3(NW * 32), dyn, st, p);
+}
+
+template <int SB, bool SPLIT, int D, bool ROWS>
+static cudaError_t launch_mx_q(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg) {
+  return p.q_len > 1 ? launch_mx_t<SB, SPLIT, D, true, ROWS>(p, grid, st, cfg)
+                     : launch_mx_t<SB, SPLIT, D, false, ROWS>(p, grid, st, cfg);
+}
+
+// Tiles copied whole: 16-bit Q, D 64 or 128.
+template <int SB>
+static cudaError_t launch_mx_tiles(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg) {
+  return p.D == 128 ? launch_mx_q<SB, false, 128, false>(p, grid, st, cfg)
+                    : launch_mx_q<SB, false, 64, false>(p, grid, st, cfg);
+}
+// Row by row.
+template <int SB, bool SPLIT>
+static cudaError_t launch_mx_rows(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg) {
+  switch (p.D) {
+    case 64: return launch_mx_q<SB, SPLIT, 64, true>(p, grid, st, cfg);
+    case 128: return launch_mx_q<SB, SPLIT, 128, true>(p, grid, st, cfg);
+    case 256: return launch_mx_q<SB, SPLIT, 256, true>(p, grid, st, cfg);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pd

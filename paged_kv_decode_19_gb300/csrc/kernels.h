@@ -93,6 +93,50 @@ struct AppendBsParams {
 };
 cudaError_t launch_append_bs(const AppendBsParams& a, int D, int in_dtype, int kv_dtype, cudaStream_t st);
 
+// 4-bit cache (e2m1 codes; sb dims share a scale: 16 e4m3, 32 e8m0): the append ...
+struct AppendMxParams {
+  uint8_t* pages;
+  uint8_t* scales;
+  const void* k_new;
+  const void* v_new;
+  const int64_t* slots;
+  unsigned* err;
+  long long k_stride, v_stride;  // elements from token to token
+  long long n_slots;             // max_pages * P
+  float k_scale, v_scale;
+  int T, H_kv, P;
+};
+cudaError_t launch_append_mx(const AppendMxParams& a, int D, int sb, int in_dtype, int num_sms, cudaStream_t st);
+// ... and the decode (decode_mx.cuh): 16-bit Q (p.q_bf16), D 64 or 128, page size a multiple of 16
+// (tiles copied whole); or 16-bit / F32 Q, any D and page size, tiles gathered row by row.
+cudaError_t launch_mx_e4m3(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_mx_e8m0(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_mx_rows_e4m3(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_mx_rows_e8m0(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_mx_f32_e4m3(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_mx_f32_e8m0(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
+
+// build_page_tables
+constexpr int kTableThreads = 512;
+constexpr int kMaxTableB = 8192;  // requests: five ints each in shared memory
+struct TableParams {
+  int32_t* table;      // [B, max_pages], rows table_stride apart
+  int32_t* lengths;
+  const int32_t* new_tokens;
+  long long* state;    // ring head, ring tail, ticket, unused
+  int32_t* ring;       // [C] free pages, or nullptr: the table holds its pages
+  int32_t* indptr;
+  int32_t* values;
+  int32_t* length_info;
+  int32_t* append_indptr;
+  int64_t* slots;      // [T]
+  int32_t* positions;  // [T]
+  unsigned* err;
+  long long table_stride;
+  int B, P, max_pages, max_rows, window, sinks, values_cap, C, T, most_tokens;
+};
+cudaError_t launch_page_tables(const TableParams& a, int num_sms, cudaStream_t st);
+
 // qk_norm_rope
 struct QkParams {
   const void* q;
