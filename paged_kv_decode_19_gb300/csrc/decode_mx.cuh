@@ -41,10 +41,19 @@ struct MxTile {
 template <int SB, int D, bool ROWS, int NW>
 constexpr int mx_smem_bytes() { return NW * (MxTile<SB, D, ROWS>::kRing + MxTile<SB, D, ROWS>::kState) + 128; }
 
-// Row of the tile that fragment row g (0..7; g + 8: the row + 8) holds.  Rows 2i and 2i + 1 of K, read
-// by one phase of lanes, lie in both halves of a 128-byte line (D 128); of the four rows of V that the
-// quad lanes read, two do.
-__device__ __forceinline__ int mx_row(int g) { return g ^ ((g >> 1) & 1); }
+// Row of the tile that fragment row g (0..7; g + 8: the row + 8) holds, and byte offset of the 16-byte
+// chunk c of row r of a tile in shared memory.  Chosen so that the rows of K that one phase of lanes
+// reads (those of g = 2i, 2i + 1; D 64: of four g), and the rows of V that the quad lanes read (those
+// of g = 0, 2, 4, 6, or of 1, 3, 5, 7), fall on different banks.
+template <int D>
+__device__ __forceinline__ int mx_row(int g) {
+  constexpr uint32_t order = D == 64 ? 0x53427160u : D == 128 ? 0x65217430u : 0x36147250u;
+  return (order >> (4 * g)) & 7;
+}
+template <int D>
+__device__ __forceinline__ int mx_chunk(int r, int c) {
+  return r * (D / 2) + ((D == 64 ? c : D == 128 ? c ^ ((r >> 1) & 3) : c ^ (r & 7)) << 4);
+}
 
 // A scale's f16 pair from two bytes in the low half of w.
 template <int SB>
@@ -74,16 +83,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-// N bytes (a multiple of 16) from global to shared memory, counted on `bar`
-__device__ __forceinline__ void bulk_load(uint32_t dst, const uint8_t* src, uint32_t n, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(dst), "l"(src), "r"(n), "r"(bar) : "memory");
-}
 template <int N>
 __device__ __forceinline__ void cp_async_n(uint32_t dst, const uint8_t* src) {
   if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
+__device__ __forceinline__ void cp_async_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but this thread's N most recent groups of copies have landed.
+template <int N>
+__device__ __forceinline__ void cp_async_group_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 template <int N>  // N bytes of shared memory as words
 __device__ __forceinline__ void lds_words(const uint8_t* src, uint32_t (&w)[N / 4]) {
   if constexpr (N == 16) {
@@ -114,16 +122,15 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   __shared__ float s_plse[NW][2][kMaxGroupPerCta]; // their lse
   __shared__ int s_last[2 * NW];
   __shared__ WorkerStart s_start[NW];
-  __shared__ __align__(8) uint64_t s_bar[NW][NST];
-  __shared__ int2 s_meta[NW][NST][NQ];  // of a tile: attended rows [lo, hi) (bits 0-7, 8-15), first row's index
-  // ROWS: which rows of a stage count; of rows with two scale bytes, which half of the copied word
-  // holds K's and V's
-  constexpr int NH = NQ > 1 ? NQ / 2 : 1;
-  __shared__ unsigned s_rowok[ROWS ? NW : 1][ROWS ? NST : 1][ROWS ? NH : 1][3];
+  // of each tile of a stage: which rows count (bit r: row r), and the attended index of row 0; of rows
+  // with two scale bytes that were copied one by one, which half of the copied word holds K's and V's
+  __shared__ __align__(8) uint16_t s_rows[NW][NST][NQ];
+  __shared__ int s_r0[MQ ? NW : 1][NST][NQ];
+  __shared__ uint16_t s_half[ROWS && NB < 4 ? NW : 1][2][NST][NQ];
+  constexpr int NH = NQ / 2;  // pairs of tiles
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint8_t* const rings = s_raw + (((smem_u32(s_raw) + 127u) & ~127u) - smem_u32(s_raw));
-  const uint32_t bar0 = smem_u32(&s_bar[warp][0]);
   uint8_t* const my_ring = rings + warp * T::kRing;
   const uint32_t ring = smem_u32(my_ring);
   // the rings' space before the first fill: scratch of the start-up scan; after a warp's last
@@ -137,11 +144,6 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     prefetch_l2_share(p.Q, (size_t)p.B * p.q_len * p.H_qo * D * (SPLIT ? 4 : 2), blockIdx.x, gridDim.x);
     if (p.values) prefetch_l2_share(p.values, (size_t)p.nnz_pages * sizeof(int32_t), blockIdx.x, gridDim.x);
   }
-  if (lane == 0) {
-    // arrivals: of a stage's tiles, one each (with the bytes of its copies); ROWS: of every lane's copies
-    for (int i = 0; i < NST; ++i) mbar_init(bar0 + i * 8, ROWS ? 32 : NQ);
-    mbar_init_fence();
-  }
   // With a host plan the start-up reads launch parameters alone and runs under the tail of the
   // kernel before; otherwise, as everywhere, nothing of the caller's is read before it completes.
   bool waited = false;
@@ -151,8 +153,6 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     waited = true;
   }
   worker_starts<NT, NW>(p, s_start, s_units);
-  // the scan's shared memory accesses before the fills that overwrite its scratch
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   if (lane < 2) s_part[warp][lane].b = -1;
   __syncthreads();  // no block-wide barrier until every warp has finished its range
 
@@ -170,14 +170,21 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   const int C = p.mode == kSchedBalanced ? p.seg_cost : 0;
   const long long cx1 = p.mode != kSchedPerSegment ? ws.x1 : sg.off + sg.n;
 
-  // this thread's fragment rows (+ 8: the second half)
-  const int kr = mx_row(g_id);
-  const int vr[2] = {mx_row(2 * q4), mx_row(2 * q4 + 1)};
+  // this thread's fragment rows (+ 8: the second half), and the byte offsets of what it reads of them
+  const int kr = mx_row<D>(g_id);
+  const int vr[2] = {mx_row<D>(2 * q4), mx_row<D>(2 * q4 + 1)};
+  int koff[KCH], voff[2];
+#pragma unroll
+  for (int c = 0; c < KCH; ++c) {
+    const int x = KB * (4 * c + q4);
+    koff[c] = mx_chunk<D>(kr, x >> 4) + (x & 15);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) voff[j] = T::kCodes + mx_chunk<D>(vr[j], VB * g_id >> 4) + (VB * g_id & 15);
 
-  // The ring: NQ tiles at a time are filled into stage `ist` and read from stage `cst`, in order.
+  // The ring: NQ tiles at a time are filled into stage `ist` and read from stage `cst`, in order, one
+  // group of copies a stage.
   int ist = 0, cst = 0;
-  uint32_t cph = 0;   // parity of the fill that stage cst waits for
-  bool dead = false;  // a wait ran out: no further fills
   if (!p.early_inputs && !waited) {
     pdl_wait();
     pdl_release();
@@ -227,6 +234,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   const int n_a = a_hi <= a_lo ? 0 : ROWS ? a_hi - a_lo : ((a_hi + 15) >> 4) - (a_lo >> 4);
   const int n_b = b_hi <= b_lo ? 0 : ROWS ? b_hi - b_lo : ((b_hi + 15) >> 4) - (b_lo >> 4);
   const int n_tiles = ROWS ? (n_a + n_b + 15) >> 4 : n_a + n_b;  // (ROWS: n_a, n_b count rows)
+  [[maybe_unused]] const int r_first = n_a ? a_lo : b_lo - pcs.shift;  // attended index of the share's first row
   auto tile_at = [&](int k) { return k < n_a ? ((a_lo >> 4) + k) << 4 : ((b_lo >> 4) + k - n_a) << 4; };  // offset
   auto load_page = [&](int k) -> int {  // page id of tile k, unchecked; -1 out of the table
     if (k >= n_tiles) return -1;
@@ -234,30 +242,33 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     return pidx < sg.seq.npages && (long long)sg.seq.page_begin + pidx < p.nnz_pages
                ? __ldg(p.values + sg.seq.page_begin + pidx) : -1;
   };
-  int t_page = -1, t_row = 0, t_span = 0, t_r0 = 0, page_next = ROWS ? -1 : load_page(lane);
+  // of this lane's tile: its K rows' place in the cache (-1: none), rows that count, first row's index
+  long long t_at = -1;
+  int t_rows = 0, t_r0 = 0, page_next = ROWS ? -1 : load_page(lane);
   auto load_batch = [&](int k0) {  // tiles k0 .. k0 + 31
     const int k = k0 + lane, page = page_next;
     page_next = load_page(k + 32);
     const int o = tile_at(k);
     const bool in_a = k < n_a;
-    t_row = o % P;
-    t_span = max((in_a ? a_lo : b_lo) - o, 0) | (min((in_a ? a_hi : b_hi) - o, 16) << 8);
+    auto below = [&](int end) { return (1 << min(max(end - o, 0), 16)) - 1; };  // the tile's rows before it
+    t_rows = below(in_a ? a_hi : b_hi) & ~below(in_a ? a_lo : b_lo);
     t_r0 = in_a ? o : o - pcs.shift;
-    t_page = page;
-    if (page < 0 || page >= p.max_pages) {
+    t_at = ((long long)page * 2 * p.H_kv + hk) * P + o % P;
+    if (k >= n_tiles || page < 0 || page >= p.max_pages) {
       if (k < n_tiles) set_error(p.err, kErrBadPage);
-      t_page = -1;  // no such tile, or its rows do not count
+      t_at = -1;  // no such tile, or its rows do not count
+      t_rows = 0;
     }
   };
   // ROWS: the page (unchecked; -1 out of the table) and slot of a lane's rows 32 h + lane of the
-  // stage that starts with tile k, loaded one stage ahead (NQ 1: 16 rows, of the first 16 lanes)
+  // stage that starts with tile k, loaded one stage ahead
   int rw_page[NH], rw_slot[NH];
   auto load_rows = [&](int k) {
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       const int i = k * 16 + 32 * h + lane;
       rw_page[h] = rw_slot[h] = -1;
-      if (i < n_a + n_b && (NQ > 1 || lane < 16)) {
+      if (i < n_a + n_b) {
         const int o = i < n_a ? a_lo + i : b_lo + i - n_a, pidx = o / P;
         rw_slot[h] = o - pidx * P;
         if (pidx < sg.seq.npages && (long long)sg.seq.page_begin + pidx < p.nnz_pages)
@@ -278,15 +289,17 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       const unsigned rows = __ballot_sync(0xffffffffu, ok);
       const long long row = ((long long)page * 2 * p.H_kv + hk) * P + slot;  // of K
       const uint32_t tile = ring + ist * T::kStage + (2 * h + (lane >> 4)) * T::kPair;
-      unsigned kpar = 0, vpar = 0;
-      if constexpr (NB < 4) {  // the aligned word that holds the row's two bytes
-        kpar = __ballot_sync(0xffffffffu, ok && (row & 1));
-        vpar = __ballot_sync(0xffffffffu, ok && ((row + to_v) & 1));
+      if (lane == 0) *reinterpret_cast<unsigned*>(&s_rows[warp][ist][2 * h]) = rows;
+      if constexpr (MQ) {
+        if (lane == 0) s_r0[warp][ist][2 * h] = r_first + (k + 2 * h) * 16, s_r0[warp][ist][2 * h + 1] = r_first + (k + 2 * h + 1) * 16;
       }
-      if (lane == 0) {
-        s_rowok[warp][ist][h][0] = rows;
-        s_rowok[warp][ist][h][1] = kpar;
-        s_rowok[warp][ist][h][2] = vpar;
+      if constexpr (NB < 4) {  // the aligned word that holds the row's two bytes
+        const unsigned kh = __ballot_sync(0xffffffffu, ok && (row & 1));
+        const unsigned vh = __ballot_sync(0xffffffffu, ok && ((row + to_v) & 1));
+        if (lane < 2) {
+          s_half[warp][0][ist][2 * h + lane] = (uint16_t)(kh >> (16 * lane));
+          s_half[warp][1][ist][2 * h + lane] = (uint16_t)(vh >> (16 * lane));
+        }
       }
       if (ok) {
         const uint32_t dst = tile + 2 * T::kCodes + (lane & 15) * SR;
@@ -295,42 +308,54 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
         cp_async_n<SR>(dst + T::kScales, p.mx_scales + vw * SR);
       }
 #pragma unroll
-      for (int it = 0; it < (NQ > 1 ? CPR : CPR / 2); ++it) {
+      for (int it = 0; it < CPR; ++it) {
         const int r = it * RPI + lane / CPR, x = lane % CPR * 16;  // row of the 32, byte of it
         const long long src_row = __shfl_sync(0xffffffffu, row, r);
         if ((rows >> r) & 1) {
           const uint8_t* src = reinterpret_cast<const uint8_t*>(p.pages) + src_row * RB + x;
-          const uint32_t dst = ring + ist * T::kStage + (2 * h + (r >> 4)) * T::kPair + (r & 15) * RB + x;
+          const uint32_t dst = ring + ist * T::kStage + (2 * h + (r >> 4)) * T::kPair + mx_chunk<D>(r & 15, x >> 4);
           cp_async_chunk(dst, src);
           cp_async_chunk(dst + T::kCodes, src + to_v * RB);
         }
       }
     }
-    mbar_arrive_cp_async(bar0 + ist * 8);
     ist = ist + 1 == NST ? 0 : ist + 1;
     load_rows(k + NQ);
   };
   // tiles k .. k + NQ - 1 (the next in order; their lanes side by side) -> stage ist
   auto issue = [&](int k) {
     if constexpr (ROWS) return issue_rows(k);
+    // bytes from K's to V's codes and scales, and where in a tile this lane's chunk goes
+    const long long v_codes = (long long)p.H_kv * P * RB, v_scales = (long long)p.H_kv * P * NB;
+    const int my_chunk = mx_chunk<D>(16 * lane / RB, 16 * lane % RB / 16);
     if ((k & 31) == 0) load_batch(k);
-    const int i = lane - (k & 31);
+    const uint32_t to = ring + ist * T::kStage;
+    const int first = k & 31, i = lane - first;
     if ((unsigned)i < (unsigned)NQ) {
-      const uint32_t bar = bar0 + ist * 8, dst = ring + ist * T::kStage + i * T::kPair;
-      s_meta[warp][ist][i] = t_page >= 0 ? make_int2(t_span, t_r0) : make_int2(0, 0);
-      if (t_page >= 0) {
-        const long long row = ((long long)t_page * 2 * p.H_kv + hk) * P + t_row, to_v = (long long)p.H_kv * P;
-        const uint8_t* codes = reinterpret_cast<const uint8_t*>(p.pages) + row * RB;
-        const uint8_t* scales = p.mx_scales + row * NB;
-        mbar_arrive_expect_tx(bar, T::kPair);
-        bulk_load(dst, codes, T::kCodes, bar);
-        bulk_load(dst + T::kCodes, codes + to_v * RB, T::kCodes, bar);
-        bulk_load(dst + 2 * T::kCodes, scales, T::kScales, bar);
-        bulk_load(dst + 2 * T::kCodes + T::kScales, scales + to_v * NB, T::kScales, bar);
-      } else {  // no attended row
-        mbar_arrive(bar);
-      }
+      s_rows[warp][ist][i] = (uint16_t)t_rows;
+      if constexpr (MQ) s_r0[warp][ist][i] = t_r0;
     }
+    // codes: a tile's are contiguous, of K and of V, and go a 16-byte chunk a lane at a time
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+      const long long at = __shfl_sync(0xffffffffu, t_at, first + t);
+      if (at < 0) continue;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.pages) + at * RB + 16 * lane;
+      const uint32_t dst = to + t * T::kPair + my_chunk;
+#pragma unroll
+      for (int j = 0; j < T::kCodes / 512; ++j) cp_async_chunk(dst + 512 * j, src + 512 * j);
+      src += v_codes;
+#pragma unroll
+      for (int j = 0; j < T::kCodes / 512; ++j) cp_async_chunk(dst + T::kCodes + 512 * j, src + 512 * j);
+    }
+    // scales: of all tiles at once
+    constexpr int CS = T::kScales / 16;  // chunks of a tile's K (or V) scales
+    static_assert(ROWS || (NQ * 2 * CS <= 32 && T::kCodes % 512 == 0), "a warp's copies");
+    const int t = lane / (2 * CS), x = lane % (2 * CS);
+    const long long at = __shfl_sync(0xffffffffu, t_at, first + t % NQ);
+    if (t < NQ && at >= 0)
+      cp_async_chunk(to + t * T::kPair + 2 * T::kCodes + 16 * x,
+                     p.mx_scales + at * NB + (x >= CS ? v_scales - 16 * CS : 0) + 16 * x);
     ist = ist + 1 == NST ? 0 : ist + 1;
   };
 
@@ -339,11 +364,14 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     pdl_release();
     waited = true;
   }
-  [[maybe_unused]] const int r_first = n_a ? a_lo : b_lo - pcs.shift;  // attended index of the share's first row
   // tiles are computed NQ at a time: the last few may be empty ones
-  int k_issued = 0, k_end = dead ? 0 : (n_tiles + NQ - 1) / NQ * NQ;
+  const int k_end = (n_tiles + NQ - 1) / NQ * NQ;
+  int k_issued = 0;
 #pragma unroll 1
-  for (; k_issued < min(NST * NQ, k_end); k_issued += NQ) issue(k_issued);
+  for (; k_issued < NST * NQ; k_issued += NQ) {
+    if (k_issued < k_end) issue(k_issued);
+    cp_async_group();
+  }
 
   // ---------------------------------------------------------------- Q^T B fragments
   // k-tile kt = 2 (KW c + w) + h: dims 2 KB (4 c + q4) + 8 w + 4 h + {0, 1} and + {2, 3} of column g_id,
@@ -375,7 +403,8 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     // 2^(14 - e) and its inverse, both normal: e is kept in [-100, 126]
     const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255) - 127, -100), 126);
     const float up = copysignf(__uint_as_float((unsigned)(127 + 14 - e) << 23), p.score_scale);
-    const float cs = __uint_as_float((unsigned)(127 - 14 + e) << 23) * fabsf(p.score_scale);
+    // (at least the least normal float, so that the -inf of a row that does not count stays one)
+    const float cs = fmaxf(__uint_as_float((unsigned)(127 - 14 + e) << 23) * fabsf(p.score_scale), FLT_MIN);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
       const float4 f = four(kt);
@@ -391,40 +420,40 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     cs1 = __shfl_sync(0xffffffffu, cs, 8 * q4 + 4);  // column 2 q4 + 1
   }
 
-  // The running maxima m are of the products before the column's factor cs (>= 0); weights are
+  // The running maxima m are of the products before the column's factor cs (> 0); weights are
   // 2^(cs s + nm) with nm = kWeightUp - cs m
   float st_m[2] = {-FLT_MAX, -FLT_MAX}, nm[2] = {0.f, 0.f}, st_d[2] = {0.f, 0.f};
-  const float over0 = kLazyMaxMx / cs0, over1 = kLazyMaxMx / cs1;  // (cs 0: the maximum never moves)
+  const float over0 = kLazyMaxMx / cs0, over1 = kLazyMaxMx / cs1;  // (infinite: the maximum never moves)
   float oacc[KT][4];
 #pragma unroll
   for (int i = 0; i < KT; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
 
   // NQ tiles from the ring: their chains of loads, products and exponentials are independent and
   // overlap in the warp, and share the vote and the rescale
-  __syncwarp();  // (what the issuing lanes wrote beside their copies)
 #pragma unroll 1
   for (int k = 0; k < k_end; k += NQ) {
-    const bool ok = mbar_wait(bar0 + cst * 8, cph, dead ? 1024u : kWaitPolls);
+    cp_async_group_wait<NST - 1>();
+    __syncwarp();  // every lane's copies, and what was written beside them
     const uint8_t* const stage = my_ring + cst * T::kStage;
     float sc[NQ][4];
     // a row's scale bytes in shared memory (v: of V)
     auto scales_at = [&](int i, int r, bool v) -> const uint8_t* {
       const uint8_t* at = stage + i * T::kPair + 2 * T::kCodes + (v ? T::kScales : 0) + r * SR;
-      if constexpr (ROWS && NB < 4) at += ((s_rowok[warp][cst][i >> 1][v ? 2 : 1] >> (16 * (i & 1) + r)) & 1) * NB;
+      if constexpr (ROWS && NB < 4) at += ((s_half[warp][v ? 1 : 0][cst][i] >> r) & 1) * NB;
       return at;
     };
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       // -------------------------------------------------------------- S^T = K Q^T
-      const uint8_t* kt_base = stage + i * T::kPair + kr * RB + KB * q4;
+      const uint8_t* const tile = stage + i * T::kPair;
       const uint8_t* sa = scales_at(i, kr, false);
       const uint8_t* sb = scales_at(i, kr + 8, false);
       sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
 #pragma unroll
       for (int c = 0; c < KCH; ++c) {
         uint32_t ka[KW], kb[KW];
-        lds_words<KB>(kt_base + 4 * KB * c, ka);
-        lds_words<KB>(kt_base + 8 * RB + 4 * KB * c, kb);
+        lds_words<KB>(tile + koff[c], ka);
+        lds_words<KB>(tile + 8 * RB + koff[c], kb);
         constexpr int BPC = 2 * KB > SB ? 2 * KB / SB : 1;  // blocks of a chunk
         const int blk = 2 * KB * (4 * c + q4) / SB;
         uint32_t fa[2], fb[2];  // their scales, twice each
@@ -456,42 +485,62 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       }
     }
     // ---------------------------------------------------------------- online softmax (log2)
-    unsigned rows[NQ];  // bit r: row r counts
-    int r0[NQ];         // MQ: attended index of the tile's first row
-    bool whole = true;  // every row of the stage counts for every column
+    // every row of the stage counts for every column (read as words: the tiles' masks side by side)
+    const uint32_t* const masks = reinterpret_cast<const uint32_t*>(s_rows[warp][cst]);
+    bool whole = masks[0] == 0xffffffffu && (!MQ || s_r0[warp][cst][NQ - 1] + 16 <= lim_all);
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      if constexpr (ROWS) {
-        rows[i] = (s_rowok[warp][cst][i >> 1][0] >> (16 * (i & 1))) & 0xffffu;
-        r0[i] = r_first + (k + i) * 16;
-      } else {
-        const int2 m = s_meta[warp][cst][i];
-        rows[i] = ((1u << (m.x >> 8)) - 1) & ~((1u << (m.x & 0xff)) - 1);
-        r0[i] = m.y;
+    for (int i = 1; i < NQ / 2; ++i) whole = whole && masks[i] == 0xffffffffu;
+    if (!whole) {
+      // Rarely (warp-uniform).  Rows that do not count get scores of -inf, and zeros for V's scales,
+      // which may be anything there.  A row that some of the queries alone attend must not reach the
+      // others by a NaN scale of V: such scales go to the outputs of those that attend it.
+      auto is_nan = [](uint8_t b) { return SB == 16 ? (b & 0x7f) == 0x7f : b > 127 + 13; };
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const unsigned rows = s_rows[warp][cst][i];
+        const int r0 = MQ ? s_r0[warp][cst][i] : 0;
+        // whether row r counts for this lane's column 2 q4 + h
+        auto counts = [&](int r, int h) { return ((rows >> r) & 1) && (!MQ || r0 + r < (h ? lim1 : lim0)); };
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!counts(kr + (e >> 1) * 8, e & 1)) sc[i][e] = -INFINITY;
+        uint8_t* const vs = const_cast<uint8_t*>(stage) + i * T::kPair + 2 * T::kCodes + T::kScales;
+        bool nan = false;
+        for (int x = lane; x < T::kScales; x += 32) {
+          if (!((rows >> (x / SR)) & 1)) vs[x] = 0;
+          nan = nan || is_nan(vs[x]);
+        }
+        if (MQ && __any_sync(0xffffffffu, nan)) {
+          constexpr int VBL = RL > SB ? RL / SB : 1;
+#pragma unroll
+          for (int b = 0; b < VBL; ++b) {
+            bool bad[2] = {false, false};
+#pragma unroll 1
+            for (int r = 0; r < 16; ++r) {
+              if (!is_nan(scales_at(i, r, true)[RL * g_id / SB + b])) continue;
+              bad[0] = bad[0] || counts(r, 0);
+              bad[1] = bad[1] || counts(r, 1);
+            }
+#pragma unroll
+            for (int mt = b * KT / VBL; mt < (b + 1) * KT / VBL; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (bad[h]) oacc[mt][h] = oacc[mt][h + 2] = __int_as_float(0x7fc00000);
+          }
+          __syncwarp();
+          for (int x = lane; x < T::kScales; x += 32)
+            if (is_nan(vs[x])) vs[x] = 0;
+        }
       }
-      whole = whole && rows[i] == 0xffffu && (!MQ || r0[i] + 16 <= lim_all);
+      __syncwarp();
     }
-    // whether row r of tile i counts for this lane's column 2 q4 + h
-    auto counts = [&](int i, int r, int h) {
-      return ((rows[i] >> r) & 1) && (!MQ || r0[i] + r < (h ? lim1 : lim0));
-    };
     float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      if (!whole) {  // (warp-uniform)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (!counts(i, kr + (e >> 1) * 8, e & 1)) sc[i][e] = -INFINITY;
-      }
       t0 = fmaxf(t0, fmaxf(sc[i][0], sc[i][2]));
       t1 = fmaxf(t1, fmaxf(sc[i][1], sc[i][3]));
     }
-    if (__any_sync(0xffffffffu, t0 - st_m[0] > over0 || t1 - st_m[1] > over1 || !ok)) {
-      if (__any_sync(0xffffffffu, !ok)) {
-        dead = true;  // the tiles in flight are still waited for; the error word says the rest
-        k_end = k_issued;
-        if (lane == 0) set_error(p.err, kErrTimeout);
-      }
+    if (__any_sync(0xffffffffu, t0 - st_m[0] > over0 || t1 - st_m[1] > over1)) {
       const float mn0 = fmaxf(st_m[0], max_over_groups(t0)), mn1 = fmaxf(st_m[1], max_over_groups(t1));
       const float a0 = fast_exp2((st_m[0] - mn0) * cs0), a1 = fast_exp2((st_m[1] - mn1) * cs1);
       st_d[0] *= a0;
@@ -514,10 +563,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     for (int i = 0; i < NQ; ++i) {
       float pr[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        pr[e] = fast_exp2(fmaf(sc[i][e], e & 1 ? cs1 : cs0, nm[e & 1]));
-        if (!whole && sc[i][e] == -INFINITY) pr[e] = 0.f;  // (whatever cs and nm are)
-      }
+      for (int e = 0; e < 4; ++e) pr[e] = fast_exp2(fmaf(sc[i][e], e & 1 ? cs1 : cs0, nm[e & 1]));
       st_d[0] += pr[0] + pr[2];
       st_d[1] += pr[1] + pr[3];
       // P^T as a B fragment: rows 2 q4, 2 q4 + 1 (+ 8) of column g_id
@@ -539,58 +585,19 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     constexpr int VBL = RL > SB ? RL / SB : 1;  // blocks of a thread's dims
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const uint8_t* vt = stage + i * T::kPair + T::kCodes + VB * g_id;
+      const uint8_t* const tile = stage + i * T::kPair;
       uint32_t v[4][VB / 4];  // rows vr[0], vr[1], vr[0] + 8, vr[1] + 8
       uint32_t sv[2][VBL];    // scales of rows (vr[0], vr[1]) and of the same + 8
 #pragma unroll
-      for (int j = 0; j < 4; ++j) lds_words<VB>(vt + (vr[j & 1] + 8 * (j >> 1)) * RB, v[j]);
+      for (int j = 0; j < 4; ++j) lds_words<VB>(tile + voff[j & 1] + 8 * RB * (j >> 1), v[j]);
 #pragma unroll
       for (int b = 0; b < VBL; ++b)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int blk = RL * g_id / SB + b;
-          uint32_t x = mx_scales<SB>(scales_at(i, vr[0] + 8 * j, true)[blk] |
-                                     ((uint32_t)scales_at(i, vr[1] + 8 * j, true)[blk] << 8));
-          if (!whole) {
-            // rows outside may have any scale (NaN): 0
-            if (!((rows[i] >> (vr[0] + 8 * j)) & 1)) x &= 0xffff0000u;
-            if (!((rows[i] >> (vr[1] + 8 * j)) & 1)) x &= 0x0000ffffu;
-          }
-          sv[j][b] = x;
+          sv[j][b] = mx_scales<SB>(scales_at(i, vr[0] + 8 * j, true)[blk] |
+                                   ((uint32_t)scales_at(i, vr[1] + 8 * j, true)[blk] << 8));
         }
-      if constexpr (MQ) {
-        if (!whole) {
-          // A row that some of the queries do not attend must not reach them by a NaN scale: such
-          // scales go to 0 here, and to the outputs of the queries that do attend the row
-          auto is_nan = [](uint32_t s) { return (s & 0x7fffu) > 0x7c00u || (s & 0x7fff0000u) > 0x7c000000u; };
-          bool any = false;
-#pragma unroll
-          for (int b = 0; b < VBL; ++b) any = any || is_nan(sv[0][b]) || is_nan(sv[1][b]);
-          if (__any_sync(0xffffffffu, any)) {
-#pragma unroll
-            for (int b = 0; b < VBL; ++b) {
-              const int blk = RL * g_id / SB + b;
-              bool bad0 = false, bad1 = false;
-#pragma unroll 1
-              for (int r = 0; r < 16; ++r) {
-                if (!is_nan(mx_scales<SB>(scales_at(i, r, true)[blk]) & 0xffffu)) continue;
-                bad0 = bad0 || counts(i, r, 0);
-                bad1 = bad1 || counts(i, r, 1);
-              }
-#pragma unroll
-              for (int mt = b * KT / VBL; mt < (b + 1) * KT / VBL; ++mt) {
-                if (bad0) oacc[mt][0] = oacc[mt][2] = __int_as_float(0x7fc00000);
-                if (bad1) oacc[mt][1] = oacc[mt][3] = __int_as_float(0x7fc00000);
-              }
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                if (is_nan(sv[j][b] & 0xffffu)) sv[j][b] &= 0xffff0000u;
-                if (is_nan(sv[j][b] & 0xffff0000u)) sv[j][b] &= 0x0000ffffu;
-              }
-            }
-          }
-        }
-      }
 #pragma unroll
       for (int w = 0; w < VB / 4; ++w) {
         // codes of rows (0, 1) and (2, 3) side by side in a byte: even dims, odd dims
@@ -614,12 +621,10 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     }
     // every lane has its codes in registers: the stage takes the next tiles
     cst = cst + 1 == NST ? 0 : cst + 1;
-    if (cst == 0) cph ^= 1;
     __syncwarp();
-    if (k_issued < k_end) {
-      issue(k_issued);
-      k_issued += NQ;
-    }
+    if (k_issued < k_end) issue(k_issued);
+    k_issued += NQ;
+    cp_async_group();
   }
   st_d[0] = sum_over_groups(st_d[0]);
   st_d[1] = sum_over_groups(st_d[1]);
