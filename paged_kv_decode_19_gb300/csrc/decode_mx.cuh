@@ -77,6 +77,18 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// f16 times one half of a pair
+__device__ __forceinline__ uint32_t mul_lo(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __low2half2(*reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t mul_hi(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __high2half2(*reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* x, int from) {
+  return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), from));
+}
 // 8x8 transpose of 16-bit elements across the warp: from row lane / 4, columns 2 (lane % 4) + {0, 1}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -182,6 +194,17 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
 #pragma unroll
   for (int j = 0; j < 2; ++j) voff[j] = T::kCodes + mx_chunk<D>(vr[j], VB * g_id >> 4) + (VB * g_id & 15);
 
+  // Where this lane's chunk of a tile's codes goes, and of its scales which tile it copies, from where
+  // (V's lie behind K's as its codes do) and to where; CS: chunks of a tile's K (or V) scales
+  constexpr int CS = T::kScales / 16;
+  static_assert(ROWS || (NQ * 2 * CS <= 32 && T::kCodes % 512 == 0), "a warp's copies");
+  [[maybe_unused]] const int my_chunk = mx_chunk<D>(16 * lane / RB, 16 * lane % RB / 16);
+  [[maybe_unused]] const int my_stile = lane / (2 * CS) % NQ;
+  [[maybe_unused]] const int my_sdst = my_stile * T::kPair + 2 * T::kCodes + 16 * (lane % (2 * CS));
+  [[maybe_unused]] const long long v_codes = (long long)p.H_kv * P * RB;
+  [[maybe_unused]] const long long my_sbyte =
+      lane % (2 * CS) < CS ? 16 * (lane % CS) : (long long)p.H_kv * P * NB + 16 * (lane % CS);
+
   // The ring: NQ tiles at a time are filled into stage `ist` and read from stage `cst`, in order, one
   // group of copies a stage.
   int ist = 0, cst = 0;
@@ -242,9 +265,12 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     return pidx < sg.seq.npages && (long long)sg.seq.page_begin + pidx < p.nnz_pages
                ? __ldg(p.values + sg.seq.page_begin + pidx) : -1;
   };
-  // of this lane's tile: its K rows' place in the cache (-1: none), rows that count, first row's index
-  long long t_at = -1;
+  // of this lane's tile: its K codes and scales, rows that count, first row's index; of this batch of
+  // 32 and the one before: tiles of which every row counts for every column
+  const uint8_t* t_codes = nullptr;
+  const uint8_t* t_scales = nullptr;
   int t_rows = 0, t_r0 = 0, page_next = ROWS ? -1 : load_page(lane);
+  unsigned full_now = 0, full_before = 0;
   auto load_batch = [&](int k0) {  // tiles k0 .. k0 + 31
     const int k = k0 + lane, page = page_next;
     page_next = load_page(k + 32);
@@ -253,12 +279,16 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     auto below = [&](int end) { return (1 << min(max(end - o, 0), 16)) - 1; };  // the tile's rows before it
     t_rows = below(in_a ? a_hi : b_hi) & ~below(in_a ? a_lo : b_lo);
     t_r0 = in_a ? o : o - pcs.shift;
-    t_at = ((long long)page * 2 * p.H_kv + hk) * P + o % P;
-    if (k >= n_tiles || page < 0 || page >= p.max_pages) {
+    long long row = ((long long)page * 2 * p.H_kv + hk) * P + o % P;
+    if (k >= n_tiles || page < 0 || page >= p.max_pages) {  // no such tile, or its rows do not count
       if (k < n_tiles) set_error(p.err, kErrBadPage);
-      t_at = -1;  // no such tile, or its rows do not count
       t_rows = 0;
+      row = 0;  // (what is copied in its place)
     }
+    t_codes = reinterpret_cast<const uint8_t*>(p.pages) + row * RB;
+    t_scales = p.mx_scales + row * NB;
+    full_before = full_now;
+    full_now = __ballot_sync(0xffffffffu, t_rows == 0xffff && (!MQ || t_r0 + 16 <= lim_all));
   };
   // ROWS: the page (unchecked; -1 out of the table) and slot of a lane's rows 32 h + lane of the
   // stage that starts with tile k, loaded one stage ahead
@@ -325,9 +355,6 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   // tiles k .. k + NQ - 1 (the next in order; their lanes side by side) -> stage ist
   auto issue = [&](int k) {
     if constexpr (ROWS) return issue_rows(k);
-    // bytes from K's to V's codes and scales, and where in a tile this lane's chunk goes
-    const long long v_codes = (long long)p.H_kv * P * RB, v_scales = (long long)p.H_kv * P * NB;
-    const int my_chunk = mx_chunk<D>(16 * lane / RB, 16 * lane % RB / 16);
     if ((k & 31) == 0) load_batch(k);
     const uint32_t to = ring + ist * T::kStage;
     const int first = k & 31, i = lane - first;
@@ -338,9 +365,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     // codes: a tile's are contiguous, of K and of V, and go a 16-byte chunk a lane at a time
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
-      const long long at = __shfl_sync(0xffffffffu, t_at, first + t);
-      if (at < 0) continue;
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.pages) + at * RB + 16 * lane;
+      const uint8_t* src = shfl_ptr(t_codes, first + t) + 16 * lane;
       const uint32_t dst = to + t * T::kPair + my_chunk;
 #pragma unroll
       for (int j = 0; j < T::kCodes / 512; ++j) cp_async_chunk(dst + 512 * j, src + 512 * j);
@@ -349,13 +374,8 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       for (int j = 0; j < T::kCodes / 512; ++j) cp_async_chunk(dst + T::kCodes + 512 * j, src + 512 * j);
     }
     // scales: of all tiles at once
-    constexpr int CS = T::kScales / 16;  // chunks of a tile's K (or V) scales
-    static_assert(ROWS || (NQ * 2 * CS <= 32 && T::kCodes % 512 == 0), "a warp's copies");
-    const int t = lane / (2 * CS), x = lane % (2 * CS);
-    const long long at = __shfl_sync(0xffffffffu, t_at, first + t % NQ);
-    if (t < NQ && at >= 0)
-      cp_async_chunk(to + t * T::kPair + 2 * T::kCodes + 16 * x,
-                     p.mx_scales + at * NB + (x >= CS ? v_scales - 16 * CS : 0) + 16 * x);
+    const uint8_t* src = shfl_ptr(t_scales, first + my_stile) + my_sbyte;
+    if (NQ * 2 * CS == 32 || lane < NQ * 2 * CS) cp_async_chunk(to + my_sdst, src);
     ist = ist + 1 == NST ? 0 : ist + 1;
   };
 
@@ -456,28 +476,26 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
         lds_words<KB>(tile + 8 * RB + koff[c], kb);
         constexpr int BPC = 2 * KB > SB ? 2 * KB / SB : 1;  // blocks of a chunk
         const int blk = 2 * KB * (4 * c + q4) / SB;
-        uint32_t fa[2], fb[2];  // their scales, twice each
+        // their scales: of row kr (low halves) and kr + 8 (high halves); of two blocks, a pair each
+        uint32_t fa, fb;
         if constexpr (BPC == 2) {
-          const uint32_t a = mx_scales<SB>(*reinterpret_cast<const uint16_t*>(sa + blk));
-          const uint32_t b = mx_scales<SB>(*reinterpret_cast<const uint16_t*>(sb + blk));
-          fa[0] = __byte_perm(a, a, 0x1010), fa[1] = __byte_perm(a, a, 0x3232);
-          fb[0] = __byte_perm(b, b, 0x1010), fb[1] = __byte_perm(b, b, 0x3232);
+          fa = mx_scales<SB>(*reinterpret_cast<const uint16_t*>(sa + blk));
+          fb = mx_scales<SB>(*reinterpret_cast<const uint16_t*>(sb + blk));
         } else {
-          const uint32_t ab = mx_scales<SB>(sa[blk] | ((uint32_t)sb[blk] << 8));
-          fa[0] = fa[1] = __byte_perm(ab, ab, 0x1010);
-          fb[0] = fb[1] = __byte_perm(ab, ab, 0x3232);
+          fa = fb = mx_scales<SB>(sa[blk] | ((uint32_t)sb[blk] << 8));
         }
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
           uint32_t ra[4], rb[4];
           mx_codes(ka[w], ra);
           mx_codes(kb[w], rb);
-          const int f = BPC == 2 ? 2 * w / KW : 0;
+          const bool second = BPC == 2 && 2 * w >= KW;
+          auto of_a = [&](uint32_t x) { return second ? mul_hi(x, fa) : mul_lo(x, fa); };
+          auto of_b = [&](uint32_t x) { return BPC == 1 || second ? mul_hi(x, fb) : mul_lo(x, fb); };
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int kt = 2 * (KW * c + w) + h;
-            const uint32_t a[4] = {mul_h2(ra[2 * h], fa[f]), mul_h2(rb[2 * h], fb[f]),
-                                   mul_h2(ra[2 * h + 1], fa[f]), mul_h2(rb[2 * h + 1], fb[f])};
+            const uint32_t a[4] = {of_a(ra[2 * h]), of_b(rb[2 * h]), of_a(ra[2 * h + 1]), of_b(rb[2 * h + 1])};
             Mma<__half>::run(sc[i], a, qf[kt][0], qf[kt][1]);
             if constexpr (SPLIT) Mma<__half>::run(sc[i], a, ql[kt][0], ql[kt][1]);
           }
@@ -485,11 +503,17 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       }
     }
     // ---------------------------------------------------------------- online softmax (log2)
-    // every row of the stage counts for every column (read as words: the tiles' masks side by side)
-    const uint32_t* const masks = reinterpret_cast<const uint32_t*>(s_rows[warp][cst]);
-    bool whole = masks[0] == 0xffffffffu && (!MQ || s_r0[warp][cst][NQ - 1] + 16 <= lim_all);
+    bool whole;  // every row of the stage counts for every column
+    if constexpr (ROWS) {
+      const uint32_t* const masks = reinterpret_cast<const uint32_t*>(s_rows[warp][cst]);  // (of two tiles each)
+      whole = masks[0] == 0xffffffffu && (!MQ || s_r0[warp][cst][NQ - 1] + 16 <= lim_all);
 #pragma unroll
-    for (int i = 1; i < NQ / 2; ++i) whole = whole && masks[i] == 0xffffffffu;
+      for (int i = 1; i < NQ / 2; ++i) whole = whole && masks[i] == 0xffffffffu;
+    } else {
+      // (tiles are issued up to NST stages ahead: at most one batch)
+      const unsigned full = (k ^ (min(k_issued, k_end) - NQ)) & ~31 ? full_before : full_now;
+      whole = ((~full >> (k & 31)) & ((1u << NQ) - 1)) == 0;
+    }
     if (!whole) {
       // Rarely (warp-uniform).  Rows that do not count get scores of -inf, and zeros for V's scales,
       // which may be anything there.  A row that some of the queries alone attend must not reach the
