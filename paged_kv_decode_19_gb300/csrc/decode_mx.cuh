@@ -134,10 +134,12 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   __shared__ float s_plse[NW][2][kMaxGroupPerCta]; // their lse
   __shared__ int s_last[2 * NW];
   __shared__ WorkerStart s_start[NW];
-  // of each tile of a stage: which rows count (bit r: row r), and the attended index of row 0; of rows
-  // with two scale bytes that were copied one by one, which half of the copied word holds K's and V's
-  __shared__ __align__(8) uint16_t s_rows[NW][NST][NQ];
-  __shared__ int s_r0[MQ ? NW : 1][NST][NQ];
+  // of each tile of two batches of 32 (ROWS: of a stage): which rows count (bit r: row r), and the
+  // attended index of row 0; of rows with two scale bytes that were copied one by one, which half of
+  // the copied word holds K's and V's
+  constexpr int NM = ROWS ? NQ : 32;
+  __shared__ __align__(8) uint16_t s_rows[NW][2][NM];
+  __shared__ int s_r0[MQ ? NW : 1][2][NM];
   __shared__ uint16_t s_half[ROWS && NB < 4 ? NW : 1][2][NST][NQ];
   constexpr int NH = NQ / 2;  // pairs of tiles
 
@@ -205,9 +207,10 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   [[maybe_unused]] const long long my_sbyte =
       lane % (2 * CS) < CS ? 16 * (lane % CS) : (long long)p.H_kv * P * NB + 16 * (lane % CS);
 
-  // The ring: NQ tiles at a time are filled into stage `ist` and read from stage `cst`, in order, one
-  // group of copies a stage.
-  int ist = 0, cst = 0;
+  // The ring: NQ tiles at a time are computed from stage `cst`, which then takes the ones that follow
+  // the other stage's; one group of copies a stage.
+  static_assert(NST == 2 && NST * NQ <= 16, "two stages, well within a batch of 32 tiles");
+  int cst = 0;
   if (!p.early_inputs && !waited) {
     pdl_wait();
     pdl_release();
@@ -265,30 +268,31 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     return pidx < sg.seq.npages && (long long)sg.seq.page_begin + pidx < p.nnz_pages
                ? __ldg(p.values + sg.seq.page_begin + pidx) : -1;
   };
-  // of this lane's tile: its K codes and scales, rows that count, first row's index; of this batch of
-  // 32 and the one before: tiles of which every row counts for every column
+  // of this lane's tile: its K codes and scales; of the batch: tiles of which every row counts for every
+  // column
   const uint8_t* t_codes = nullptr;
   const uint8_t* t_scales = nullptr;
-  int t_rows = 0, t_r0 = 0, page_next = ROWS ? -1 : load_page(lane);
-  unsigned full_now = 0, full_before = 0;
+  int page_next = ROWS ? -1 : load_page(lane);
+  unsigned full = 0;
   auto load_batch = [&](int k0) {  // tiles k0 .. k0 + 31
     const int k = k0 + lane, page = page_next;
     page_next = load_page(k + 32);
     const int o = tile_at(k);
     const bool in_a = k < n_a;
     auto below = [&](int end) { return (1 << min(max(end - o, 0), 16)) - 1; };  // the tile's rows before it
-    t_rows = below(in_a ? a_hi : b_hi) & ~below(in_a ? a_lo : b_lo);
-    t_r0 = in_a ? o : o - pcs.shift;
+    int rows = below(in_a ? a_hi : b_hi) & ~below(in_a ? a_lo : b_lo);
+    const int r0 = in_a ? o : o - pcs.shift;
     long long row = ((long long)page * 2 * p.H_kv + hk) * P + o % P;
     if (k >= n_tiles || page < 0 || page >= p.max_pages) {  // no such tile, or its rows do not count
       if (k < n_tiles) set_error(p.err, kErrBadPage);
-      t_rows = 0;
+      rows = 0;
       row = 0;  // (what is copied in its place)
     }
     t_codes = reinterpret_cast<const uint8_t*>(p.pages) + row * RB;
     t_scales = p.mx_scales + row * NB;
-    full_before = full_now;
-    full_now = __ballot_sync(0xffffffffu, t_rows == 0xffff && (!MQ || t_r0 + 16 <= lim_all));
+    s_rows[warp][(k0 >> 5) & 1][lane] = (uint16_t)rows;
+    if constexpr (MQ) s_r0[warp][(k0 >> 5) & 1][lane] = r0;
+    full = __ballot_sync(0xffffffffu, rows == 0xffff && (!MQ || r0 + 16 <= lim_all));
   };
   // ROWS: the page (unchecked; -1 out of the table) and slot of a lane's rows 32 h + lane of the
   // stage that starts with tile k, loaded one stage ahead
@@ -307,8 +311,8 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     }
   };
   if constexpr (ROWS) load_rows(0);
-  // its rows -> stage ist: RB / 16 lanes copy a row's 16-byte chunks, the row's own lane its scales
-  auto issue_rows = [&](int k) {
+  // its rows -> stage st: RB / 16 lanes copy a row's 16-byte chunks, the row's own lane its scales
+  auto issue_rows = [&](int k, int st) {
     constexpr int CPR = RB / 16, RPI = 32 / CPR;  // chunks per row, rows per instruction
     const long long to_v = (long long)p.H_kv * P;  // rows
 #pragma unroll
@@ -318,17 +322,17 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       if (slot >= 0 && !ok) set_error(p.err, kErrBadPage);  // its row does not count
       const unsigned rows = __ballot_sync(0xffffffffu, ok);
       const long long row = ((long long)page * 2 * p.H_kv + hk) * P + slot;  // of K
-      const uint32_t tile = ring + ist * T::kStage + (2 * h + (lane >> 4)) * T::kPair;
-      if (lane == 0) *reinterpret_cast<unsigned*>(&s_rows[warp][ist][2 * h]) = rows;
-      if constexpr (MQ) {
-        if (lane == 0) s_r0[warp][ist][2 * h] = r_first + (k + 2 * h) * 16, s_r0[warp][ist][2 * h + 1] = r_first + (k + 2 * h + 1) * 16;
+      const uint32_t tile = ring + st * T::kStage + (2 * h + (lane >> 4)) * T::kPair;
+      if (lane < 2) {
+        s_rows[warp][st][2 * h + lane] = (uint16_t)(rows >> (16 * lane));
+        if constexpr (MQ) s_r0[warp][st][2 * h + lane] = r_first + (k + 2 * h + lane) * 16;
       }
       if constexpr (NB < 4) {  // the aligned word that holds the row's two bytes
         const unsigned kh = __ballot_sync(0xffffffffu, ok && (row & 1));
         const unsigned vh = __ballot_sync(0xffffffffu, ok && ((row + to_v) & 1));
         if (lane < 2) {
-          s_half[warp][0][ist][2 * h + lane] = (uint16_t)(kh >> (16 * lane));
-          s_half[warp][1][ist][2 * h + lane] = (uint16_t)(vh >> (16 * lane));
+          s_half[warp][0][st][2 * h + lane] = (uint16_t)(kh >> (16 * lane));
+          s_half[warp][1][st][2 * h + lane] = (uint16_t)(vh >> (16 * lane));
         }
       }
       if (ok) {
@@ -343,25 +347,20 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
         const long long src_row = __shfl_sync(0xffffffffu, row, r);
         if ((rows >> r) & 1) {
           const uint8_t* src = reinterpret_cast<const uint8_t*>(p.pages) + src_row * RB + x;
-          const uint32_t dst = ring + ist * T::kStage + (2 * h + (r >> 4)) * T::kPair + mx_chunk<D>(r & 15, x >> 4);
+          const uint32_t dst = ring + st * T::kStage + (2 * h + (r >> 4)) * T::kPair + mx_chunk<D>(r & 15, x >> 4);
           cp_async_chunk(dst, src);
           cp_async_chunk(dst + T::kCodes, src + to_v * RB);
         }
       }
     }
-    ist = ist + 1 == NST ? 0 : ist + 1;
     load_rows(k + NQ);
   };
-  // tiles k .. k + NQ - 1 (the next in order; their lanes side by side) -> stage ist
-  auto issue = [&](int k) {
-    if constexpr (ROWS) return issue_rows(k);
+  // tiles k .. k + NQ - 1 (the next in order; their lanes side by side) -> stage st
+  auto issue = [&](int k, int st) {
+    if constexpr (ROWS) return issue_rows(k, st);
     if ((k & 31) == 0) load_batch(k);
-    const uint32_t to = ring + ist * T::kStage;
-    const int first = k & 31, i = lane - first;
-    if ((unsigned)i < (unsigned)NQ) {
-      s_rows[warp][ist][i] = (uint16_t)t_rows;
-      if constexpr (MQ) s_r0[warp][ist][i] = t_r0;
-    }
+    const uint32_t to = ring + st * T::kStage;
+    const int first = k & 31;
     // codes: a tile's are contiguous, of K and of V, and go a 16-byte chunk a lane at a time
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
@@ -376,7 +375,6 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     // scales: of all tiles at once
     const uint8_t* src = shfl_ptr(t_scales, first + my_stile) + my_sbyte;
     if (NQ * 2 * CS == 32 || lane < NQ * 2 * CS) cp_async_chunk(to + my_sdst, src);
-    ist = ist + 1 == NST ? 0 : ist + 1;
   };
 
   if (!waited) {  // pages and scales may still be written by the previous kernel until here
@@ -389,7 +387,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   int k_issued = 0;
 #pragma unroll 1
   for (; k_issued < NST * NQ; k_issued += NQ) {
-    if (k_issued < k_end) issue(k_issued);
+    if (k_issued < k_end) issue(k_issued, k_issued == 0 ? cst : cst ^ 1);
     cp_async_group();
   }
 
@@ -441,12 +439,14 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   }
 
   // The running maxima m are of the products before the column's factor cs (> 0); weights are
-  // 2^(cs s + nm) with nm = kWeightUp - cs m
+  // 2^(cs s + nm) with nm = kWeightUp - cs m.  They move when a product is above th
   float st_m[2] = {-FLT_MAX, -FLT_MAX}, nm[2] = {0.f, 0.f}, st_d[2] = {0.f, 0.f};
-  const float over0 = kLazyMaxMx / cs0, over1 = kLazyMaxMx / cs1;  // (infinite: the maximum never moves)
+  float th[2] = {-FLT_MAX, -FLT_MAX};
   float oacc[KT][4];
 #pragma unroll
   for (int i = 0; i < KT; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
+
+  [[maybe_unused]] unsigned full_left = 0;  // `full` from tile k on
 
   // NQ tiles from the ring: their chains of loads, products and exponentials are independent and
   // overlap in the warp, and share the vote and the rescale
@@ -505,32 +505,34 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     // ---------------------------------------------------------------- online softmax (log2)
     bool whole;  // every row of the stage counts for every column
     if constexpr (ROWS) {
-      const uint32_t* const masks = reinterpret_cast<const uint32_t*>(s_rows[warp][cst]);  // (of two tiles each)
-      whole = masks[0] == 0xffffffffu && (!MQ || s_r0[warp][cst][NQ - 1] + 16 <= lim_all);
+      whole = !MQ || s_r0[warp][cst][NQ - 1] + 16 <= lim_all;
 #pragma unroll
-      for (int i = 1; i < NQ / 2; ++i) whole = whole && masks[i] == 0xffffffffu;
+      for (int i = 0; i < NQ; ++i) whole = whole && s_rows[warp][cst][i] == 0xffff;
     } else {
-      // (tiles are issued up to NST stages ahead: at most one batch)
-      const unsigned full = (k ^ (min(k_issued, k_end) - NQ)) & ~31 ? full_before : full_now;
-      whole = ((~full >> (k & 31)) & ((1u << NQ) - 1)) == 0;
+      if ((k & 31) == 0) full_left = full;  // (the batch of k is the last one loaded: fewer than 32 tiles are ahead)
+      whole = (full_left & ((1u << NQ) - 1)) == (1u << NQ) - 1;
+      full_left >>= NQ;
     }
     if (!whole) {
       // Rarely (warp-uniform).  Rows that do not count get scores of -inf, and zeros for V's scales,
       // which may be anything there.  A row that some of the queries alone attend must not reach the
       // others by a NaN scale of V: such scales go to the outputs of those that attend it.
+      const int m_at = ROWS ? cst : (k >> 5) & 1, m_i = ROWS ? 0 : k & 31;  // the tiles' masks
+      int ln;  // (the lane's number, read here: nothing of this branch is worked out in every stage)
+      asm volatile("mov.u32 %0, %%laneid;" : "=r"(ln)::"memory");
       auto is_nan = [](uint8_t b) { return SB == 16 ? (b & 0x7f) == 0x7f : b > 127 + 13; };
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        const unsigned rows = s_rows[warp][cst][i];
-        const int r0 = MQ ? s_r0[warp][cst][i] : 0;
+        const unsigned rows = s_rows[warp][m_at][m_i + i];
+        const int r0 = MQ ? s_r0[warp][m_at][m_i + i] : 0;
         // whether row r counts for this lane's column 2 q4 + h
         auto counts = [&](int r, int h) { return ((rows >> r) & 1) && (!MQ || r0 + r < (h ? lim1 : lim0)); };
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (!counts(kr + (e >> 1) * 8, e & 1)) sc[i][e] = -INFINITY;
+          if (!counts(mx_row<D>(ln >> 2) + (e >> 1) * 8, e & 1)) sc[i][e] = -INFINITY;
         uint8_t* const vs = const_cast<uint8_t*>(stage) + i * T::kPair + 2 * T::kCodes + T::kScales;
         bool nan = false;
-        for (int x = lane; x < T::kScales; x += 32) {
+        for (int x = ln; x < T::kScales; x += 32) {
           if (!((rows >> (x / SR)) & 1)) vs[x] = 0;
           nan = nan || is_nan(vs[x]);
         }
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
                 if (bad[h]) oacc[mt][h] = oacc[mt][h + 2] = __int_as_float(0x7fc00000);
           }
           __syncwarp();
-          for (int x = lane; x < T::kScales; x += 32)
+          for (int x = ln; x < T::kScales; x += 32)
             if (is_nan(vs[x])) vs[x] = 0;
         }
       }
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       t0 = fmaxf(t0, fmaxf(sc[i][0], sc[i][2]));
       t1 = fmaxf(t1, fmaxf(sc[i][1], sc[i][3]));
     }
-    if (__any_sync(0xffffffffu, t0 - st_m[0] > over0 || t1 - st_m[1] > over1)) {
+    if (__any_sync(0xffffffffu, t0 > th[0] || t1 > th[1])) {
       const float mn0 = fmaxf(st_m[0], max_over_groups(t0)), mn1 = fmaxf(st_m[1], max_over_groups(t1));
       const float a0 = fast_exp2((st_m[0] - mn0) * cs0), a1 = fast_exp2((st_m[1] - mn1) * cs1);
       st_d[0] *= a0;
@@ -573,6 +575,8 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       st_m[1] = mn1;
       nm[0] = fmaf(-mn0, cs0, kWeightUp);
       nm[1] = fmaf(-mn1, cs1, kWeightUp);
+      th[0] = mn0 + kLazyMaxMx / cs0;
+      th[1] = mn1 + kLazyMaxMx / cs1;
 #pragma unroll
       for (int mt = 0; mt < KT; ++mt) {
         oacc[mt][0] *= a0;
@@ -644,11 +648,11 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       }
     }
     // every lane has its codes in registers: the stage takes the next tiles
-    cst = cst + 1 == NST ? 0 : cst + 1;
     __syncwarp();
-    if (k_issued < k_end) issue(k_issued);
+    if (k_issued < k_end) issue(k_issued, cst);
     k_issued += NQ;
     cp_async_group();
+    cst ^= 1;
   }
   st_d[0] = sum_over_groups(st_d[0]);
   st_d[1] = sum_over_groups(st_d[1]);
