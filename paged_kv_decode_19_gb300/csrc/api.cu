@@ -345,7 +345,7 @@ static int slices_side_by_side(int n_z) { return n_z == 2 || n_z == 4 ? n_z : 1;
 // Block-scaled cache with host copies of the table: whether one block per (sequence, KV head)
 // beats equal shares of all pages.  The longest segment's share of a warp may be kCrossTiles larger
 // than the equal share; all segments must be resident at once, with a slice per KV head.
-static bool block_per_segment(const pd_decode_desc& d, int n_z, int wave) {
+static bool block_per_segment(const pd_decode_desc& d, int n_z, int wave, int warps) {
   if (n_z != 1 || (long long)d.B * d.H_kv > wave) return false;
   const int B = d.B;
   long long total = 0, most = 0;
@@ -358,7 +358,7 @@ static bool block_per_segment(const pd_decode_desc& d, int n_z, int wave) {
     total += n;
     most = std::max(most, n);
   }
-  return (most + kMmaWarps - 1) / kMmaWarps <= total * d.H_kv / ((long long)wave * kMmaWarps) + kCrossTiles;
+  return (most + warps - 1) / warps <= total * d.H_kv / ((long long)wave * warps) + kCrossTiles;
 }
 
 // Fixed-point RoPE frequencies: F_i = 2^64 * frac(rope_scale / rope_theta^(2i/D) / (2 pi)).
@@ -523,7 +523,7 @@ size_t pd_workspace_size_mx(const pd_decode_desc* desc, int32_t q_len) {
   int ctas = 1, mode, grid;
   if (mx_occupancy_for(desc, &ctas, ds, q_len) != PD_OK) return 0;
   size_t ws;
-  plan_impl(desc, ds->num_sms, ctas, kMmaWarps, &mode, &grid, &ws, q_len);
+  plan_impl(desc, ds->num_sms, ctas, mx_warps(desc->q_dtype == kF32, desc->D), &mode, &grid, &ws, q_len);
   return ws;
 }
 
@@ -600,13 +600,13 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   }
   int mode = 0, grid_blocks = 0;
   size_t ws_need = 0;
-  const int wpb = use_mma ? kMmaWarps : 1;
+  const int wpb = mx ? mx_warps(d.q_dtype == kF32, d.D) : use_mma ? kMmaWarps : 1;
   plan_impl(desc, ds->num_sms, ctas, wpb, &mode, &grid_blocks, &ws_need, q_len);
   if (grid_blocks == 0) return PD_OK;
   if ((bs || mx) && use_mma && mode == kSchedBalanced && d.num_splits == 0) {
     const int wave = ds->num_sms * ctas;
     if (d.host_indptr) {
-      if (block_per_segment(d, (d.H_qo / d.H_kv * q_len + kMaxGroupPerCta - 1) / kMaxGroupPerCta, wave)) {
+      if (block_per_segment(d, (d.H_qo / d.H_kv * q_len + kMaxGroupPerCta - 1) / kMaxGroupPerCta, wave, wpb)) {
         mode = kSchedPerBlock;
         grid_blocks = d.B * d.H_kv;
         ws_need = 0;
@@ -614,7 +614,7 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
     } else {
       const int n_z = (d.H_qo / d.H_kv * q_len + kMaxGroupPerCta - 1) / kMaxGroupPerCta;
       grid_blocks = bs_device_grid(d.B, d.H_kv, n_z, slices_side_by_side(n_z), d.nnz_pages * d.page_size / 16, wave,
-                                   kMmaWarps, grid_blocks);
+                                   wpb, grid_blocks);
     }
   }
 

@@ -14,6 +14,13 @@
 
 namespace pd {
 
+#ifndef MXLEAD
+#define MXLEAD 6
+#endif
+#ifndef MXNAP
+#define MXNAP 500
+#endif
+constexpr int kLead = MXLEAD, kNap = MXNAP;
 constexpr float kLazyMaxMx = 8.f;   // the running maximum moves when exceeded by more than 2^8 ...
 constexpr float kWeightUp = 7.f;    // ... and a weight is held times 2^7: at most 2^15 in f16
 
@@ -130,9 +137,10 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   constexpr int RB = T::RB, NB = T::NB, SR = T::SR;
   constexpr int KW = KB / 4;  // words
   extern __shared__ uint8_t s_raw[];
-  __shared__ PartEntry s_part[NW][2];              // each warp's partial states: first, last segment
-  __shared__ float s_plse[NW][2][kMaxGroupPerCta]; // their lse
-  __shared__ int s_last[2 * NW];
+  __shared__ float s_plse[NW][2][kMaxGroupPerCta]; // lse of each warp's partial states: first, last segment
+  __shared__ int s_cnt[NW][2];                     // units that have arrived, by a segment's first such state
+  __shared__ WideMerge s_wide[NW + 2];
+  __shared__ int s_n_wide, s_done[NW];             // s_done: stages each warp has computed
   __shared__ WorkerStart s_start[NW];
   // of each tile of two batches of 32 (ROWS: of a stage): which rows count (bit r: row r), and the
   // attended index of row 0; of rows with two scale bytes that were copied one by one, which half of
@@ -149,8 +157,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   const uint32_t ring = smem_u32(my_ring);
   // the rings' space before the first fill: scratch of the start-up scan; after a warp's last
   // tile, its part: the state of its last segment
-  static_assert(NW * T::kRing >= kStartCacheB * 4, "scratch");
-  int* const s_units = reinterpret_cast<int*>(rings);
+  static_assert(NW * T::kRing >= (NT + 1) * 8, "scratch");
   auto state_of = [&](int w, int side) -> float* {
     return reinterpret_cast<float*>(side ? rings + w * T::kRing : rings + NW * T::kRing + w * T::kState);
   };
@@ -166,8 +173,10 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     pdl_release();
     waited = true;
   }
-  worker_starts<NT, NW>(p, s_start, s_units);
-  if (lane < 2) s_part[warp][lane].b = -1;
+  line_starts<NT, NW>(p, s_start, reinterpret_cast<long long*>(rings));
+  if (lane < 2) s_cnt[warp][lane] = 0;
+  if (lane == 0) s_done[warp] = 0;
+  if (threadIdx.x == 0) s_n_wide = 0;
   __syncthreads();  // no block-wide barrier until every warp has finished its range
 
   const int g_id = lane >> 2, q4 = lane & 3;
@@ -210,7 +219,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   // The ring: NQ tiles at a time are computed from stage `cst`, which then takes the ones that follow
   // the other stage's; one group of copies a stage.
   static_assert(NST == 2 && NST * NQ <= 16, "two stages, well within a batch of 32 tiles");
-  int cst = 0;
+  int cst = 0, stages = 0;
   if (!p.early_inputs && !waited) {
     pdl_wait();
     pdl_release();
@@ -653,56 +662,178 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     k_issued += NQ;
     cp_async_group();
     cst ^= 1;
+    // A scheduler's older warps run ahead of its younger ones, which then end alone and leave it idle:
+    // a warp that is kLead stages ahead of another of its scheduler lets it catch up for a moment.
+    ++stages;
+    if constexpr (NW > 4) {
+      if ((stages & 3) == 0) {
+        if (lane == 0) *(volatile int*)&s_done[warp] = stages;
+        int least = INT_MAX;
+#pragma unroll
+        for (int i = 4; i < NW; i += 4) least = min(least, *(volatile int*)&s_done[warp + i < NW ? warp + i : warp + i - NW]);
+        if (stages > least + kLead) __nanosleep(kNap);
+      }
+    }
   }
   st_d[0] = sum_over_groups(st_d[0]);
   st_d[1] = sum_over_groups(st_d[1]);
 
   // ---------------------------------------------------------------- finish the segment
   // This thread holds columns 2 q4 (o0, o2) and 2 q4 + 1 (o1, o3), dims RL g_id .. + RL - 1.
-  // A segment within the range goes to out/lse; else its state (O / d, lse) waits in shared
-  // memory for the block's other warps.
-  const bool all = (ua == 0 && ub == sg.n);
-  const int side = sg.off <= ws.x0 ? 0 : 1;
+  float lse[2];
 #pragma unroll
-  for (int hh = 0; hh < 2; ++hh) {
-    const int j = 2 * q4 + hh;
-    if (j < hcount) {
-      const bool empty = st_d[hh] == 0.f;
-      float inv = empty ? 0.f : p.out_scale / st_d[hh];
-      float l = empty ? kEmptyM : log2f(st_d[hh]) - nm[hh];
-      const size_t row = col_row<MQ>(p, sg.b, hk, c0 + j);
-      if (all && p.sink) {
-        const SinkAdj sa = apply_sink(p, col_head<MQ>(p, hk, c0 + j), l);
-        inv *= sa.scale;
-        l = sa.lse;
-      }
+  for (int h = 0; h < 2; ++h) {
+    const bool empty = st_d[h] == 0.f;
+    lse[h] = empty ? kEmptyM : log2f(st_d[h]) - nm[h];
+    const float inv = empty ? 0.f : p.out_scale / st_d[h];
 #pragma unroll
-      for (int o = 0; o < RL / 4; ++o) {
-        const float4 v = make_float4(oacc[2 * o][hh] * inv, oacc[2 * o][hh + 2] * inv,
-                                     oacc[2 * o + 1][hh] * inv, oacc[2 * o + 1][hh + 2] * inv);
-        if (all) store_four(p, row * D + RL * g_id + 4 * o, v);
-        else reinterpret_cast<float4*>(state_of(warp, side) + j * D + RL * g_id)[o] = v;
+    for (int mt = 0; mt < KT; ++mt) oacc[mt][h] *= inv, oacc[mt][h + 2] *= inv;
+  }
+  // the state to memory, and another one's from it: lse_M = M + log2 (2^(lse - M) + 2^(l - M))
+  auto put_state = [&](float* o, float* l) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = 2 * q4 + h;
+      if (j >= hcount) continue;
+#pragma unroll
+      for (int x = 0; x < RL / 4; ++x)
+        reinterpret_cast<float4*>(o + j * D + RL * g_id)[x] =
+            make_float4(oacc[2 * x][h], oacc[2 * x][h + 2], oacc[2 * x + 1][h], oacc[2 * x + 1][h + 2]);
+      if (g_id == 0) l[j] = lse[h];
+    }
+  };
+  bool mine = true;  // whether this warp writes the output
+  if (ua != 0 || ub != sg.n) {
+    const PartMerge e{sg.off, ws.U, sg.b, sg.hz, sg.n, hk, c0, hcount, C, zg};
+    // its units in the block, how many warps hold some, and which is the first
+    int in_block = 0, states = 0, lw = 0;
+#pragma unroll 1
+    for (int i = NW - zg + warp % zg; i >= 0; i -= zg) {
+      const int n = units_within(sg.off, C, sg.n, s_start[i].x0, s_start[i].x1);
+      in_block += n;
+      states += n > 0;
+      lw = n > 0 ? i : lw;
+    }
+    const int ls = sg.off > s_start[lw].x0;
+    const bool wide = states > kWarpStates;
+    SegmentBlocks sb{};
+    // first the block's warps (from shared memory), then the blocks (from their slots)
+#pragma unroll 1
+    for (int level = in_block == ub - ua ? 1 : 0; level < 2; ++level) {
+      int last = 0;
+      if (level == 0) {
+        const int side = sg.off > ws.x0;
+        // (if all others are there already the state need not go to memory)
+        if (lane == 0) last = !wide && *(volatile int*)&s_cnt[lw][ls] + (ub - ua) == in_block;
+        last = __shfl_sync(0xffffffffu, last, 0);
+        if (!last) {
+          put_state(state_of(warp, side), s_plse[warp][side]);
+          __threadfence_block();
+          __syncwarp();
+          if (lane == 0) last = atomicAdd(&s_cnt[lw][ls], ub - ua) + (ub - ua) == in_block;
+          last = __shfl_sync(0xffffffffu, last, 0);
+        }
+        __threadfence_block();
+        if (last && wide) {
+          if (lane == 0) s_wide[atomicAdd(&s_n_wide, 1)] = WideMerge{e, in_block};
+          last = 0;
+        }
+      } else {
+        if (in_block == sg.n) break;
+        sb = blocks_of(e);
+        const long long at = slot_of(e, sb, (int)(blockIdx.x - sb.first));
+        put_state(p.part_o + at * D, p.part_lse + at);
+        fence_acq_rel_gpu();
+        __syncwarp();
+        if (lane == 0) {
+          int* cnt = p.counters + (size_t)sg.b * p.H_kv * p.n_z + sg.hz;
+          last = atomicAdd(cnt, in_block) + in_block == sg.n;
+          if (last) *cnt = 0;  // every other block's units have arrived: reset for reuse
+        }
+        last = __shfl_sync(0xffffffffu, last, 0);
+        fence_acq_rel_gpu();
+        if (last && sb.n > kWarpMerge) {
+          if (lane == 0) s_wide[atomicAdd(&s_n_wide, 1)] = WideMerge{e, 0};
+          last = 0;
+        }
       }
-      if (g_id == 0) {
-        if (all) p.lse[row] = l;
-        else s_plse[warp][side][j] = l;
+      if (!last) {
+        mine = false;
+        break;
+      }
+      const int count = level ? sb.n : NW;
+#pragma unroll 1
+      for (int i = level ? 0 : lw; i < count; i += level ? 1 : zg) {
+        const float* o;
+        const float* l;
+        if (level == 0) {
+          if (i == warp || units_within(sg.off, C, sg.n, s_start[i].x0, s_start[i].x1) == 0) continue;
+          const int side = sg.off > s_start[i].x0;
+          o = state_of(i, side);
+          l = s_plse[i][side];
+        } else {
+          if (sb.first + i == blockIdx.x || !holds_units(e, sb, i)) continue;
+          const long long at = slot_of(e, sb, i);
+          o = p.part_o + at * D;
+          l = p.part_lse + at;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = min(2 * q4 + h, hcount - 1);
+          const float other = l[j];
+          float4 v[RL / 4];
+#pragma unroll
+          for (int x = 0; x < RL / 4; ++x) v[x] = reinterpret_cast<const float4*>(o + j * D + RL * g_id)[x];
+          const float M = fmaxf(lse[h], other);
+          // (NaN counts; two empty states stay one)
+          const float a = lse[h] <= kEmptyM ? 0.f : fast_exp2(lse[h] - M), b = other <= kEmptyM ? 0.f : fast_exp2(other - M);
+          const float den = a + b;
+          const float wa = den == 0.f ? 0.f : a / den, wb = den == 0.f ? 0.f : b / den;
+          lse[h] = den == 0.f ? kEmptyM : M + log2f(den);
+#pragma unroll
+          for (int x = 0; x < RL / 4; ++x) {
+            oacc[2 * x][h] = fmaf(oacc[2 * x][h], wa, v[x].x * wb);
+            oacc[2 * x][h + 2] = fmaf(oacc[2 * x][h + 2], wa, v[x].y * wb);
+            oacc[2 * x + 1][h] = fmaf(oacc[2 * x + 1][h], wa, v[x].z * wb);
+            oacc[2 * x + 1][h + 2] = fmaf(oacc[2 * x + 1][h + 2], wa, v[x].w * wb);
+          }
+        }
       }
     }
   }
-  if (!all && lane == 0) s_part[warp][side] = PartEntry{sg.off, sg.b, sg.hz, ub - ua, sg.n, hk, c0, hcount};
+  if (mine) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = 2 * q4 + h;
+      if (j >= hcount) continue;
+      const size_t row = col_row<MQ>(p, sg.b, hk, c0 + j);
+      float inv = 1.f;
+      if (p.sink) {
+        const SinkAdj sa = apply_sink(p, col_head<MQ>(p, hk, c0 + j), lse[h]);
+        inv = sa.scale;
+        lse[h] = sa.lse;
+      }
+#pragma unroll
+      for (int x = 0; x < RL / 4; ++x)
+        store_four(p, row * D + RL * g_id + 4 * x,
+                   make_float4(oacc[2 * x][h] * inv, oacc[2 * x][h + 2] * inv, oacc[2 * x + 1][h] * inv,
+                               oacc[2 * x + 1][h + 2] * inv));
+      if (g_id == 0) p.lse[row] = lse[h];
+    }
+  }
   }  // ua < ub
   if (sg.off + C + sg.n >= cx1 || !next_segment(p, sg, C)) break;
   }  // segments
-  if (!waited) pdl_wait();  // (a worker without units: the block's partials still follow it)
-
-  merge_parts<D, MQ, NW>(p, s_part, s_plse, s_last, s_start[0], C, zg, state_of);
+  if (!waited) pdl_wait();  // (a worker without units: what the block merges may still follow it)
+  if (lane == 0) *(volatile int*)&s_done[warp] = INT_MAX / 2;
+  merge_wide<D, MQ, NW>(p, s_wide, s_n_wide, s_start, s_plse, state_of);
 }
 
 // ----------------------------------------------------------------------------- launch
 template <int SB, bool SPLIT, int D, bool MQ, bool ROWS>
 static cudaError_t launch_mx_t(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg) {
-  constexpr int NW = kMmaWarps;
-  constexpr int BLOCKS = SPLIT || D == 256 ? 2 : 3;
+  constexpr int NW = mx_warps(SPLIT, D);
+  constexpr int BLOCKS = 1;
   constexpr int dyn = mx_smem_bytes<SB, D, ROWS, NW>();
   auto kern = decode_mx_kernel<SB, SPLIT, D, MQ, ROWS, NW, BLOCKS>;
   // the dynamic shared memory above 48 KB is opted into on every query of the launch

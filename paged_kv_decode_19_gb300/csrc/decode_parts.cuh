@@ -72,7 +72,232 @@ struct PartEntry {
   int b, hz, mine, n, hk, c0, hcount;
 };
 
-// ----------------------------------------------------------------------------- partial states
+// ----------------------------------------------------------------------------- line starts
+// The start of each of the block's NW workers on the cost line, as worker_starts (decode_common.cuh)
+// gives it, by a binary search over the sequences' places: those of a host plan, or sums made here by
+// the whole block (each thread those of `per` consecutive sequences).  Ends with a block barrier.
+template <int NT, int NW>
+__device__ __forceinline__ void line_starts(const DecodeParams& p, WorkerStart* s_ws, long long* s_pre) {
+  __shared__ long long s_warp[NT / 32];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, C = p.seg_cost;
+  const int zg = p.mode == kSchedBalanced ? p.zg : 1, HZ = p.H_kv * p.n_z / zg;
+  const int per = p.hp_B ? 1 : (p.B + NT - 1) / NT;
+  auto cost = [&](int b) { return units_of(load_seq(p, b), p.P) + C; };
+  if (p.mode == kSchedBalanced && !p.hp_B) {
+    long long mine = 0;
+    for (int b = min(tid * per, p.B); b < min((tid + 1) * per, p.B); ++b) mine += cost(b);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) s_warp[wid] = incl;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < wid; ++i) incl += s_warp[i];
+    s_pre[tid] = incl - mine;
+    if (tid == NT - 1) s_pre[NT] = incl;
+    __syncthreads();
+  }
+  if (tid < NW) {
+    WorkerStart s{};
+    s.b = -1;
+    if (p.mode == kSchedBalanced) {
+      const int parts = p.hp_B ? p.B : NT;  // places known: of each sequence, or of each thread's
+      auto place = [&](int i) { return p.hp_B ? (long long)p.hp[i] : s_pre[i]; };
+      const long long W = (long long)gridDim.x * NW / zg, w = ((long long)blockIdx.x * NW + tid) / zg;
+      s.U = place(parts) * HZ;
+      s.x0 = div_floor(w * s.U, W);
+      s.x1 = div_floor((w + 1) * s.U, W);
+      if (s.x0 < s.x1) {
+        int lo = 0, hi = parts - 1;  // last i with place(i) * HZ <= x0
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (place(mid) * HZ <= s.x0) lo = mid;
+          else hi = mid - 1;
+        }
+        long long first = place(lo);
+        int b = lo, n;
+        if (p.hp_B) {
+          n = p.hp[lo + 1] - p.hp[lo];
+        } else {
+          b = lo * per;
+          while ((first + (n = cost(b))) * HZ <= s.x0) {
+            first += n;
+            ++b;
+          }
+        }
+        s.b = b;
+        s.hz = (int)div_floor(s.x0 - first * HZ, n);
+        s.off = first * HZ + (long long)s.hz * n;
+        s.hz = s.hz * zg + tid % zg;  // (NW is a multiple of zg)
+      }
+    } else if (p.mode == kSchedPerBlock) {
+      s.b = (int)(blockIdx.x / HZ);
+      s.hz = (int)(blockIdx.x - (unsigned)s.b * HZ);
+      s.U = units_of(load_seq(p, s.b), p.P);
+      s.x0 = tid * s.U / NW;
+      s.x1 = (tid + 1) * s.U / NW;
+      if (s.x0 == s.x1) s.b = -1;
+    } else {
+      const long long w = (long long)blockIdx.x * NW + tid;
+      s.U = (long long)p.B * HZ;
+      if (w < s.U) {
+        s.b = (int)(w / HZ);
+        s.hz = (int)(w - (long long)s.b * HZ);
+        s.x1 = LLONG_MAX;
+      }
+    }
+    s_ws[tid] = s;
+  }
+  __syncthreads();
+}
+
+// ----------------------------------------------------------------------------- states in registers
+// A segment shared by several warps, of one block or of several, is merged by the one that completes
+// it, from its own registers: the others leave their normalised states (outputs and lse) in shared
+// memory, a block's merged state in its slot of the workspace, and go on.
+struct PartMerge {
+  long long off, U;  // the segment's place on the cost line, and the line's length
+  int b, hz, n, hk, c0, hcount, C, zg;
+};
+
+// The units of a segment at line position off within the positions [x0, x1).
+__device__ __forceinline__ int units_within(long long off, int C, int n, long long x0, long long x1) {
+  return (int)(min(max(x1 - off - C, 0ll), (long long)n) - min(max(x0 - off - C, 0ll), (long long)n));
+}
+
+// Blocks whose states one warp merges by itself, one after the other (a trip to L2 each); the states of
+// more are left for the whole block.
+#ifndef WM
+#define WM 4
+#endif
+constexpr int kWarpMerge = WM;
+
+// The first block that holds units of a segment, how many blocks do, and the slot of one's state:
+// two per block and slice of side-by-side columns, for the segment that the block's range starts in
+// (or at) and the one that it ends in.
+struct SegmentBlocks {
+  long long first;
+  int n;
+  bool ends_in;  // the first block's range does not start in the segment
+};
+__device__ __forceinline__ SegmentBlocks blocks_of(const PartMerge& e) {
+  const long long G = gridDim.x;
+  SegmentBlocks s;
+  s.first = share_of(e.off + e.C, e.U, G);
+  s.n = (int)(share_of(e.off + e.C + e.n - 1, e.U, G) - s.first + 1);
+  s.ends_in = e.off > div_floor(s.first * e.U, G);
+  return s;
+}
+__device__ __forceinline__ long long slot_of(const PartMerge& e, const SegmentBlocks& s, int i) {
+  return ((2 * (s.first + i) + (i == 0 && s.ends_in)) * e.zg + (e.zg > 1 ? e.hz % e.zg : 0)) * kMaxGroupPerCta;
+}
+// Whether block first + i has units: with fewer positions than blocks some between have none.
+__device__ __forceinline__ bool holds_units(const PartMerge& e, const SegmentBlocks& s, int i) {
+  const long long G = gridDim.x;
+  return e.U >= G || div_floor((s.first + i) * e.U, G) < div_floor((s.first + i + 1) * e.U, G);
+}
+
+// One more state (o, l) into unnormalised sums of four dims against a running maximum.
+__device__ __forceinline__ void add_state(float& M, float& den, float4& acc, float l, float4 o) {
+  if (l <= kEmptyM) return;  // (NaN counts)
+  const float m = fmaxf(M, l), f = fast_exp2(M - m), x = fast_exp2(l - m);
+  M = m;
+  den = fmaf(den, f, x);
+  acc = make_float4(fmaf(acc.x, f, o.x * x), fmaf(acc.y, f, o.y * x), fmaf(acc.z, f, o.z * x), fmaf(acc.w, f, o.w * x));
+}
+
+// Segments for the whole block to merge at its end: of more than kWarpStates of its warps (their states
+// in shared memory: state_of(warp, side), s_plse), or of more than kWarpMerge blocks (published).
+struct WideMerge {
+  PartMerge e;
+  int in_block;  // units in the block to merge and publish; 0: the blocks' states are all there
+};
+#ifndef WS
+#define WS 4
+#endif
+constexpr int kWarpStates = WS;
+template <int D, bool MQ, int NW, typename StateOf>
+__device__ __forceinline__ void merge_wide(const DecodeParams& p, const WideMerge* s_wide, const int& s_n,
+                                           const WorkerStart (&s_start)[NW],
+                                           const float (&s_plse)[NW][2][kMaxGroupPerCta], StateOf state_of) {
+  __shared__ int s_all;
+  __syncthreads();
+#pragma unroll 1
+  for (int w = 0; w < s_n; ++w) {
+    const PartMerge e = s_wide[w].e;
+    const int in_block = s_wide[w].in_block;
+    const SegmentBlocks s = p.mode == kSchedBalanced ? blocks_of(e) : SegmentBlocks{0, 1, false};
+    const int z = e.zg > 1 ? e.hz % e.zg : 0;
+    bool final = in_block == e.n;
+    // the block's own states, then (if it completes the segment) the blocks'
+#pragma unroll 1
+    for (int level = in_block ? 0 : 1; level < 2; ++level) {
+#pragma unroll 1
+      for (int it = threadIdx.x; it < e.hcount * (D / 4); it += NW * 32) {
+        const int j = it / (D / 4), d = it % (D / 4) * 4;
+        float M = kEmptyM, den = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (level == 0) {
+#pragma unroll 1
+          for (int i = z; i < NW; i += e.zg) {
+            if (units_within(e.off, e.C, e.n, s_start[i].x0, s_start[i].x1) == 0) continue;
+            const int side = e.off > s_start[i].x0;
+            add_state(M, den, acc, s_plse[i][side][j], *reinterpret_cast<const float4*>(state_of(i, side) + j * D + d));
+          }
+        } else {
+#pragma unroll 1
+          for (int i0 = 0; i0 < s.n; i0 += 8) {  // eight states' lse and rows in flight together
+            float l[8];
+            float4 o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const long long at = slot_of(e, s, min(i0 + i, s.n - 1)) + j;
+              l[i] = __ldcg(p.part_lse + at);
+              o[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i0 + i < s.n && holds_units(e, s, i0 + i)) add_state(M, den, acc, l[i], o[i]);
+          }
+        }
+        const bool empty = den == 0.f;
+        float inv = empty ? 0.f : 1.f / den;
+        float l = empty ? kEmptyM : M + log2f(den);
+        if (final || level == 1) {
+          if (p.sink) {
+            const SinkAdj sa = apply_sink(p, col_head<MQ>(p, e.hk, e.c0 + j), l);
+            inv *= sa.scale;
+            l = sa.lse;
+          }
+          const size_t row = col_row<MQ>(p, e.b, e.hk, e.c0 + j);
+          store_four(p, row * D + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+          if (d == 0) p.lse[row] = l;
+        } else {
+          const long long at = slot_of(e, s, (int)(blockIdx.x - s.first)) + j;
+          *reinterpret_cast<float4*>(p.part_o + at * D + d) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          if (d == 0) p.part_lse[at] = l;
+        }
+      }
+      if (level == 1 || final) break;
+      fence_acq_rel_gpu();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        int* cnt = p.counters + (size_t)e.b * p.H_kv * p.n_z + e.hz;
+        s_all = atomicAdd(cnt, in_block) + in_block == e.n;
+        if (s_all) *cnt = 0;  // every other block's units have arrived: reset for reuse
+      }
+      __syncthreads();
+      if (!s_all) break;
+      fence_acq_rel_gpu();
+    }
+    __syncthreads();  // (s_all is written again)
+  }
+}
+
+// ----------------------------------------------------------------------------- states in shared memory
 // A segment's states within the block are merged first (lse = M + log2 sum 2^(lse_s - M), out =
 // sum 2^(lse_s - M) o_s / sum 2^(lse_s - M)).  If the block holds all of its units that is the
 // result; else the block publishes one state and adds its units to the segment's counter, and
