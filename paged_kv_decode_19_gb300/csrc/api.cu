@@ -1027,7 +1027,7 @@ pd_status pd_append_paged_kv_mx(void* pages, void* scales, const void* k_new, co
     return fail(PD_ERR_INVALID_ARG, "k_stride and v_stride must be at least H_kv * D");
   if (d.max_pages > INT_MAX || d.max_pages * 2 * d.H_kv > INT_MAX)
     return fail(PD_ERR_UNSUPPORTED, "max_pages * 2 * H_kv exceeds 2^31");
-  if ((long long)d.T * d.H_kv > INT_MAX || d.T > (1 << 30) || row > INT_MAX)
+  if ((long long)d.T * d.H_kv > INT_MAX || d.T > (1 << 30) || row > (1 << 28))
     return fail(PD_ERR_UNSUPPORTED, "T or H_kv too large");
   if (d.T == 0) return PD_OK;
   if (!pages || !scales || !k_new || !v_new || !slot_mapping) return fail(PD_ERR_INVALID_ARG, "NULL device pointer");
@@ -1053,8 +1053,7 @@ pd_status pd_append_paged_kv_mx(void* pages, void* scales, const void* k_new, co
   a.T = d.T;
   a.H_kv = d.H_kv;
   a.P = d.page_size;
-  const cudaError_t e = launch_append_mx(a, d.D, d.kv_dtype == PD_MX_E4M3 ? 16 : 32, d.in_dtype, ds->num_sms,
-                                         (cudaStream_t)stream);
+  const cudaError_t e = launch_append_mx(a, d.D, d.kv_dtype == PD_MX_E4M3 ? 16 : 32, d.in_dtype, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "append launch");
   return PD_OK;
 }

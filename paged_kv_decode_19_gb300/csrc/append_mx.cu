@@ -15,6 +15,7 @@
 // nothing but their own values, so a thread takes 16 dims, which share a scale (two threads of 32),
 // and the stores alone wait for the token's slot.
 #include <algorithm>
+#include <cfloat>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -54,6 +55,19 @@ __device__ __forceinline__ void load16(const IT* src, float (&x)[16]) {
   }
 }
 
+// y / s, correctly rounded, for the s of a scale (at most four significant bits, r = 1 / s rounded):
+// Markstein's correction of a product by the remainder, which the fma gives exactly.
+__device__ __forceinline__ float quotient(float y, float s, float r) {
+  const float q = y * r;
+  return copysignf(fmaf(fmaf(-q, s, y), r, q), y);  // (a zero keeps its sign)
+}
+// The larger of two magnitudes, NaN if either is.
+__device__ __forceinline__ float max_abs(float m, float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(x)));
+  return r;
+}
+
 // Eight values already divided by their scale -> eight codes, the first in the lowest bits.
 __device__ __forceinline__ uint32_t encode8(const float* q) {
   uint32_t r;
@@ -69,86 +83,108 @@ __device__ __forceinline__ uint32_t encode8(const float* q) {
 }
 }  // namespace
 
+// n / d for n < 2^31 by a multiplication.
+struct Divisor {
+  unsigned mul, shift, d;
+  explicit Divisor(unsigned by) : d(by) {
+    for (shift = 0; shift < 32 && (1ull << shift) < by; ++shift) {}
+    mul = (unsigned)(((1ull << 32) * ((1ull << shift) - by)) / by + 1);
+  }
+  __device__ __forceinline__ unsigned quot(unsigned n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 template <typename IT, int SB, bool VEC>
-__global__ void __launch_bounds__(kThreads) append_mx_kernel(const __grid_constant__ AppendMxParams a, int D) {
-  const int per_row = a.H_kv * (D / 16);  // threads of a token's K (or V)
-  const long long items = 2ll * a.T * per_row;
+__global__ void __launch_bounds__(kThreads)
+    append_mx_kernel(const __grid_constant__ AppendMxParams a, const __grid_constant__ Divisor per_row, int log_d) {
   pdl_wait();  // inputs and pages are the previous kernel's to write until it completes
   pdl_release();
-  // a warp's 32 items (SB 32: a block's two are side by side, as per_row is even) in step
-  for (long long i0 = (long long)blockIdx.x * kThreads + (threadIdx.x & ~31u); i0 < items;
-       i0 += (long long)gridDim.x * kThreads) {
-    const long long i = min(i0 + (threadIdx.x & 31), items - 1);
-    const int row = (int)(i / per_row), j = (int)(i - (long long)row * per_row);
-    const int t = row >> 1, kv = row & 1;
-    long long slot = __ldg(a.slots + t);
-    float y[16];
-    load16<IT, VEC>(reinterpret_cast<const IT*>(kv ? a.v_new : a.k_new) + t * (kv ? a.v_stride : a.k_stride) + 16 * j, y);
-    const float g = kv ? a.v_scale : a.k_scale;
-    if (g != 1.f) {
+  // an item is 16 dims of a token's K or V: item = (token, K | V, head, 16 dims); SB 32: a block's two
+  // are side by side, in one warp
+  const unsigned items = 2u * a.T * per_row.d, i0 = blockIdx.x * kThreads + threadIdx.x;
+  const unsigned i = min(i0, items - 1);
+  const unsigned row = per_row.quot(i), j = i - row * per_row.d;
+  const int t = row >> 1, kv = row & 1;
+  long long slot = __ldg(a.slots + t);
+  float y[16];
+  load16<IT, VEC>(reinterpret_cast<const IT*>(kv ? a.v_new : a.k_new) + t * (kv ? a.v_stride : a.k_stride) + 16 * j, y);
+  const float g = kv ? a.v_scale : a.k_scale;
+  if (g != 1.f) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = __fdiv_rn(y[e], g);
-    }
-    unsigned m = 0;  // magnitude patterns order like the values, and a non-finite one shows as the largest
-#pragma unroll
-    for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(y[e]) & 0x7fffffffu);
-    if constexpr (SB == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    const bool finite = m < 0x7f800000u;
-    float s;
-    uint8_t sb;
-    if constexpr (SB == 16) {
-      const uint8_t c = f32_to_e4m3(__fdiv_rn(__uint_as_float(m), 6.f));
-      sb = finite ? max(c, (uint8_t)1) : (uint8_t)0x7f;  // (code 1: 2^-9)
-      F8 f;
-      f.v = sb;
-      s = to_f32(f);
-    } else {
-      // 6 = 1.5 * 2^2: two below the exponent, one more where the significand is above 1.5
-      const int k = (int)(m >> 23) - 2 + ((m & 0x7fffffu) > 0x400000u ? 1 : 0);
-      sb = finite ? (uint8_t)min(max(k, 127 - 14), 127 + 13) : (uint8_t)0xff;
-      s = __uint_as_float((254u - sb) << 23);  // the inverse 2^-k, exact
-    }
-    uint2 codes = make_uint2(0u, 0u);
-    if (finite) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = SB == 16 ? __fdiv_rn(y[e], s) : y[e] * s;
-      codes = make_uint2(encode8(y), encode8(y + 8));
-    }
-    if (slot >= a.n_slots) {
-      set_error(a.err, kErrBadSlot);
-      slot = -1;
-    }
-    if (slot >= 0 && i == i0 + (threadIdx.x & 31)) {
-      const long long page = slot / a.P;
-      const int h = 16 * j / D, d = 16 * j - h * D;
-      const long long at = ((page * 2 + kv) * a.H_kv + h) * a.P + (slot - page * a.P);  // the row in the cache
-      *reinterpret_cast<uint2*>(a.pages + at * (D / 2) + d / 2) = codes;
-      if (SB == 16 || (d & 16) == 0) a.scales[at * (D / SB) + d / SB] = sb;
-    }
+    for (int e = 0; e < 16; ++e) y[e] = __fdiv_rn(y[e], g);
   }
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) m = max_abs(m, y[e]);
+  if constexpr (SB == 32) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  const bool finite = m <= FLT_MAX;
+  float s, r;
+  uint8_t sb;
+  if constexpr (SB == 16) {
+    const uint8_t c = f32_to_e4m3(__fdiv_rn(m, 6.f));
+    sb = finite ? max(c, (uint8_t)1) : (uint8_t)0x7f;  // (code 1: 2^-9)
+    F8 f;
+    f.v = sb;
+    s = to_f32(f);
+    r = __frcp_rn(s);
+  } else {
+    // 6 = 1.5 * 2^2: two below the exponent, one more where the significand is above 1.5
+    const unsigned b = __float_as_uint(m);
+    const int k = (int)(b >> 23) - 2 + ((b & 0x7fffffu) > 0x400000u ? 1 : 0);
+    sb = finite ? (uint8_t)min(max(k, 127 - 14), 127 + 13) : (uint8_t)0xff;
+    s = 0.f;
+    r = __uint_as_float((254u - sb) << 23);  // 2^-k: the product is the quotient
+  }
+  uint2 codes = make_uint2(0u, 0u);
+  if (finite) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = SB == 16 ? quotient(y[e], s, r) : y[e] * r;
+    codes = make_uint2(encode8(y), encode8(y + 8));
+  }
+  if (i != i0 || slot < 0) return;
+  if (slot >= a.n_slots) {
+    set_error(a.err, kErrBadSlot);
+    return;
+  }
+  const unsigned h = 16 * j >> log_d, d = 16 * j - (h << log_d);
+  const long long page = slot >> 32 ? slot / a.P : (unsigned)slot / (unsigned)a.P;
+  const long long at = ((page * 2 + kv) * a.H_kv + h) * a.P + (slot - page * a.P);  // the row in the cache
+  *reinterpret_cast<uint2*>(a.pages + (at << (log_d - 1)) + d / 2) = codes;
+  if (SB == 16 || (d & 16) == 0) a.scales[((at << log_d) + d) / SB] = sb;
 }
 
 template <typename IT, int SB>
-static cudaError_t launch_t(const AppendMxParams& a, int D, bool vec, int num_sms, cudaStream_t st) {
-  const long long items = 2ll * a.T * a.H_kv * (D / 16);
-  const dim3 grid((unsigned)std::min<long long>((items + kThreads - 1) / kThreads, (long long)num_sms * 32));
-  return vec ? launch_pdl(append_mx_kernel<IT, SB, true>, grid, dim3(kThreads), 0, st, a, D)
-             : launch_pdl(append_mx_kernel<IT, SB, false>, grid, dim3(kThreads), 0, st, a, D);
+static cudaError_t launch_t(const AppendMxParams& all, int D, bool vec, cudaStream_t st) {
+  const Divisor per_row((unsigned)(all.H_kv * (D / 16)));
+  const int log_d = D == 64 ? 6 : D == 128 ? 7 : 8;
+  // as many tokens a launch as keep the items below 2^31
+  const int most = (int)std::max(1ll, (1ll << 30) / (2ll * per_row.d));
+  for (int t0 = 0; t0 < all.T; t0 += most) {
+    AppendMxParams a = all;
+    a.T = std::min(most, all.T - t0);
+    a.slots += t0;
+    a.k_new = reinterpret_cast<const IT*>(a.k_new) + t0 * a.k_stride;
+    a.v_new = reinterpret_cast<const IT*>(a.v_new) + t0 * a.v_stride;
+    const dim3 grid((unsigned)((2ll * a.T * per_row.d + kThreads - 1) / kThreads));
+    const cudaError_t e = vec ? launch_pdl(append_mx_kernel<IT, SB, true>, grid, dim3(kThreads), 0, st, a, per_row, log_d)
+                              : launch_pdl(append_mx_kernel<IT, SB, false>, grid, dim3(kThreads), 0, st, a, per_row, log_d);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 template <typename IT>
-static cudaError_t launch_i(const AppendMxParams& a, int D, int sb, bool vec, int num_sms, cudaStream_t st) {
-  return sb == 16 ? launch_t<IT, 16>(a, D, vec, num_sms, st) : launch_t<IT, 32>(a, D, vec, num_sms, st);
+static cudaError_t launch_i(const AppendMxParams& a, int D, int sb, bool vec, cudaStream_t st) {
+  return sb == 16 ? launch_t<IT, 16>(a, D, vec, st) : launch_t<IT, 32>(a, D, vec, st);
 }
 
-cudaError_t launch_append_mx(const AppendMxParams& a, int D, int sb, int in_dtype, int num_sms, cudaStream_t st) {
+cudaError_t launch_append_mx(const AppendMxParams& a, int D, int sb, int in_dtype, cudaStream_t st) {
   const int eb = in_dtype == kF32 ? 4 : 2;
   // 16-byte loads where the tensors allow them, element loads else
   const bool vec = ((reinterpret_cast<uintptr_t>(a.k_new) | reinterpret_cast<uintptr_t>(a.v_new)) & 15) == 0 &&
                    a.k_stride * eb % 16 == 0 && a.v_stride * eb % 16 == 0;
-  if (in_dtype == kF32) return launch_i<float>(a, D, sb, vec, num_sms, st);
-  if (in_dtype == kF16) return launch_i<__half>(a, D, sb, vec, num_sms, st);
-  if (in_dtype == kBF16) return launch_i<__nv_bfloat16>(a, D, sb, vec, num_sms, st);
+  if (in_dtype == kF32) return launch_i<float>(a, D, sb, vec, st);
+  if (in_dtype == kF16) return launch_i<__half>(a, D, sb, vec, st);
+  if (in_dtype == kBF16) return launch_i<__nv_bfloat16>(a, D, sb, vec, st);
   return cudaErrorInvalidValue;
 }
 

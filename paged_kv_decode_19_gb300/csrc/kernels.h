@@ -106,7 +106,7 @@ struct AppendMxParams {
   float k_scale, v_scale;
   int T, H_kv, P;
 };
-cudaError_t launch_append_mx(const AppendMxParams& a, int D, int sb, int in_dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_append_mx(const AppendMxParams& a, int D, int sb, int in_dtype, cudaStream_t st);
 // Warps of a block of the decode, one block an SM: what its registers allow.
 constexpr int mx_warps(bool q_f32, int D) { return q_f32 || D == 256 ? 8 : 12; }
 // ... and the decode (decode_mx.cuh): 16-bit Q (p.q_bf16), D 64 or 128, page size a multiple of 16

@@ -119,30 +119,16 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_cons
   // (spare + freed within the ring: what is given back then lies behind all that may be taken)
   const bool short_ = a.ring && (head < 0 || spare < 0 || n_grown > spare || spare + n_freed > a.C);
   const bool ok = !long_ && !short_;  // else nothing is taken, and the tables describe empty sequences
-  if (tid == 0) {
+  // Every read of lengths and state is behind the barriers above: the last block to come here may move
+  // them on.  Its last thread asks for the ticket; the answer is looked at when the outputs are written.
+  if (tid == kThreads - 1) {
     if (!ok) set_error(a.err, long_ ? kErrBadLength : kErrNoPages);
-    // every thread's reads of lengths and state are behind the barriers above
-    fence_acq_rel_gpu();
-    const unsigned long long before = atomicAdd(reinterpret_cast<unsigned long long*>(a.state) + 2, 1ull);
+    unsigned long long before = 0;
+    if (gridDim.x > 1) {
+      fence_acq_rel_gpu();
+      before = atomicAdd(reinterpret_cast<unsigned long long*>(a.state) + 2, 1ull);
+    }
     s_flag = before == gridDim.x - 1;
-    fence_acq_rel_gpu();
-  }
-  __syncthreads();
-  if (s_flag) {
-    if (ok) {
-      for (int b = tid; b < B; b += kThreads) {
-        const int n = a.new_tokens[b], len = a.lengths[b];
-        const long long now = (long long)len + n;
-        if (len >= 0 && len <= a.max_rows && now >= 0 && now <= a.max_rows) a.lengths[b] = (int)now;
-      }
-    }
-    if (tid == 0) {
-      if (ok) {
-        a.state[0] = head + n_grown;
-        a.state[1] = tail + n_freed;
-      }
-      a.state[2] = 0;
-    }
   }
   const long long first = (long long)blockIdx.x * kThreads + tid, step = (long long)gridDim.x * kThreads;
   for (long long b = first; b <= B; b += step) {
@@ -165,22 +151,32 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_cons
   }
   if (!ok) n_pages = n_tok = 0;
   const int C = a.C;
-  const int head_at = a.ring && ok ? (int)(head % C) : 0, tail_at = a.ring && ok ? (int)(tail % C) : 0;
+  auto place = [&](long long x) { return x >> 32 ? (int)(x % C) : (int)((unsigned)x % (unsigned)C); };
+  const int head_at = ok && n_grown ? place(head) : 0, tail_at = ok && n_freed ? place(tail) : 0;
   auto wrap = [&](int at0, int i) {  // (at0 + i) mod C, i <= C
     const long long x = (long long)at0 + i;
     return (int)(x >= C ? x - C : x);
   };
   auto held_of = [&](int b) { return (s_len[b] + P - 1) / P; };
-  // page k of request b: held, or the next of the ring
-  auto page_of = [&](int b, int k) {
-    const int held = held_of(b);
-    return a.ring && k >= held ? a.ring[wrap(head_at, s_grown[b] + k - held)] : a.table[b * a.table_stride + k];
-  };
-  for (long long i = first; i < n_pages; i += step) {
-    const int b = request_of(s_pages, B, (int)i), k = (int)i - s_pages[b];
-    const int page = page_of(b, k);
-    a.values[i] = page;
-    if (a.ring && k >= held_of(b)) a.table[b * a.table_stride + k] = page;
+  // four pages a thread at a time: one search, and the loads of all four under way together
+  for (long long i0 = 4 * first; i0 < n_pages; i0 += 4 * step) {
+    int b = request_of(s_pages, B, (int)i0), at[4], page[4];
+    bool taken[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int i = (int)min(i0 + x, n_pages - 1ll);
+      while (i >= s_pages[b + 1]) ++b;
+      const int k = i - s_pages[b], held = held_of(b);
+      at[x] = b;
+      taken[x] = a.ring && k >= held;
+      page[x] = taken[x] ? a.ring[wrap(head_at, s_grown[b] + k - held)] : a.table[b * a.table_stride + k];
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (i0 + x >= n_pages) break;
+      a.values[i0 + x] = page[x];
+      if (taken[x]) a.table[at[x] * a.table_stride + (i0 + x - s_pages[at[x]])] = page[x];
+    }
   }
   if (ok) {
     for (long long i = first; i < n_freed; i += step) {
@@ -196,13 +192,30 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_cons
         const int b = request_of(s_tok, B, (int)t);
         o = s_len[b] + (int)t - s_tok[b];
         const int k = o / P;
-        const int page = a.slots ? page_of(b, k) : 0;
+        const int held = held_of(b);
+        const int page = a.ring && k >= held ? a.ring[wrap(head_at, s_grown[b] + k - held)] : a.table[b * a.table_stride + k];
         if (page < 0) set_error(a.err, kErrBadPage);  // (a table that does not hold the row: skipped)
         else slot = (long long)page * P + (o - k * P);
       }
       if (a.slots) a.slots[t] = slot;
       if (a.positions) a.positions[t] = o;
     }
+  }
+  __syncthreads();
+  if (!s_flag) return;
+  if (ok) {
+    for (int b = tid; b < B; b += kThreads) {
+      const int n = a.new_tokens[b], len = a.lengths[b];
+      const long long now = (long long)len + n;
+      if (len >= 0 && len <= a.max_rows && now >= 0 && now <= a.max_rows) a.lengths[b] = (int)now;
+    }
+  }
+  if (tid == 0) {
+    if (ok) {
+      a.state[0] = head + n_grown;
+      a.state[1] = tail + n_freed;
+    }
+    if (gridDim.x > 1) a.state[2] = 0;
   }
 }
 
