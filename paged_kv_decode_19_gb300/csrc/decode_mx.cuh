@@ -407,24 +407,32 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   [[maybe_unused]] uint32_t ql[SPLIT ? KT : 1][2];
   float cs0, cs1;  // column factors of this lane's score columns: 2^(e - 14) |sm_scale| log2(e) k_scale
   {
-    auto four = [&](int kt) -> float4 {  // this lane's four dims of k-tile kt
-      const int c = kt / (2 * KW), i = kt % (2 * KW);
-      if constexpr (SPLIT) {
-        const uint4 v = qraw[c][i];
-        return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
-      } else {
-        const uint32_t x = comp(qraw[c][i >> 1], 2 * (i & 1)), y = comp(qraw[c][i >> 1], 2 * (i & 1) + 1);
-        const float2 a = p.q_bf16 ? unpack2<__nv_bfloat16>(x) : unpack2<__half>(x);
-        const float2 b = p.q_bf16 ? unpack2<__nv_bfloat16>(y) : unpack2<__half>(y);
-        return make_float4(a.x, a.y, b.x, b.y);
+    float q[KT][4];  // this lane's four dims of each k-tile
+    auto unpack = [&](auto tag) {
+      using QT = decltype(tag);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const int c = kt / (2 * KW), i = kt % (2 * KW);
+        if constexpr (SPLIT) {
+          const uint4 v = qraw[c][i];
+          q[kt][0] = __uint_as_float(v.x), q[kt][1] = __uint_as_float(v.y);
+          q[kt][2] = __uint_as_float(v.z), q[kt][3] = __uint_as_float(v.w);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float2 f = unpack2<QT>(comp(qraw[c][i >> 1], 2 * (i & 1) + h));
+            q[kt][2 * h] = f.x, q[kt][2 * h + 1] = f.y;
+          }
+        }
       }
     };
+    if (p.q_bf16) unpack(__nv_bfloat16{});
+    else unpack(__half{});
     float amax = 0.f;
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      const float4 f = four(kt);
-      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w))));
-    }
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fabsf(q[kt][i]));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     // 2^(14 - e) and its inverse, both normal: e is kept in [-100, 126]
@@ -433,16 +441,13 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     // (at least the least normal float, so that the -inf of a row that does not count stays one)
     const float cs = fmaxf(__uint_as_float((unsigned)(127 - 14 + e) << 23) * fabsf(p.score_scale), FLT_MIN);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      const float4 f = four(kt);
-      if constexpr (SPLIT) {
-        split2<__half>(f.x * up, f.y * up, qf[kt][0], ql[kt][0]);
-        split2<__half>(f.z * up, f.w * up, qf[kt][1], ql[kt][1]);
-      } else {
-        qf[kt][0] = pack2<__half>(f.x * up, f.y * up);
-        qf[kt][1] = pack2<__half>(f.z * up, f.w * up);
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float x = q[kt][2 * h] * up, y = q[kt][2 * h + 1] * up;
+        if constexpr (SPLIT) split2<__half>(x, y, qf[kt][h], ql[kt][h]);
+        else qf[kt][h] = pack2<__half>(x, y);
       }
-    }
     cs0 = __shfl_sync(0xffffffffu, cs, 8 * q4);      // column 2 q4
     cs1 = __shfl_sync(0xffffffffu, cs, 8 * q4 + 4);  // column 2 q4 + 1
   }

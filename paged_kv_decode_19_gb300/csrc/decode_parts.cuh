@@ -3,6 +3,8 @@
 // workers of a block and the blocks of a segment leave.
 #pragma once
 
+#include <type_traits>
+
 #include "decode_common.cuh"
 
 namespace pd {
@@ -220,81 +222,84 @@ struct WideMerge {
 #endif
 constexpr int kWarpStates = WS;
 template <int D, bool MQ, int NW, typename StateOf>
-__device__ __forceinline__ void merge_wide(const DecodeParams& p, const WideMerge* s_wide, const int& s_n,
+__device__ __forceinline__ void merge_wide(const DecodeParams& p, const WideMerge (&s_wide)[NW + 2], const int& s_n,
                                            const WorkerStart (&s_start)[NW],
                                            const float (&s_plse)[NW][2][kMaxGroupPerCta], StateOf state_of) {
-  __shared__ int s_all;
+  constexpr int NT = NW * 32, kItems = kMaxGroupPerCta * (D / 4);  // of a segment: a column and four dims each
+  __shared__ bool s_all[NW + 2];  // the segment is complete, and its blocks' states are to be merged
   __syncthreads();
+  const int n = s_n;
+  if (n == 0) return;
+  // all segments at each step: the block's own states; the count of their units; the blocks' states
+  auto merge = [&](auto of_blocks) {
 #pragma unroll 1
-  for (int w = 0; w < s_n; ++w) {
-    const PartMerge e = s_wide[w].e;
-    const int in_block = s_wide[w].in_block;
-    const SegmentBlocks s = p.mode == kSchedBalanced ? blocks_of(e) : SegmentBlocks{0, 1, false};
-    const int z = e.zg > 1 ? e.hz % e.zg : 0;
-    bool final = in_block == e.n;
-    // the block's own states, then (if it completes the segment) the blocks'
+    for (int x = threadIdx.x; x < n * kItems; x += NT) {
+      const int w = x / kItems, j = x % kItems / (D / 4), d = x % (D / 4) * 4;
+      const PartMerge& e = s_wide[w].e;
+      if (j >= e.hcount || (of_blocks ? !s_all[w] : s_wide[w].in_block == 0)) continue;
+      const SegmentBlocks s = p.mode == kSchedBalanced ? blocks_of(e) : SegmentBlocks{0, 1, false};
+      float M = kEmptyM, den = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if constexpr (of_blocks) {
 #pragma unroll 1
-    for (int level = in_block ? 0 : 1; level < 2; ++level) {
-#pragma unroll 1
-      for (int it = threadIdx.x; it < e.hcount * (D / 4); it += NW * 32) {
-        const int j = it / (D / 4), d = it % (D / 4) * 4;
-        float M = kEmptyM, den = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (level == 0) {
-#pragma unroll 1
-          for (int i = z; i < NW; i += e.zg) {
-            if (units_within(e.off, e.C, e.n, s_start[i].x0, s_start[i].x1) == 0) continue;
-            const int side = e.off > s_start[i].x0;
-            add_state(M, den, acc, s_plse[i][side][j], *reinterpret_cast<const float4*>(state_of(i, side) + j * D + d));
-          }
-        } else {
-#pragma unroll 1
-          for (int i0 = 0; i0 < s.n; i0 += 8) {  // eight states' lse and rows in flight together
-            float l[8];
-            float4 o[8];
+        for (int i0 = 0; i0 < s.n; i0 += 8) {  // eight states' lse and rows in flight together
+          float l[8];
+          float4 o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const long long at = slot_of(e, s, min(i0 + i, s.n - 1)) + j;
-              l[i] = __ldcg(p.part_lse + at);
-              o[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i0 + i < s.n && holds_units(e, s, i0 + i)) add_state(M, den, acc, l[i], o[i]);
+          for (int i = 0; i < 8; ++i) {
+            const long long at = slot_of(e, s, min(i0 + i, s.n - 1)) + j;
+            l[i] = __ldcg(p.part_lse + at);
+            o[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i0 + i < s.n && holds_units(e, s, i0 + i)) add_state(M, den, acc, l[i], o[i]);
         }
-        const bool empty = den == 0.f;
-        float inv = empty ? 0.f : 1.f / den;
-        float l = empty ? kEmptyM : M + log2f(den);
-        if (final || level == 1) {
-          if (p.sink) {
-            const SinkAdj sa = apply_sink(p, col_head<MQ>(p, e.hk, e.c0 + j), l);
-            inv *= sa.scale;
-            l = sa.lse;
-          }
-          const size_t row = col_row<MQ>(p, e.b, e.hk, e.c0 + j);
-          store_four(p, row * D + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-          if (d == 0) p.lse[row] = l;
-        } else {
-          const long long at = slot_of(e, s, (int)(blockIdx.x - s.first)) + j;
-          *reinterpret_cast<float4*>(p.part_o + at * D + d) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-          if (d == 0) p.part_lse[at] = l;
+      } else {
+#pragma unroll 1
+        for (int i = e.zg > 1 ? e.hz % e.zg : 0; i < NW; i += e.zg) {
+          if (units_within(e.off, e.C, e.n, s_start[i].x0, s_start[i].x1) == 0) continue;
+          const int side = e.off > s_start[i].x0;
+          add_state(M, den, acc, s_plse[i][side][j], *reinterpret_cast<const float4*>(state_of(i, side) + j * D + d));
         }
       }
-      if (level == 1 || final) break;
-      fence_acq_rel_gpu();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        int* cnt = p.counters + (size_t)e.b * p.H_kv * p.n_z + e.hz;
-        s_all = atomicAdd(cnt, in_block) + in_block == e.n;
-        if (s_all) *cnt = 0;  // every other block's units have arrived: reset for reuse
+      const bool empty = den == 0.f;
+      float inv = empty ? 0.f : 1.f / den;
+      float l = empty ? kEmptyM : M + log2f(den);
+      if (of_blocks || s_wide[w].in_block == e.n) {
+        if (p.sink) {
+          const SinkAdj sa = apply_sink(p, col_head<MQ>(p, e.hk, e.c0 + j), l);
+          inv *= sa.scale;
+          l = sa.lse;
+        }
+        const size_t row = col_row<MQ>(p, e.b, e.hk, e.c0 + j);
+        store_four(p, row * D + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        if (d == 0) p.lse[row] = l;
+      } else {
+        const long long at = slot_of(e, s, (int)(blockIdx.x - s.first)) + j;
+        *reinterpret_cast<float4*>(p.part_o + at * D + d) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (d == 0) p.part_lse[at] = l;
       }
-      __syncthreads();
-      if (!s_all) break;
-      fence_acq_rel_gpu();
     }
-    __syncthreads();  // (s_all is written again)
+  };
+  merge(std::false_type{});
+  if (p.mode != kSchedBalanced) return;
+  fence_acq_rel_gpu();
+  __syncthreads();
+  if (threadIdx.x < n) {
+    const PartMerge& e = s_wide[threadIdx.x].e;
+    const int in_block = s_wide[threadIdx.x].in_block;
+    bool all = in_block == 0;
+    if (in_block && in_block < e.n) {
+      int* cnt = p.counters + (size_t)e.b * p.H_kv * p.n_z + e.hz;
+      all = atomicAdd(cnt, in_block) + in_block == e.n;
+      if (all) *cnt = 0;  // every other block's units have arrived: reset for reuse
+    }
+    s_all[threadIdx.x] = all;
   }
+  __syncthreads();
+  fence_acq_rel_gpu();
+  merge(std::true_type{});
 }
 
 // ----------------------------------------------------------------------------- states in shared memory
