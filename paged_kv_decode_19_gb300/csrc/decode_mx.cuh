@@ -710,16 +710,13 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   bool mine = true;  // whether this warp writes the output
   if (ua != 0 || ub != sg.n) {
     const PartMerge e{sg.off, ws.U, sg.b, sg.hz, sg.n, hk, c0, hcount, C, zg};
-    // its units in the block, how many warps hold some, and which is the first
-    int in_block = 0, states = 0, lw = 0;
-#pragma unroll 1
-    for (int i = NW - zg + warp % zg; i >= 0; i -= zg) {
-      const int n = units_within(sg.off, C, sg.n, s_start[i].x0, s_start[i].x1);
-      in_block += n;
-      states += n > 0;
-      lw = n > 0 ? i : lw;
-    }
-    const int ls = sg.off > s_start[lw].x0;
+    // its units in the block, and the warps that hold some (lane i looks at warp i)
+    const int wi = lane < NW && lane % zg == warp % zg ? lane : -1;
+    const long long w0 = wi >= 0 ? s_start[wi].x0 : 0, w1 = wi >= 0 ? s_start[wi].x1 : 0;
+    const int units = wi >= 0 ? units_within(sg.off, C, sg.n, w0, w1) : 0;
+    const int in_block = __reduce_add_sync(0xffffffffu, units);
+    const unsigned from = __ballot_sync(0xffffffffu, units > 0), late = __ballot_sync(0xffffffffu, units > 0 && sg.off > w0);
+    const int states = __popc(from), lw = __ffs(from) - 1, ls = (late >> lw) & 1;
     const bool wide = states > kWarpStates;
     SegmentBlocks sb{};
     // first the block's warps (from shared memory), then the blocks (from their slots)
@@ -740,7 +737,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
         }
         __threadfence_block();
         if (last && wide) {
-          if (lane == 0) s_wide[atomicAdd(&s_n_wide, 1)] = WideMerge{e, in_block};
+          if (lane == 0) s_wide[atomicAdd(&s_n_wide, 1)] = WideMerge{e, in_block == sg.n ? SegmentBlocks{} : blocks_of(e), in_block, from, late};
           last = 0;
         }
       } else {
@@ -748,17 +745,17 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
         sb = blocks_of(e);
         const long long at = slot_of(e, sb, (int)(blockIdx.x - sb.first));
         put_state(p.part_o + at * D, p.part_lse + at);
-        fence_acq_rel_gpu();
         __syncwarp();
         if (lane == 0) {
+          fence_acq_rel_gpu();  // (after the whole warp's stores)
           int* cnt = p.counters + (size_t)sg.b * p.H_kv * p.n_z + sg.hz;
           last = atomicAdd(cnt, in_block) + in_block == sg.n;
           if (last) *cnt = 0;  // every other block's units have arrived: reset for reuse
+          fence_acq_rel_gpu();
         }
         last = __shfl_sync(0xffffffffu, last, 0);
-        fence_acq_rel_gpu();
         if (last && sb.n > kWarpMerge) {
-          if (lane == 0) s_wide[atomicAdd(&s_n_wide, 1)] = WideMerge{e, 0};
+          if (lane == 0) s_wide[atomicAdd(&s_n_wide, 1)] = WideMerge{e, sb, 0, 0u, 0u};
           last = 0;
         }
       }
@@ -772,8 +769,8 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
         const float* o;
         const float* l;
         if (level == 0) {
-          if (i == warp || units_within(sg.off, C, sg.n, s_start[i].x0, s_start[i].x1) == 0) continue;
-          const int side = sg.off > s_start[i].x0;
+          if (i == warp || !((from >> i) & 1)) continue;
+          const int side = (late >> i) & 1;
           o = state_of(i, side);
           l = s_plse[i][side];
         } else {
@@ -831,7 +828,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   }  // segments
   if (!waited) pdl_wait();  // (a worker without units: what the block merges may still follow it)
   if (lane == 0) *(volatile int*)&s_done[warp] = INT_MAX / 2;
-  merge_wide<D, MQ, NW>(p, s_wide, s_n_wide, s_start, s_plse, state_of);
+  merge_wide<D, MQ, NW>(p, s_wide, s_n_wide, s_plse, state_of);
 }
 
 // ----------------------------------------------------------------------------- launch

@@ -202,104 +202,143 @@ __device__ __forceinline__ bool holds_units(const PartMerge& e, const SegmentBlo
   return e.U >= G || div_floor((s.first + i) * e.U, G) < div_floor((s.first + i + 1) * e.U, G);
 }
 
-// One more state (o, l) into unnormalised sums of four dims against a running maximum.
-__device__ __forceinline__ void add_state(float& M, float& den, float4& acc, float l, float4 o) {
-  if (l <= kEmptyM) return;  // (NaN counts)
-  const float m = fmaxf(M, l), f = fast_exp2(M - m), x = fast_exp2(l - m);
-  M = m;
-  den = fmaf(den, f, x);
-  acc = make_float4(fmaf(acc.x, f, o.x * x), fmaf(acc.y, f, o.y * x), fmaf(acc.z, f, o.z * x), fmaf(acc.w, f, o.w * x));
-}
-
 // Segments for the whole block to merge at its end: of more than kWarpStates of its warps (their states
 // in shared memory: state_of(warp, side), s_plse), or of more than kWarpMerge blocks (published).
 struct WideMerge {
   PartMerge e;
-  int in_block;  // units in the block to merge and publish; 0: the blocks' states are all there
+  SegmentBlocks blocks;
+  int in_block;         // units in the block to merge and publish; 0: the blocks' states are all there
+  unsigned from, late;  // the warps that hold states of it, and those whose state is that of their last segment
 };
 #ifndef WS
 #define WS 4
 #endif
 constexpr int kWarpStates = WS;
+template <int NW>
+struct WideScratch {
+  float weight[NW + 2][NW][kMaxGroupPerCta];  // of a segment's states, by column
+  float lse[NW + 2][kMaxGroupPerCta];
+  bool all[NW + 2];  // the segment is complete, and its blocks' states are to be merged
+};
 template <int D, bool MQ, int NW, typename StateOf>
 __device__ __forceinline__ void merge_wide(const DecodeParams& p, const WideMerge (&s_wide)[NW + 2], const int& s_n,
-                                           const WorkerStart (&s_start)[NW],
                                            const float (&s_plse)[NW][2][kMaxGroupPerCta], StateOf state_of) {
-  constexpr int NT = NW * 32, kItems = kMaxGroupPerCta * (D / 4);  // of a segment: a column and four dims each
-  __shared__ bool s_all[NW + 2];  // the segment is complete, and its blocks' states are to be merged
+  constexpr int NT = NW * 32, G8 = kMaxGroupPerCta, kItems = G8 * (D / 4);  // of a segment: a column and four dims each
+  __shared__ WideScratch<NW> s;
+  const int tid = threadIdx.x;
   __syncthreads();
   const int n = s_n;
   if (n == 0) return;
-  // all segments at each step: the block's own states; the count of their units; the blocks' states
-  auto merge = [&](auto of_blocks) {
-#pragma unroll 1
-    for (int x = threadIdx.x; x < n * kItems; x += NT) {
-      const int w = x / kItems, j = x % kItems / (D / 4), d = x % (D / 4) * 4;
-      const PartMerge& e = s_wide[w].e;
-      if (j >= e.hcount || (of_blocks ? !s_all[w] : s_wide[w].in_block == 0)) continue;
-      const SegmentBlocks s = p.mode == kSchedBalanced ? blocks_of(e) : SegmentBlocks{0, 1, false};
-      float M = kEmptyM, den = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      if constexpr (of_blocks) {
-#pragma unroll 1
-        for (int i0 = 0; i0 < s.n; i0 += 8) {  // eight states' lse and rows in flight together
-          float l[8];
-          float4 o[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const long long at = slot_of(e, s, min(i0 + i, s.n - 1)) + j;
-            l[i] = __ldcg(p.part_lse + at);
-            o[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i0 + i < s.n && holds_units(e, s, i0 + i)) add_state(M, den, acc, l[i], o[i]);
-        }
-      } else {
-#pragma unroll 1
-        for (int i = e.zg > 1 ? e.hz % e.zg : 0; i < NW; i += e.zg) {
-          if (units_within(e.off, e.C, e.n, s_start[i].x0, s_start[i].x1) == 0) continue;
-          const int side = e.off > s_start[i].x0;
-          add_state(M, den, acc, s_plse[i][side][j], *reinterpret_cast<const float4*>(state_of(i, side) + j * D + d));
-        }
+  auto put = [&](int w, int j, int d, float4 o, float l, bool final) {
+    const PartMerge& e = s_wide[w].e;
+    if (final) {
+      if (p.sink) {
+        const SinkAdj sa = apply_sink(p, col_head<MQ>(p, e.hk, e.c0 + j), l);
+        o = make_float4(o.x * sa.scale, o.y * sa.scale, o.z * sa.scale, o.w * sa.scale);
+        l = sa.lse;
       }
-      const bool empty = den == 0.f;
-      float inv = empty ? 0.f : 1.f / den;
-      float l = empty ? kEmptyM : M + log2f(den);
-      if (of_blocks || s_wide[w].in_block == e.n) {
-        if (p.sink) {
-          const SinkAdj sa = apply_sink(p, col_head<MQ>(p, e.hk, e.c0 + j), l);
-          inv *= sa.scale;
-          l = sa.lse;
-        }
-        const size_t row = col_row<MQ>(p, e.b, e.hk, e.c0 + j);
-        store_four(p, row * D + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-        if (d == 0) p.lse[row] = l;
-      } else {
-        const long long at = slot_of(e, s, (int)(blockIdx.x - s.first)) + j;
-        *reinterpret_cast<float4*>(p.part_o + at * D + d) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (d == 0) p.part_lse[at] = l;
-      }
+      const size_t row = col_row<MQ>(p, e.b, e.hk, e.c0 + j);
+      store_four(p, row * D + d, o);
+      if (d == 0) p.lse[row] = l;
+    } else {
+      const SegmentBlocks& sb = s_wide[w].blocks;
+      const long long at = slot_of(e, sb, (int)(blockIdx.x - sb.first)) + j;
+      *reinterpret_cast<float4*>(p.part_o + at * D + d) = o;
+      if (d == 0) p.part_lse[at] = l;
     }
   };
-  merge(std::false_type{});
-  if (p.mode != kSchedBalanced) return;
-  fence_acq_rel_gpu();
+  // the block's own states: their weights, then the sums
+  for (int x = tid; x < n * G8; x += NT) {
+    const int w = x / G8, j = x % G8;
+    float l[NW], M = kEmptyM, den = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      l[i] = (s_wide[w].from >> i) & 1 ? s_plse[i][(s_wide[w].late >> i) & 1][j] : kEmptyM;
+      M = fmaxf(M, l[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      l[i] = l[i] <= kEmptyM ? 0.f : fast_exp2(l[i] - M);  // (NaN counts)
+      den += l[i];
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) s.weight[w][i][j] = l[i] * inv;
+    s.lse[w][j] = den == 0.f ? kEmptyM : M + log2f(den);
+  }
   __syncthreads();
-  if (threadIdx.x < n) {
-    const PartMerge& e = s_wide[threadIdx.x].e;
-    const int in_block = s_wide[threadIdx.x].in_block;
+  for (int x = tid; x < n * kItems; x += NT) {
+    const int w = x / kItems, j = x % kItems / (D / 4), d = x % (D / 4) * 4;
+    if (j >= s_wide[w].e.hcount || s_wide[w].in_block == 0) continue;
+    const unsigned from = s_wide[w].from, late = s_wide[w].late;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < NW; ++i) {
+      if (!((from >> i) & 1)) continue;
+      const float x_ = s.weight[w][i][j];
+      const float4 o = *reinterpret_cast<const float4*>(state_of(i, (late >> i) & 1) + j * D + d);
+      acc = make_float4(fmaf(x_, o.x, acc.x), fmaf(x_, o.y, acc.y), fmaf(x_, o.z, acc.z), fmaf(x_, o.w, acc.w));
+    }
+    put(w, j, d, acc, s.lse[w][j], s_wide[w].in_block == s_wide[w].e.n);
+  }
+  if (p.mode != kSchedBalanced) return;
+  __syncthreads();
+  // the counts of the segments' units (the fence follows the whole block's stores)
+  if (tid < n) {
+    const PartMerge& e = s_wide[tid].e;
+    const int in_block = s_wide[tid].in_block;
     bool all = in_block == 0;
     if (in_block && in_block < e.n) {
+      fence_acq_rel_gpu();
       int* cnt = p.counters + (size_t)e.b * p.H_kv * p.n_z + e.hz;
       all = atomicAdd(cnt, in_block) + in_block == e.n;
       if (all) *cnt = 0;  // every other block's units have arrived: reset for reuse
+      fence_acq_rel_gpu();
     }
-    s_all[threadIdx.x] = all;
+    s.all[tid] = all;
   }
   __syncthreads();
-  fence_acq_rel_gpu();
-  merge(std::true_type{});
+  // the blocks' states
+#pragma unroll 1
+  for (int x = tid; x < n * kItems; x += NT) {
+    const int w = x / kItems, j = x % kItems / (D / 4), d = x % (D / 4) * 4;
+    const PartMerge& e = s_wide[w].e;
+    if (j >= e.hcount || !s.all[w]) continue;
+    const SegmentBlocks sb = s_wide[w].blocks;
+    float M = kEmptyM, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int i0 = 0; i0 < sb.n; i0 += 8) {  // eight states' lse and rows in flight together
+      float l[8];
+      float4 o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const long long at = slot_of(e, sb, min(i0 + i, sb.n - 1)) + j;
+        l[i] = __ldcg(p.part_lse + at);
+        o[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
+      }
+      float m = M;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i0 + i >= sb.n || !holds_units(e, sb, i0 + i)) l[i] = kEmptyM;
+        m = fmaxf(m, l[i]);
+      }
+      const float f = fast_exp2(M - m);
+      M = m;
+      den *= f;
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (l[i] <= kEmptyM) continue;  // (NaN counts)
+        const float x_ = fast_exp2(l[i] - M);
+        den += x_;
+        acc = make_float4(fmaf(x_, o[i].x, acc.x), fmaf(x_, o[i].y, acc.y), fmaf(x_, o[i].z, acc.z), fmaf(x_, o[i].w, acc.w));
+      }
+    }
+    const bool empty = den == 0.f;
+    const float inv = empty ? 0.f : 1.f / den;
+    put(w, j, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), empty ? kEmptyM : M + log2f(den), true);
+  }
 }
 
 // ----------------------------------------------------------------------------- states in shared memory
