@@ -138,9 +138,8 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   constexpr int KW = KB / 4;  // words
   extern __shared__ uint8_t s_raw[];
   __shared__ float s_plse[NW][2][kMaxGroupPerCta]; // lse of each warp's partial states: first, last segment
-  __shared__ int s_cnt[NW][2];                     // units that have arrived, by a segment's first such state
-  __shared__ WideMerge s_wide[NW + 2];
-  __shared__ int s_n_wide, s_done[NW];             // s_done: stages each warp has computed
+  __shared__ SegmentMerge s_merge[NW + 4];
+  __shared__ int s_n_merge, s_done[NW];             // s_done: stages each warp has computed
   __shared__ WorkerStart s_start[NW];
   // of each tile of two batches of 32 (ROWS: of a stage): which rows count (bit r: row r), and the
   // attended index of row 0; of rows with two scale bytes that were copied one by one, which half of
@@ -174,9 +173,8 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     waited = true;
   }
   line_starts<NT, NW>(p, s_start, reinterpret_cast<long long*>(rings));
-  if (lane < 2) s_cnt[warp][lane] = 0;
   if (lane == 0) s_done[warp] = 0;
-  if (threadIdx.x == 0) s_n_wide = 0;
+  if (threadIdx.x == 0) s_n_merge = 0;
   __syncthreads();  // no block-wide barrier until every warp has finished its range
 
   const int g_id = lane >> 2, q4 = lane & 3;
@@ -694,8 +692,12 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
 #pragma unroll
     for (int mt = 0; mt < KT; ++mt) oacc[mt][h] *= inv, oacc[mt][h + 2] *= inv;
   }
-  // the state to memory, and another one's from it: lse_M = M + log2 (2^(lse - M) + 2^(l - M))
-  auto put_state = [&](float* o, float* l) {
+  const bool mine = ua == 0 && ub == sg.n;  // the whole segment: this warp writes the output
+  if (!mine) {
+    // its state to shared memory; the first of the block's warps that share the segment notes it for the
+    // block to merge (lane i looks at warp i's range)
+    const int side = sg.off > ws.x0;
+    float* const o = state_of(warp, side);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int j = 2 * q4 + h;
@@ -704,103 +706,17 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       for (int x = 0; x < RL / 4; ++x)
         reinterpret_cast<float4*>(o + j * D + RL * g_id)[x] =
             make_float4(oacc[2 * x][h], oacc[2 * x][h + 2], oacc[2 * x + 1][h], oacc[2 * x + 1][h + 2]);
-      if (g_id == 0) l[j] = lse[h];
+      if (g_id == 0) s_plse[warp][side][j] = lse[h];
     }
-  };
-  bool mine = true;  // whether this warp writes the output
-  if (ua != 0 || ub != sg.n) {
-    const PartMerge e{sg.off, ws.U, sg.b, sg.hz, sg.n, hk, c0, hcount, C, zg};
-    // its units in the block, and the warps that hold some (lane i looks at warp i)
     const int wi = lane < NW && lane % zg == warp % zg ? lane : -1;
     const long long w0 = wi >= 0 ? s_start[wi].x0 : 0, w1 = wi >= 0 ? s_start[wi].x1 : 0;
     const int units = wi >= 0 ? units_within(sg.off, C, sg.n, w0, w1) : 0;
     const int in_block = __reduce_add_sync(0xffffffffu, units);
     const unsigned from = __ballot_sync(0xffffffffu, units > 0), late = __ballot_sync(0xffffffffu, units > 0 && sg.off > w0);
-    const int states = __popc(from), lw = __ffs(from) - 1, ls = (late >> lw) & 1;
-    const bool wide = states > kWarpStates;
-    SegmentBlocks sb{};
-    // first the block's warps (from shared memory), then the blocks (from their slots)
-#pragma unroll 1
-    for (int level = in_block == ub - ua ? 1 : 0; level < 2; ++level) {
-      int last = 0;
-      if (level == 0) {
-        const int side = sg.off > ws.x0;
-        // (if all others are there already the state need not go to memory)
-        if (lane == 0) last = !wide && *(volatile int*)&s_cnt[lw][ls] + (ub - ua) == in_block;
-        last = __shfl_sync(0xffffffffu, last, 0);
-        if (!last) {
-          put_state(state_of(warp, side), s_plse[warp][side]);
-          __threadfence_block();
-          __syncwarp();
-          if (lane == 0) last = atomicAdd(&s_cnt[lw][ls], ub - ua) + (ub - ua) == in_block;
-          last = __shfl_sync(0xffffffffu, last, 0);
-        }
-        __threadfence_block();
-        if (last && wide) {
-          if (lane == 0) s_wide[atomicAdd(&s_n_wide, 1)] = WideMerge{e, in_block == sg.n ? SegmentBlocks{} : blocks_of(e), in_block, from, late};
-          last = 0;
-        }
-      } else {
-        if (in_block == sg.n) break;
-        sb = blocks_of(e);
-        const long long at = slot_of(e, sb, (int)(blockIdx.x - sb.first));
-        put_state(p.part_o + at * D, p.part_lse + at);
-        __syncwarp();
-        if (lane == 0) {
-          fence_acq_rel_gpu();  // (after the whole warp's stores)
-          int* cnt = p.counters + (size_t)sg.b * p.H_kv * p.n_z + sg.hz;
-          last = atomicAdd(cnt, in_block) + in_block == sg.n;
-          if (last) *cnt = 0;  // every other block's units have arrived: reset for reuse
-          fence_acq_rel_gpu();
-        }
-        last = __shfl_sync(0xffffffffu, last, 0);
-        if (last && sb.n > kWarpMerge) {
-          if (lane == 0) s_wide[atomicAdd(&s_n_wide, 1)] = WideMerge{e, sb, 0, 0u, 0u};
-          last = 0;
-        }
-      }
-      if (!last) {
-        mine = false;
-        break;
-      }
-      const int count = level ? sb.n : NW;
-#pragma unroll 1
-      for (int i = level ? 0 : lw; i < count; i += level ? 1 : zg) {
-        const float* o;
-        const float* l;
-        if (level == 0) {
-          if (i == warp || !((from >> i) & 1)) continue;
-          const int side = (late >> i) & 1;
-          o = state_of(i, side);
-          l = s_plse[i][side];
-        } else {
-          if (sb.first + i == blockIdx.x || !holds_units(e, sb, i)) continue;
-          const long long at = slot_of(e, sb, i);
-          o = p.part_o + at * D;
-          l = p.part_lse + at;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int j = min(2 * q4 + h, hcount - 1);
-          const float other = l[j];
-          float4 v[RL / 4];
-#pragma unroll
-          for (int x = 0; x < RL / 4; ++x) v[x] = reinterpret_cast<const float4*>(o + j * D + RL * g_id)[x];
-          const float M = fmaxf(lse[h], other);
-          // (NaN counts; two empty states stay one)
-          const float a = lse[h] <= kEmptyM ? 0.f : fast_exp2(lse[h] - M), b = other <= kEmptyM ? 0.f : fast_exp2(other - M);
-          const float den = a + b;
-          const float wa = den == 0.f ? 0.f : a / den, wb = den == 0.f ? 0.f : b / den;
-          lse[h] = den == 0.f ? kEmptyM : M + log2f(den);
-#pragma unroll
-          for (int x = 0; x < RL / 4; ++x) {
-            oacc[2 * x][h] = fmaf(oacc[2 * x][h], wa, v[x].x * wb);
-            oacc[2 * x][h + 2] = fmaf(oacc[2 * x][h + 2], wa, v[x].y * wb);
-            oacc[2 * x + 1][h] = fmaf(oacc[2 * x + 1][h], wa, v[x].z * wb);
-            oacc[2 * x + 1][h + 2] = fmaf(oacc[2 * x + 1][h + 2], wa, v[x].w * wb);
-          }
-        }
-      }
+    if (lane == 0 && warp == __ffs(from) - 1) {
+      const PartMerge e{sg.off, ws.U, sg.b, sg.hz, sg.n, hk, c0, hcount, C, zg};
+      s_merge[atomicAdd(&s_n_merge, 1)] =
+          SegmentMerge{e, in_block == sg.n ? SegmentBlocks{} : blocks_of(e), in_block, from, late};
     }
   }
   if (mine) {
@@ -828,7 +744,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   }  // segments
   if (!waited) pdl_wait();  // (a worker without units: what the block merges may still follow it)
   if (lane == 0) *(volatile int*)&s_done[warp] = INT_MAX / 2;
-  merge_wide<D, MQ, NW>(p, s_wide, s_n_wide, s_plse, state_of);
+  merge_states<D, MQ, NW>(p, s_merge, s_n_merge, s_plse, state_of);
 }
 
 // ----------------------------------------------------------------------------- launch
