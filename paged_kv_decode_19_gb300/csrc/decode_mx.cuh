@@ -62,15 +62,15 @@ __device__ __forceinline__ int mx_chunk(int r, int c) {
   return r * (D / 2) + ((D == 64 ? c : D == 128 ? c ^ ((r >> 1) & 3) : c ^ (r & 7)) << 4);
 }
 
-// A scale's f16 pair from two bytes in the low half of w.
+// Two scales as f16.
 template <int SB>
-__device__ __forceinline__ uint32_t mx_scales(uint32_t w) {
-  if constexpr (SB == 16) return e4m3x2_to_f16x2((uint16_t)w);
-  // 2^(b - 127) as f16: exponent b - 112 for 2^-14 to 2^15; 0 below, NaN above 2^13 (where a code
-  // times it would overflow)
-  const int a = (int)(w & 255u) - 112, b = (int)((w >> 8) & 255u) - 112;
-  const uint32_t x = a > 28 ? 0x7e00u : (uint32_t)max(a, 0) << 10, y = b > 28 ? 0x7e00u : (uint32_t)max(b, 0) << 10;
-  return x | (y << 16);
+__device__ __forceinline__ uint32_t mx_scales(uint32_t a, uint32_t b) {
+  if constexpr (SB == 16) return e4m3x2_to_f16x2((uint16_t)(a | (b << 8)));
+  // 2^(x - 127): exponent x - 112 for 2^-14 to 2^13, 0 below; above, where a code times it would
+  // overflow, NaN (141 has 29 in the exponent: 0x7400 + 0xbff).  On both halves at once.
+  const uint32_t x = __vminu2(__vmaxu2(a | (b << 16), 0x00700070u), 0x008d008du);
+  constexpr uint32_t c = (112u * 1024u + 140u * 0xbffu) * 0x10001u;
+  return x * 1024u + __vmaxu2(x, 0x008c008cu) * 0xbffu - c;
 }
 
 // eight codes (four bytes) -> f16x2 of each byte, exact
@@ -491,10 +491,15 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
         // their scales: of row kr (low halves) and kr + 8 (high halves); of two blocks, a pair each
         uint32_t fa, fb;
         if constexpr (BPC == 2) {
-          fa = mx_scales<SB>(*reinterpret_cast<const uint16_t*>(sa + blk));
-          fb = mx_scales<SB>(*reinterpret_cast<const uint16_t*>(sb + blk));
+          if constexpr (SB == 16) {  // (both bytes at once)
+            fa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sa + blk));
+            fb = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sb + blk));
+          } else {
+            fa = mx_scales<SB>(sa[blk], sa[blk + 1]);
+            fb = mx_scales<SB>(sb[blk], sb[blk + 1]);
+          }
         } else {
-          fa = fb = mx_scales<SB>(sa[blk] | ((uint32_t)sb[blk] << 8));
+          fa = fb = mx_scales<SB>(sa[blk], sb[blk]);
         }
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
@@ -635,8 +640,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int blk = RL * g_id / SB + b;
-          sv[j][b] = mx_scales<SB>(scales_at(i, vr[0] + 8 * j, true)[blk] |
-                                   ((uint32_t)scales_at(i, vr[1] + 8 * j, true)[blk] << 8));
+          sv[j][b] = mx_scales<SB>(scales_at(i, vr[0] + 8 * j, true)[blk], scales_at(i, vr[1] + 8 * j, true)[blk]);
         }
 #pragma unroll
       for (int w = 0; w < VB / 4; ++w) {
