@@ -55,11 +55,12 @@ __device__ __forceinline__ void load16(const IT* src, float (&x)[16]) {
   }
 }
 
-// y / s, correctly rounded, for the s of a scale (at most four significant bits, r = 1 / s rounded):
-// Markstein's correction of a product by the remainder, which the fma gives exactly.
+// y / s, correctly rounded, for an s of at most four significant bits and r = 1 / s rounded: Markstein's
+// correction of a product by the remainder, which the fma gives exactly.  (The remainder is taken
+// negative, so that a zero keeps its sign.)
 __device__ __forceinline__ float quotient(float y, float s, float r) {
   const float q = y * r;
-  return copysignf(fmaf(fmaf(-q, s, y), r, q), y);  // (a zero keeps its sign)
+  return fmaf(fmaf(q, s, -y), -r, q);
 }
 // The larger of two magnitudes, NaN if either is.
 __device__ __forceinline__ float max_abs(float m, float x) {
@@ -95,7 +96,8 @@ struct Divisor {
 
 template <typename IT, int SB, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    append_mx_kernel(const __grid_constant__ AppendMxParams a, const __grid_constant__ Divisor per_row, int log_d) {
+    append_mx_kernel(const __grid_constant__ AppendMxParams a, const __grid_constant__ Divisor per_row,
+                     const __grid_constant__ Divisor per_page, int log_d) {
   pdl_wait();  // inputs and pages are the previous kernel's to write until it completes
   pdl_release();
   // an item is 16 dims of a token's K or V: item = (token, K | V, head, 16 dims); SB 32: a block's two
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kThreads)
   float s, r;
   uint8_t sb;
   if constexpr (SB == 16) {
-    const uint8_t c = f32_to_e4m3(__fdiv_rn(m, 6.f));
+    const uint8_t c = f32_to_e4m3(quotient(m, 6.f, 1.f / 6.f));
     sb = finite ? max(c, (uint8_t)1) : (uint8_t)0x7f;  // (code 1: 2^-9)
     F8 f;
     f.v = sb;
@@ -146,15 +148,16 @@ __global__ void __launch_bounds__(kThreads)
     return;
   }
   const unsigned h = 16 * j >> log_d, d = 16 * j - (h << log_d);
-  const long long page = slot >> 32 ? slot / a.P : (unsigned)slot / (unsigned)a.P;
-  const long long at = ((page * 2 + kv) * a.H_kv + h) * a.P + (slot - page * a.P);  // the row in the cache
+  const unsigned page = slot >> 31 ? (unsigned)(slot / a.P) : per_page.quot((unsigned)slot);
+  // the row in the cache (2 max_pages H_kv is below 2^31)
+  const long long at = (long long)((page * 2 + kv) * a.H_kv + h) * a.P + (int)(slot - (long long)page * a.P);
   *reinterpret_cast<uint2*>(a.pages + (at << (log_d - 1)) + d / 2) = codes;
   if (SB == 16 || (d & 16) == 0) a.scales[((at << log_d) + d) / SB] = sb;
 }
 
 template <typename IT, int SB>
 static cudaError_t launch_t(const AppendMxParams& all, int D, bool vec, cudaStream_t st) {
-  const Divisor per_row((unsigned)(all.H_kv * (D / 16)));
+  const Divisor per_row((unsigned)(all.H_kv * (D / 16))), per_page((unsigned)all.P);
   const int log_d = D == 64 ? 6 : D == 128 ? 7 : 8;
   // as many tokens a launch as keep the items below 2^31
   const int most = (int)std::max(1ll, (1ll << 30) / (2ll * per_row.d));
@@ -165,8 +168,8 @@ static cudaError_t launch_t(const AppendMxParams& all, int D, bool vec, cudaStre
     a.k_new = reinterpret_cast<const IT*>(a.k_new) + t0 * a.k_stride;
     a.v_new = reinterpret_cast<const IT*>(a.v_new) + t0 * a.v_stride;
     const dim3 grid((unsigned)((2ll * a.T * per_row.d + kThreads - 1) / kThreads));
-    const cudaError_t e = vec ? launch_pdl(append_mx_kernel<IT, SB, true>, grid, dim3(kThreads), 0, st, a, per_row, log_d)
-                              : launch_pdl(append_mx_kernel<IT, SB, false>, grid, dim3(kThreads), 0, st, a, per_row, log_d);
+    const cudaError_t e = vec ? launch_pdl(append_mx_kernel<IT, SB, true>, grid, dim3(kThreads), 0, st, a, per_row, per_page, log_d)
+                              : launch_pdl(append_mx_kernel<IT, SB, false>, grid, dim3(kThreads), 0, st, a, per_row, per_page, log_d);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
