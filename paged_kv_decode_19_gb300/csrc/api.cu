@@ -33,11 +33,10 @@ constexpr int kSegCostTiles = PD_SEG_COST_TILES;
 #define PD_BS_SEG_COST_TILES 8
 #endif
 constexpr int kBsSegCostTiles = PD_BS_SEG_COST_TILES;
-// And of the 4-bit one.
-#ifndef PD_MX_SEG_COST_TILES
-#define PD_MX_SEG_COST_TILES 8
-#endif
-constexpr int kMxSegCostTiles = PD_MX_SEG_COST_TILES;
+// And of the 4-bit one, in tiles times head dim: 8 tiles at D 128, 16 at D 64.  Measured (us; 256 and 32
+// sequences at D 128, 24 with four queries at D 64): half of it 117.0, 23.4 and 20.9, as it is 116.7,
+// 22.3 and 19.2, twice 120.3, 23.4 and 20.7.
+constexpr int kMxSegCostDims = 1024;
 constexpr size_t kWsAlign = 256;
 
 static thread_local std::string t_last_error;
@@ -706,7 +705,7 @@ static pd_status decode_call(const void* Q, const void* pages, const int32_t* pa
   p.rotary = rotary_mode;
   p.mode = mode;
   // tensor-core schedule: a segment's set-up and finish cost about kSegCostTiles tiles
-  const int seg_tiles = mx ? kMxSegCostTiles : bs ? kBsSegCostTiles : kSegCostTiles;
+  const int seg_tiles = mx ? kMxSegCostDims / d.D : bs ? kBsSegCostTiles : kSegCostTiles;
   p.seg_cost = use_mma && mode == kSchedBalanced && seg_tiles > 0
                    ? std::max(1, seg_tiles * 16 / d.page_size) : 0;
   p.out_dtype = d.out_dtype;

@@ -3,8 +3,38 @@
 //
 //   K_rd = c_rd ks_r,d/SB k_scale,  s_r = sm_scale log2(e) q.K_r,  out = sum_r 2^(s_r) V_r / sum_r 2^(s_r)
 //
-// The work split, the schedule and the merge are those of the other tensor-core decodes
-// (decode_common.cuh, decode_parts.cuh): every warp is an independent worker on its share of the pages.
+// The work split and the schedule are those of the other tensor-core decodes (decode_common.cuh): every
+// warp is an independent worker on its share of the pages; shares of a segment are merged by its block
+// (decode_parts.cuh).
+//
+// What bounds it: the codes and scales are 9/16 of a byte per dim (17/32 with power-of-two scales), so
+// the copy rate leaves an SM about 98 cycles for a 16-row tile of D 128, K and V; the tile takes about
+// 250 instructions, of which 64 turn codes to f16 and 64 multiply the scales in (each on a pipe of half
+// rate), 16 bring the codes of two rows of V side by side, 23 copy, 16 are products.  The loop issues 2.4
+// instructions a cycle (the schedulers' four warps-slots wait for fixed latencies and those two pipes), so
+// it takes 105 cycles; what is measured above that is the start (3 us from the first instruction to the
+// first tile), the merge and the launch.  The steps that carried it (256 sequences of 300 to 4200 rows /
+// eight contexts of 32K to 128K rows, us): tiles by bulk copies of a lane 163 / 181; by 16-byte
+// asynchronous copies of all lanes (a bulk copy takes uniform registers, so lanes took turns) 136 / 141;
+// masks and rare paths out of the loop 128 / 137; one block of twelve warps an SM, in which the older
+// warps of a scheduler do not run ahead of the younger (three blocks of four: 128 / 137; sixteen warps of
+// 128 registers: 121 / 145) and merges by the whole block at the end 117 / 130; power-of-two scales two at
+// a time 117 / 127.  The copies alone take 97 us and 94 us.
+//   Measured on one GB300 (of the 6791 GB/s copy rate): 256 sequences, 64 heads, e4m3 scales 117 us (82 %),
+// eight long contexts, power-of-two scales 126 us (79 %), 32 sequences of 512 to 4096 rows 22.3 us (47 %),
+// 24 sequences with four queries, D 64 19.2 us (36 %), one of 300 rows 6.3 us (launch and latency); F32 Q at
+// D 256 in pages of 20 rows 16.0 us (14 %: bound by its start and its few warps).
+//
+// Arithmetic (mma.sync m16n8k16, fp32 accumulation: at most 8 query columns share a KV head's tile, an
+// eighth of the rows of a tcgen05 tile, whose 4-bit products would want Q in 4 bits too and cannot scale
+// single rows of V):
+//   - a code times its scale has at most 6 significant bits and is exact in f16.
+//   - Q is scaled per column by a power of two into the upper f16 range: a bf16 or f16 value keeps all
+//     its bits unless it is below 2^-28 of the column's largest.  F32 Q goes as hi + lo (22 bits).
+//   - the denominator is held in fp32; the weights of P.V go to f16 once, times 2^7 against a lazy running
+//     maximum (F32 Q: hi + lo): the largest lies between 2^7 and 2^15.
+//   - rows that do not count get scores of -inf and zero scales of V; a NaN scale of a row that counts
+//     makes NaN what attends it.
 #pragma once
 
 #include <cfloat>
@@ -14,15 +44,11 @@
 
 namespace pd {
 
-#ifndef MXLEAD
-#define MXLEAD 6
-#endif
-#ifndef MXNAP
-#define MXNAP 500
-#endif
-constexpr int kLead = MXLEAD, kNap = MXNAP;
 constexpr float kLazyMaxMx = 8.f;   // the running maximum moves when exceeded by more than 2^8 ...
 constexpr float kWeightUp = 7.f;    // ... and a weight is held times 2^7: at most 2^15 in f16
+// How many stages ahead of another warp of its scheduler a warp lets it catch up, and for how long (ns);
+// 3 to 12 stages and 200 to 1000 ns measure the same.
+constexpr int kLead = 6, kNap = 500;
 
 // ----------------------------------------------------------------------------- geometry
 template <int SB, int D, bool ROWS>

@@ -335,3 +335,54 @@ def test_decode_streams_workspaces_and_unaligned_outputs():
                                 c["li"], out, lse)
     _mx.check_decode(out, lse, ref, 3000, False, 128)
     assert big[0] == 0
+
+
+@pytest.mark.parametrize("q_len", [1, 3])
+@pytest.mark.parametrize("B,P,dt", [(1500, 16, "bf16"), (700, 20, "f32")])
+def test_decode_more_sequences_than_threads(B, P, dt, q_len):
+    """The places of the sequences are summed on the device, several to a thread."""
+    g = torch.Generator().manual_seed(B)
+    lengths = torch.where(torch.rand(B, generator=g) < 0.3, 0, torch.randint(0, 60, (B,), generator=g)).tolist()
+    lengths[-1] = 900
+    c = _decode_case(lengths, 2, 1, 64, P, dt, "e4m3", seed=3, q_len=q_len)
+    _check(c)
+
+
+@pytest.mark.parametrize("Hq,H,q_len", [(16, 1, 1), (32, 1, 1), (24, 1, 1), (8, 2, 8), (64, 2, 1), (3, 1, 7)])
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f32", 64), ("f16", 256)])
+def test_decode_slices_of_columns(Hq, H, q_len, dt, D):
+    """Two to five slices of eight query columns, on warps that walk the pages side by side or not."""
+    c = _decode_case([0, 17, 3000, 640, 5], Hq, H, D, 16, dt, "e8m0", q_len=q_len, seed=Hq)
+    ref = _ref(c)
+    _check(c, ref=ref)
+    _check(c, ref=ref, host_meta=pd.host_meta_of(c["indptr"], c["li"]))
+    _check(c, ref=ref, num_splits=7)
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 7, 40, 200])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_decode_shares_of_every_size(n, dt):
+    """Few rows on many warps, one sequence over all blocks, sequences of one length: the merges."""
+    for lengths in ([n], [16 * n], [16 * n + 1] * 5, [50 * n] * 3, [1, 400 * n, 1]):
+        c = _decode_case(lengths, 8, 2, 128, 16, dt, "e4m3", seed=n)
+        ref = _ref(c)
+        _check(c, ref=ref)
+        _check(c, ref=ref, host_meta=pd.host_meta_of(c["indptr"], c["li"]))
+
+
+def test_decode_right_behind_the_append():
+    """early_inputs: the decode starts under the append that writes the rows it reads."""
+    c = _decode_case([600, 33, 5, 1024] * 8, 8, 2, 128, 16, "bf16", "e4m3", seed=4)
+    ip, B = c["indptr"].tolist(), 32
+    last = torch.tensor([n - 1 for n in c["lengths"]], device=dev)
+    page = c["vals"][torch.tensor([ip[b] + (n - 1) // 16 for b, n in enumerate(c["lengths"])], device=dev)].long()
+    slots = page * 16 + last % 16
+    g = torch.Generator().manual_seed(0)
+    hm = pd.host_meta_of(c["indptr"], c["li"])
+    for i in range(6):
+        k, v = torch.randn(2, B, 2, 128, generator=g).bfloat16().to(dev) * (i + 1)
+        torch.cuda.synchronize()
+        pd.append_paged_kv_mx(c["codes"], c["scales"].view(SC["e4m3"]), k, v, slots)
+        out, lse = _run(c, early_inputs=True, host_meta=hm if i % 2 else None)
+        assert pd.check_device_errors() == "PD_OK"
+        _mx.check_decode(out, lse, _ref(c), 1024, False, 128)
