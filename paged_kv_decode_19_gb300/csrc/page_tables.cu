@@ -12,7 +12,9 @@
 // (8 per page, 12 per token) count from some 10^5 pages on.  So every block makes the scan of all
 // requests itself, in shared memory, and fills its share of the outputs without waiting for another:
 // each output finds its request by a binary search over the sums.  lengths and the ring's state, which
-// every block reads, are moved on by the last block to have read them (a ticket in `state`).
+// every block reads, are moved on by the last block to have read them (a ticket in `state`).  Measured
+// on one GB300, a call: one request 3.8 us, 256 requests 4.9 us, 61 requests with 230,000 pages and
+// 75,000 new tokens 5.2 us (one page a thread at a time, and the ticket before the outputs: 7.2 us).
 #include <algorithm>
 
 #include "common.cuh"
