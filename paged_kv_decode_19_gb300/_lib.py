@@ -708,6 +708,22 @@ def page_pool(num_pages, device="cuda"):
             torch.tensor([0, num_pages, 0, 0], dtype=_I64, device=device))
 
 
+def _tables_refuse(page_table, lengths, new_tokens, state, page_table_indptr, page_table_values, length_info, window):
+    """What is wrong with the arguments of build_page_tables that every call has."""
+    if page_table.dim() != 2 or page_table.dtype != _I32:
+        raise ValueError("page_table must be int32 [B, pages]")
+    B = page_table.shape[0]
+    if lengths.dtype != _I32 or new_tokens.dtype != _I32 or lengths.shape != (B,) or new_tokens.shape != (B,):
+        raise ValueError("lengths and new_tokens must be int32 [B]")
+    if state.dtype != _I64 or state.shape != (4,):
+        raise ValueError("state must be int64 [4]")
+    if page_table_values.dtype != _I32 or page_table_values.dim() != 1:
+        raise ValueError("page_table_values must be int32 [capacity]")
+    if page_table_indptr.dtype != _I32 or page_table_indptr.shape != (B + 1,):
+        raise ValueError("page_table_indptr must be int32 [B+1]")
+    raise ValueError("length_info must be int32 [B], with a window [3, B]")
+
+
 def build_page_tables(page_table, lengths, new_tokens, state, page_size, page_table_indptr, page_table_values,
                       length_info, append_indptr=None, slot_mapping=None, positions=None, *, free_pages=None,
                       window=0, sinks=0, stream=None):
@@ -717,54 +733,59 @@ def build_page_tables(page_table, lengths, new_tokens, state, page_size, page_ta
     page_table_indptr [B+1], page_table_values, length_info ([B], with a window [3, B]), append_indptr
     [B+1] (all int32), slot_mapping int64 [T] and positions int32 [T], as the appends and decodes take
     them.  free_pages int32: the ring of free pages (page_pool); None: page_table holds its pages."""
-    if page_table.dim() != 2 or page_table.dtype != _I32:
-        raise ValueError("page_table must be int32 [B, pages]")
-    B, width = page_table.shape
-    if lengths.dtype != _I32 or new_tokens.dtype != _I32 or lengths.shape != (B,) or new_tokens.shape != (B,):
-        raise ValueError("lengths and new_tokens must be int32 [B]")
-    if state.dtype != _I64 or state.shape != (4,):
-        raise ValueError("state must be int64 [4]")
-    if page_table_values.dtype != _I32 or page_table_values.dim() != 1:
-        raise ValueError("page_table_values must be int32 [capacity]")
-    if page_table_indptr.dtype != _I32 or page_table_indptr.shape != (B + 1,):
-        raise ValueError("page_table_indptr must be int32 [B+1]")
-    if length_info.dtype != _I32 or length_info.shape != ((3, B) if window else (B,)):
-        raise ValueError("length_info must be int32 [B], with a window [3, B]")
-    if append_indptr is not None and (append_indptr.dtype != _I32 or append_indptr.shape != (B + 1,)):
-        raise ValueError("append_indptr must be int32 [B+1]")
-    T = 0
-    if slot_mapping is not None:
-        T = slot_mapping.numel()
-        if slot_mapping.dtype != _I64 or slot_mapping.dim() != 1:
-            raise ValueError("slot_mapping must be int64 [T]")
-    if positions is not None:
-        if positions.dtype != _I32 or positions.dim() != 1 or (slot_mapping is not None and positions.numel() != T):
-            raise ValueError("positions must be int32 [T]")
-        T = positions.numel()
-    if free_pages is not None and (free_pages.dtype != _I32 or free_pages.dim() != 1 or not free_pages.numel()):
-        raise ValueError("free_pages must be int32 [pages]")
-    dev = _device(state)
+    tshape, i32, i64 = page_table.shape, _I32, _I64
+    B = tshape[0] if len(tshape) == 2 else -1
+    of_b, of_b1 = (B,), (B + 1,)
+    slots_at = pos_at = append_at = free_at = None
+    T = n_free = 0
+    if (B < 0 or page_table.dtype != i32 or lengths.dtype != i32 or new_tokens.dtype != i32 or lengths.shape != of_b
+            or new_tokens.shape != of_b or state.dtype != i64 or state.shape != (4,)
+            or page_table_values.dtype != i32 or page_table_values.dim() != 1 or page_table_indptr.dtype != i32
+            or page_table_indptr.shape != of_b1 or length_info.dtype != i32
+            or length_info.shape != ((3, B) if window else of_b)):
+        _tables_refuse(page_table, lengths, new_tokens, state, page_table_indptr, page_table_values, length_info, window)
+    dev, width = state.get_device(), tshape[1]
     stride, last = page_table.stride()
-    if B > 1 and width and (last != 1 and width > 1 or stride < width):
+    if (width > 1 and last != 1) or (B > 1 and stride < width):
         raise ValueError("the rows of page_table must be contiguous, and apart")
-    if B == 1 and width > 1 and last != 1:
-        raise ValueError("the rows of page_table must be contiguous, and apart")
-    at = []
-    for t in (lengths, new_tokens, state, free_pages, page_table_indptr, page_table_values, length_info,
-              append_indptr, slot_mapping, positions):
-        if t is None:
-            at.append(None)
-            continue
-        if t.get_device() != dev or not t.is_contiguous():
-            _refuse(dev, t)
-        at.append(t.data_ptr())
-    if page_table.get_device() != dev:
-        _refuse(dev, page_table)
-    desc = _PACK_TABLES(B, page_size, width, T, window, sinks, 0, 0, stride, page_table_values.numel(),
-                        0 if free_pages is None else free_pages.numel())
+    if append_indptr is not None:
+        if append_indptr.dtype != i32 or append_indptr.shape != of_b1:
+            raise ValueError("append_indptr must be int32 [B+1]")
+        if append_indptr.get_device() != dev or not append_indptr.is_contiguous():
+            _refuse(dev, append_indptr)
+        append_at = append_indptr.data_ptr()
+    if slot_mapping is not None:
+        if slot_mapping.dtype != i64 or slot_mapping.dim() != 1:
+            raise ValueError("slot_mapping must be int64 [T]")
+        if slot_mapping.get_device() != dev or not slot_mapping.is_contiguous():
+            _refuse(dev, slot_mapping)
+        T, slots_at = slot_mapping.numel(), slot_mapping.data_ptr()
+    if positions is not None:
+        n = positions.numel()
+        if positions.dtype != i32 or positions.dim() != 1 or (slot_mapping is not None and n != T):
+            raise ValueError("positions must be int32 [T]")
+        if positions.get_device() != dev or not positions.is_contiguous():
+            _refuse(dev, positions)
+        T, pos_at = n, positions.data_ptr()
+    if free_pages is not None:
+        n_free = free_pages.numel()
+        if free_pages.dtype != i32 or free_pages.dim() != 1 or not n_free:
+            raise ValueError("free_pages must be int32 [pages]")
+        if free_pages.get_device() != dev or not free_pages.is_contiguous():
+            _refuse(dev, free_pages)
+        free_at = free_pages.data_ptr()
+    if not (page_table.get_device() == lengths.get_device() == new_tokens.get_device()
+            == page_table_indptr.get_device() == page_table_values.get_device() == length_info.get_device() == dev
+            and lengths.is_contiguous() and new_tokens.is_contiguous() and state.is_contiguous()
+            and page_table_indptr.is_contiguous() and page_table_values.is_contiguous()
+            and length_info.is_contiguous()):
+        _refuse(dev, page_table, lengths, new_tokens, state, page_table_indptr, page_table_values, length_info)
+    _device(state)
+    desc = _PACK_TABLES(B, page_size, width, T, window, sinks, 0, 0, stride, page_table_values.numel(), n_free)
     st = (_lib or lib()).pd_build_page_tables(
-        page_table.data_ptr(), *at, desc,
-        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        page_table.data_ptr(), lengths.data_ptr(), new_tokens.data_ptr(), state.data_ptr(), free_at,
+        page_table_indptr.data_ptr(), page_table_values.data_ptr(), length_info.data_ptr(), append_at, slots_at,
+        pos_at, desc, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         _check(st)
     return page_table_indptr, page_table_values, length_info
