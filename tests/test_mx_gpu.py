@@ -348,7 +348,7 @@ def test_decode_more_sequences_than_threads(B, P, dt, q_len):
     _check(c)
 
 
-@pytest.mark.parametrize("Hq,H,q_len", [(16, 1, 1), (32, 1, 1), (24, 1, 1), (8, 2, 8), (64, 2, 1), (3, 1, 7)])
+@pytest.mark.parametrize("Hq,H,q_len", [(16, 1, 1), (32, 1, 1), (20, 1, 1), (8, 2, 8), (64, 2, 1), (3, 1, 7)])
 @pytest.mark.parametrize("dt,D", [("bf16", 128), ("f32", 64), ("f16", 256)])
 def test_decode_slices_of_columns(Hq, H, q_len, dt, D):
     """Two to five slices of eight query columns, on warps that walk the pages side by side or not."""
