@@ -1049,6 +1049,9 @@ pd_status pd_append_paged_kv_mx(void* pages, void* scales, const void* k_new, co
   a.n_slots = d.max_pages * d.page_size;
   a.k_scale = d.k_scale;
   a.v_scale = d.v_scale;
+  auto recip = [](float g) { return g >= 0x1p-60f && g <= 0x1p60f ? 1.f / g : 0.f; };
+  a.k_recip = recip(d.k_scale);
+  a.v_recip = recip(d.v_scale);
   a.T = d.T;
   a.H_kv = d.H_kv;
   a.P = d.page_size;

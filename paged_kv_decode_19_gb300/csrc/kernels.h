@@ -104,6 +104,7 @@ struct AppendMxParams {
   long long k_stride, v_stride;  // elements from token to token
   long long n_slots;             // max_pages * P
   float k_scale, v_scale;
+  float k_recip, v_recip;        // 1 / scale rounded, of a scale between 2^-60 and 2^60; else 0
   int T, H_kv, P;
 };
 cudaError_t launch_append_mx(const AppendMxParams& a, int D, int sb, int in_dtype, cudaStream_t st);

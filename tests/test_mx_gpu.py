@@ -92,6 +92,37 @@ def test_append_on_the_borders(sc):
 
 
 @pytest.mark.parametrize("sc", ["e4m3", "e8m0"])
+@pytest.mark.parametrize("ks,vs", [(0.1, 3.0), (1 + 2.0 ** -23, 1 - 2.0 ** -24), (2.0 ** -60, 2.0 ** 60), (7e-19, 1.6e18),
+                                   (1e-30, 1e30), (1.2e-38, 3e38), (1e-44, 0.7)])
+def test_append_on_the_borders_of_a_cache_scale(sc, ks, vs):
+    """x / g on a border or a step or two beside it, for large and small x and g: the fp32 quotient, and
+    a zero's sign."""
+    g = torch.Generator().manual_seed(2)
+    edges = torch.tensor([6.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64)
+    ks, vs = torch.tensor([ks, vs], dtype=torch.float32).tolist()
+    sides = []
+    for scale in (ks, vs):
+        rows = []
+        for e in range(-10, 10):
+            x = (edges.repeat(2) * (1 + torch.randint(8, (1,), generator=g) / 8) * 2.0 ** e * scale).float()
+            up = torch.nextafter(x, torch.tensor(math.inf))
+            x = torch.where(torch.rand(16, generator=g) < 0.5, x, torch.where(torch.rand(16, generator=g) < 0.5, up, torch.nextafter(x, torch.tensor(0.0))))
+            x[15] = 0
+            rows += [x.clamp(max=3.4e38), (torch.randn(16, generator=g).double() * scale).clamp(-3e38, 3e38).float()]
+        rows += [torch.randn(16, generator=g) * 1e-38, torch.full((16,), 1e-44), torch.full((16,), 3.4e38), torch.rand(16, generator=g) * 3.4e38]
+        x = torch.stack(rows[: len(rows) // 4 * 4])
+        sides.append((x * torch.where(torch.rand(x.shape, generator=g) < 0.5, -1.0, 1.0)).view(-1, 1, 64))
+    k, v = sides
+    T = len(k)
+    codes, scales = _mx.cache(-(-T // 4), 1, 4, 64, sc, dev, g)
+    c = dict(k=k.to(dev), v=v.to(dev), slots=torch.arange(T, device=dev), codes=codes, scales=scales, ks=ks, vs=vs, P=4, sc=sc)
+    ref = _append_ref(c)
+    _append(c)
+    assert pd.check_device_errors() == "PD_OK"
+    _same(c, ref)
+
+
+@pytest.mark.parametrize("sc", ["e4m3", "e8m0"])
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 def test_append_non_finite(sc, dt):
     """A non-finite value takes its block alone."""
