@@ -248,9 +248,9 @@ static cudaError_t bs_mma_dispatch(const DecodeParams& p, const CUtensorMap& tm,
 }
 
 // Whether the tiles of a 4-bit decode are gathered row by row: copied whole they are 16 rows of a page.
-// (F32 Q and D 256 are bound by their products: one kernel, which takes any page.)
+// (F32 Q is bound by its products: one kernel, which takes any page.)
 static bool mx_rows(const pd_decode_desc* d) {
-  return d->page_size % 16 != 0 || d->q_dtype == kF32 || d->D == 256;
+  return d->page_size % 16 != 0 || d->q_dtype == kF32;
 }
 
 static cudaError_t mx_dispatch(const DecodeParams& p, int q_dtype, int kv_dtype, bool rows, dim3 grid,

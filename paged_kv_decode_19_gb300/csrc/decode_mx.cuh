@@ -231,10 +231,10 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
 
   // Where this lane's chunk of a tile's codes goes, and of its scales which tile it copies, from where
   // (V's lie behind K's as its codes do) and to where; CS: chunks of a tile's K (or V) scales
-  constexpr int CS = T::kScales / 16;
-  static_assert(ROWS || (NQ * 2 * CS <= 32 && T::kCodes % 512 == 0), "a warp's copies");
+  constexpr int CS = T::kScales / 16, TPC = CS < 16 ? 16 / CS : 1;  // (TPC: tiles whose scales go at once)
+  static_assert(ROWS || (CS <= 16 && (NQ <= TPC || NQ % TPC == 0) && T::kCodes % 512 == 0), "a warp's copies");
   [[maybe_unused]] const int my_chunk = mx_chunk<D>(16 * lane / RB, 16 * lane % RB / 16);
-  [[maybe_unused]] const int my_stile = lane / (2 * CS) % NQ;
+  [[maybe_unused]] const int my_stile = lane / (2 * CS) % (NQ < TPC ? NQ : TPC);
   [[maybe_unused]] const int my_sdst = my_stile * T::kPair + 2 * T::kCodes + 16 * (lane % (2 * CS));
   [[maybe_unused]] const long long v_codes = (long long)p.H_kv * P * RB;
   [[maybe_unused]] const long long my_sbyte =
@@ -398,16 +398,21 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
       const uint8_t* src = shfl_ptr(t_codes, first + t) + 16 * lane;
-      const uint32_t dst = to + t * T::kPair + my_chunk;
+      const uint32_t dst = to + t * T::kPair;
+      // (D 256: 512 bytes are four rows, which turn bit 2 of a chunk's place over)
+      auto at = [&](int j) { return 512 * j + (D == 256 && (j & 1) ? my_chunk ^ 64 : my_chunk); };
 #pragma unroll
-      for (int j = 0; j < T::kCodes / 512; ++j) cp_async_chunk(dst + 512 * j, src + 512 * j);
+      for (int j = 0; j < T::kCodes / 512; ++j) cp_async_chunk(dst + at(j), src + 512 * j);
       src += v_codes;
 #pragma unroll
-      for (int j = 0; j < T::kCodes / 512; ++j) cp_async_chunk(dst + T::kCodes + 512 * j, src + 512 * j);
+      for (int j = 0; j < T::kCodes / 512; ++j) cp_async_chunk(dst + T::kCodes + at(j), src + 512 * j);
     }
-    // scales: of all tiles at once
-    const uint8_t* src = shfl_ptr(t_scales, first + my_stile) + my_sbyte;
-    if (NQ * 2 * CS == 32 || lane < NQ * 2 * CS) cp_async_chunk(to + my_sdst, src);
+    // scales: of TPC tiles at once
+#pragma unroll
+    for (int t = 0; t < NQ; t += TPC) {
+      const uint8_t* src = shfl_ptr(t_scales, first + t + my_stile) + my_sbyte;
+      if (NQ >= TPC || lane < NQ * 2 * CS) cp_async_chunk(to + t * T::kPair + my_sdst, src);
+    }
   };
 
   if (!waited) {  // pages and scales may still be written by the previous kernel until here
@@ -805,11 +810,15 @@ static cudaError_t launch_mx_q(const DecodeParams& p, dim3 grid, cudaStream_t st
                      : launch_mx_t<SB, SPLIT, D, false, ROWS>(p, grid, st, cfg);
 }
 
-// Tiles copied whole: 16-bit Q, D 64 or 128.
+// Tiles copied whole: 16-bit Q.
 template <int SB>
 static cudaError_t launch_mx_tiles(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg) {
-  return p.D == 128 ? launch_mx_q<SB, false, 128, false>(p, grid, st, cfg)
-                    : launch_mx_q<SB, false, 64, false>(p, grid, st, cfg);
+  switch (p.D) {
+    case 64: return launch_mx_q<SB, false, 64, false>(p, grid, st, cfg);
+    case 128: return launch_mx_q<SB, false, 128, false>(p, grid, st, cfg);
+    case 256: return launch_mx_q<SB, false, 256, false>(p, grid, st, cfg);
+  }
+  return cudaErrorInvalidValue;
 }
 // Row by row.
 template <int SB, bool SPLIT>
