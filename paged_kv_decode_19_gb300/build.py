@@ -25,7 +25,8 @@ SOURCES = ["api.cu", "decode_simt.cu", "decode_mma_bf16.cu", "decode_mma_f16.cu"
            "decode_mma_pair_fp8.cu", "merge_append.cu", "decode_noalloc.cu", "decode_bs_e4m3.cu",
            "decode_bs_int.cu", "decode_bs_rows_e4m3.cu", "decode_bs_rows_int.cu", "decode_simt_bs.cu", "append_bs.cu",
            "qk_norm_rope.cu", "decode_mx_e4m3.cu", "decode_mx_e8m0.cu", "decode_mx_rows_e4m3.cu",
-           "decode_mx_rows_e8m0.cu", "decode_mx_f32_e4m3.cu", "decode_mx_f32_e8m0.cu", "append_mx.cu",
+           "decode_mx_rows_e8m0.cu", "decode_mx_f32_e4m3.cu", "decode_mx_f32_e8m0.cu", "decode_mx_rows_f32_e4m3.cu",
+           "decode_mx_rows_f32_e8m0.cu", "append_mx.cu",
            "page_tables.cu"]
 
 

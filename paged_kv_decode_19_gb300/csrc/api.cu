@@ -248,17 +248,15 @@ static cudaError_t bs_mma_dispatch(const DecodeParams& p, const CUtensorMap& tm,
 }
 
 // Whether the tiles of a 4-bit decode are gathered row by row: copied whole they are 16 rows of a page.
-// (F32 Q is bound by its products: one kernel, which takes any page.)
-static bool mx_rows(const pd_decode_desc* d) {
-  return d->page_size % 16 != 0 || d->q_dtype == kF32;
-}
+static bool mx_rows(const pd_decode_desc* d) { return d->page_size % 16 != 0; }
 
 static cudaError_t mx_dispatch(const DecodeParams& p, int q_dtype, int kv_dtype, bool rows, dim3 grid,
                                cudaStream_t st, MmaConfig* cfg) {
-  const bool e4m3 = kv_dtype == PD_MX_E4M3;
-  if (q_dtype == kF32) return e4m3 ? launch_mx_f32_e4m3(p, grid, st, cfg) : launch_mx_f32_e8m0(p, grid, st, cfg);
-  if (rows) return e4m3 ? launch_mx_rows_e4m3(p, grid, st, cfg) : launch_mx_rows_e8m0(p, grid, st, cfg);
-  return e4m3 ? launch_mx_e4m3(p, grid, st, cfg) : launch_mx_e8m0(p, grid, st, cfg);
+  using Launch = cudaError_t (*)(const DecodeParams&, dim3, cudaStream_t, MmaConfig*);
+  static constexpr Launch of[2][2][2] = {{{launch_mx_e4m3, launch_mx_e8m0}, {launch_mx_f32_e4m3, launch_mx_f32_e8m0}},
+                                         {{launch_mx_rows_e4m3, launch_mx_rows_e8m0},
+                                          {launch_mx_rows_f32_e4m3, launch_mx_rows_f32_e8m0}}};
+  return of[rows][q_dtype == kF32][kv_dtype == PD_MX_E8M0](p, grid, st, cfg);
 }
 
 // The pages of an 8-bit cache as TMA boxes of 16 rows of a head, K and V: [max_pages, 2, H_kv, P, D]

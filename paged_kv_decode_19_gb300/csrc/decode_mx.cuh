@@ -689,8 +689,17 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
           const int mt = 4 * w + u, b = mt * VBL / KT;
           const uint32_t a[4] = {mul_h2(ev[0][u], sv[0][b]), mul_h2(od[0][u], sv[0][b]),
                                  mul_h2(ev[1][u], sv[1][b]), mul_h2(od[1][u], sv[1][b])};
-          Mma<__half>::run(oacc[mt], a, pb[i][0], pb[i][1]);
-          if constexpr (SPLIT) Mma<__half>::run(oacc[mt], a, pl[i][0], pl[i][1]);
+          if constexpr (SPLIT) {
+            // (the products' own sum is cut off at 24 bits, which adds up over hundreds of tiles: a tile's
+            // are summed from zero, and rounded to nearest into the output)
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            Mma<__half>::run(part, a, pl[i][0], pl[i][1]);
+            Mma<__half>::run(part, a, pb[i][0], pb[i][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) oacc[mt][e] += part[e];
+          } else {
+            Mma<__half>::run(oacc[mt], a, pb[i][0], pb[i][1]);
+          }
         }
       }
     }
@@ -810,23 +819,12 @@ static cudaError_t launch_mx_q(const DecodeParams& p, dim3 grid, cudaStream_t st
                      : launch_mx_t<SB, SPLIT, D, false, ROWS>(p, grid, st, cfg);
 }
 
-// Tiles copied whole: 16-bit Q.
-template <int SB>
-static cudaError_t launch_mx_tiles(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg) {
+template <int SB, bool SPLIT, bool ROWS>
+static cudaError_t launch_mx(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg) {
   switch (p.D) {
-    case 64: return launch_mx_q<SB, false, 64, false>(p, grid, st, cfg);
-    case 128: return launch_mx_q<SB, false, 128, false>(p, grid, st, cfg);
-    case 256: return launch_mx_q<SB, false, 256, false>(p, grid, st, cfg);
-  }
-  return cudaErrorInvalidValue;
-}
-// Row by row.
-template <int SB, bool SPLIT>
-static cudaError_t launch_mx_rows(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg) {
-  switch (p.D) {
-    case 64: return launch_mx_q<SB, SPLIT, 64, true>(p, grid, st, cfg);
-    case 128: return launch_mx_q<SB, SPLIT, 128, true>(p, grid, st, cfg);
-    case 256: return launch_mx_q<SB, SPLIT, 256, true>(p, grid, st, cfg);
+    case 64: return launch_mx_q<SB, SPLIT, 64, ROWS>(p, grid, st, cfg);
+    case 128: return launch_mx_q<SB, SPLIT, 128, ROWS>(p, grid, st, cfg);
+    case 256: return launch_mx_q<SB, SPLIT, 256, ROWS>(p, grid, st, cfg);
   }
   return cudaErrorInvalidValue;
 }

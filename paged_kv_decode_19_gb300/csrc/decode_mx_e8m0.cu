@@ -1,10 +1,11 @@
-// Instantiations of the 4-bit tensor-core decode (decode_mx.cuh) for power-of-two scales, one per 32 dims, tiles copied whole.
+// Instantiations of the 4-bit tensor-core decode (decode_mx.cuh) for power-of-two scales, one per 32 dims:
+// 16-bit Q, tiles copied whole.
 #include "decode_mx.cuh"
 
 namespace pd {
 
 cudaError_t launch_mx_e8m0(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg) {
-  return launch_mx_tiles<32>(p, grid, st, cfg);
+  return launch_mx<32, false, false>(p, grid, st, cfg);
 }
 
 }  // namespace pd

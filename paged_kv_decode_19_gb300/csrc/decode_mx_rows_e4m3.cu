@@ -1,11 +1,11 @@
-// Instantiations of the 4-bit tensor-core decode (decode_mx.cuh) for e4m3 scales, one per 16 dims, tiles
-// gathered row by row, 16-bit Q.
+// Instantiations of the 4-bit tensor-core decode (decode_mx.cuh) for e4m3 scales, one per 16 dims:
+// 16-bit Q, tiles gathered row by row.
 #include "decode_mx.cuh"
 
 namespace pd {
 
 cudaError_t launch_mx_rows_e4m3(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg) {
-  return launch_mx_rows<16, false>(p, grid, st, cfg);
+  return launch_mx<16, false, true>(p, grid, st, cfg);
 }
 
 }  // namespace pd

@@ -110,14 +110,16 @@ struct AppendMxParams {
 cudaError_t launch_append_mx(const AppendMxParams& a, int D, int sb, int in_dtype, cudaStream_t st);
 // Warps of a block of the decode, one block an SM: what its registers allow.
 constexpr int mx_warps(bool q_f32, int D) { return q_f32 || D == 256 ? 8 : 12; }
-// ... and the decode (decode_mx.cuh): 16-bit Q (p.q_bf16), page size a multiple of 16 (tiles copied
-// whole); or 16-bit / F32 Q, any D and page size, tiles gathered row by row.
+// ... and the decode (decode_mx.cuh): 16-bit (p.q_bf16) or F32 Q; tiles copied whole, of pages of a
+// multiple of 16 rows, or gathered row by row.
 cudaError_t launch_mx_e4m3(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
 cudaError_t launch_mx_e8m0(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
-cudaError_t launch_mx_rows_e4m3(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
-cudaError_t launch_mx_rows_e8m0(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
 cudaError_t launch_mx_f32_e4m3(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
 cudaError_t launch_mx_f32_e8m0(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_mx_rows_e4m3(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_mx_rows_e8m0(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_mx_rows_f32_e4m3(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
+cudaError_t launch_mx_rows_f32_e8m0(const DecodeParams& p, dim3 grid, cudaStream_t st, MmaConfig* cfg);
 
 // build_page_tables
 constexpr int kTableThreads = 512;
