@@ -22,15 +22,18 @@
 // a time 117 / 127.  The copies alone take 97 us and 94 us.
 //   Measured on one GB300 (of the 6791 GB/s copy rate): 256 sequences, 64 heads, e4m3 scales 117 us (82 %),
 // eight long contexts, power-of-two scales 126 us (79 %), 32 sequences of 512 to 4096 rows 22.3 us (47 %),
-// 24 sequences with four queries, D 64 19.2 us (36 %), one of 300 rows 6.3 us (launch and latency); F32 Q at
-// D 256 in pages of 20 rows 16.0 us (14 %: bound by its start and its few warps).
+// 24 sequences with four queries, D 64 19.2 us (36 %), one of 300 rows 6.3 us (launch and latency); seven short
+// ones with F32 Q, D 256, in pages of 20 rows 17.1 us (13 %: bound by its start and its few warps).  256
+// sequences in other forms: bf16 D 256 219 us (87 %; its rows gathered one by one 257), F32 Q 162 us (60 %;
+// gathered 186; each product twice), pages of 20 rows 145 us.
 //
 // Arithmetic (mma.sync m16n8k16, fp32 accumulation: at most 8 query columns share a KV head's tile, an
 // eighth of the rows of a tcgen05 tile, whose 4-bit products would want Q in 4 bits too and cannot scale
 // single rows of V):
 //   - a code times its scale has at most 6 significant bits and is exact in f16.
 //   - Q is scaled per column by a power of two into the upper f16 range: a bf16 or f16 value keeps all
-//     its bits unless it is below 2^-28 of the column's largest.  F32 Q goes as hi + lo (22 bits).
+//     its bits unless it is below 2^-28 of the column's largest.  F32 Q goes as hi + lo (22 bits), and a
+//     tile's outputs are added to the sum by rounded additions (the products' own cut off).
 //   - the denominator is held in fp32; the weights of P.V go to f16 once, times 2^7 against a lazy running
 //     maximum (F32 Q: hi + lo): the largest lies between 2^7 and 2^15.
 //   - rows that do not count get scores of -inf and zero scales of V; a NaN scale of a row that counts

@@ -390,6 +390,22 @@ def test_decode_slices_of_columns(Hq, H, q_len, dt, D):
     _check(c, ref=ref, num_splits=7)
 
 
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 32), (128, 20), (256, 16), (256, 12)])
+def test_decode_f32_sums_over_many_tiles(D, P):
+    """Equal values of V come out as they are, whatever the weights: what is off is the sums.  n tiles of
+    16 rows go into a sum one after the other, each rounded to nearest: an error that is even over +-2^-24
+    of the sum, and independent, so that six deviations of all are 6 2^-24 sqrt(n / 3).  (Each rounded
+    down instead: n 2^-24, seven times the bound.)  A weight's split into two f16 parts, of 22 bits, and the
+    denominator's own sums add the same again at most."""
+    n = 2500
+    c = _decode_case([16 * n, 16 * n - 5], 8, 1, D, P, "f32", "e4m3", seed=D, qs=0.3)
+    c["codes"][:, 1] = 0x22   # 1.0
+    c["scales"][:, 1] = 0x38  # 1.0
+    out, _ = _run(c, num_splits=1)
+    assert pd.check_device_errors() == "PD_OK"
+    assert (out.double() - 1).abs().max().item() <= 2 * 6 * 2.0 ** -24 * math.sqrt(n / 3)
+
+
 @pytest.mark.parametrize("n", [1, 2, 3, 7, 40, 200])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_decode_shares_of_every_size(n, dt):
