@@ -624,10 +624,10 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       st_d[1] *= a1;
       st_m[0] = mn0;
       st_m[1] = mn1;
-      nm[0] = fmaf(-mn0, cs0, kWeightUp);
-      nm[1] = fmaf(-mn1, cs1, kWeightUp);
-      th[0] = mn0 + kLazyMaxMx / cs0;
-      th[1] = mn1 + kLazyMaxMx / cs1;
+      // (a column without a row so far keeps 0 and its threshold: cs FLT_MAX may be infinite, and the weight
+      // of a row that does not count would be NaN)
+      if (mn0 != -FLT_MAX) nm[0] = fmaf(-mn0, cs0, kWeightUp), th[0] = mn0 + kLazyMaxMx / cs0;
+      if (mn1 != -FLT_MAX) nm[1] = fmaf(-mn1, cs1, kWeightUp), th[1] = mn1 + kLazyMaxMx / cs1;
 #pragma unroll
       for (int mt = 0; mt < KT; ++mt) {
         oacc[mt][0] *= a0;
