@@ -115,9 +115,11 @@ struct SinkAdj {
 __device__ __forceinline__ SinkAdj apply_sink(const DecodeParams& p, int h, float l) {
   if (!p.sink) return {1.f, l};
   const float ls = __ldg(p.sink + h) * 1.4426950408889634f;
-  if (ls == -INFINITY) return {1.f, l};  // (a head without one; of an empty sequence it would be 0 / 0)
+  if (ls == -INFINITY) return {1.f, l};  // (a head without one)
+  // no rows: the sink alone, however low it is (against kEmptyM as a maximum it would vanish too, 0 / 0)
+  if (l <= kEmptyM) return {ls == ls ? 0.f : ls, ls};
   const float m = fmaxf(l, ls);
-  const float a = l <= kEmptyM ? 0.f : exp2f(l - m);  // weight of the attended rows (NaN: NaN)
+  const float a = exp2f(l - m);  // weight of the attended rows (NaN: NaN)
   const float den = a + exp2f(ls - m);
   return {a / den, m + log2f(den)};
 }
