@@ -73,6 +73,7 @@ struct DeviceState {
   int bs_occupancy[3][4][2][3][2] = {};
   // of the 4-bit kernels: [e4m3 / e8m0 scales][16-bit / F32 Q][whole tiles / rows][D][single / multi-query]
   int mx_occupancy[2][2][2][3][2] = {};
+  std::atomic<bool> tables_ready{false};  // build_page_tables' kernel may use the shared memory of the largest batch
 };
 constexpr int kMaxDevices = 64;
 static DeviceState g_dev[kMaxDevices];
@@ -1085,6 +1086,11 @@ pd_status pd_build_page_tables(int32_t* page_table, int32_t* lengths, const int3
   DeviceState* ds = nullptr;
   pd_status st = device_state(&ds);
   if (st != PD_OK) return st;
+  if (!ds->tables_ready.load(std::memory_order_acquire)) {  // (two threads may both do it: it is the same)
+    const cudaError_t e = prepare_page_tables();
+    if (e != cudaSuccess) return cuda_fail(e, "page tables set-up");
+    ds->tables_ready.store(true, std::memory_order_release);
+  }
   TableParams a{};
   a.table = page_table;
   a.lengths = lengths;

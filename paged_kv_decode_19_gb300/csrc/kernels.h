@@ -140,6 +140,7 @@ struct TableParams {
   long long table_stride;
   int B, P, max_pages, max_rows, window, sinks, values_cap, C, T, most_tokens;
 };
+cudaError_t prepare_page_tables();  // once per device, before its first launch
 cudaError_t launch_page_tables(const TableParams& a, int num_sms, cudaStream_t st);
 
 // qk_norm_rope

@@ -221,17 +221,20 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_cons
   }
 }
 
+constexpr int smem_bytes(int B) { return (B + 4 * (B + 1)) * (int)sizeof(int); }
+
+// The shared memory of the largest batch is allowed once per device: a limit set by every call to its own size could
+// fall, between another thread's and its launch, below what that one asks for.
+cudaError_t prepare_page_tables() {
+  return cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kMaxTableB));
+}
+
 cudaError_t launch_page_tables(const TableParams& a, int num_sms, cudaStream_t st) {
-  const int smem = (a.B + 4 * (a.B + 1)) * (int)sizeof(int);
   // four outputs a thread, at most one block an SM
   const long long items = std::max<long long>(std::min<long long>(a.values_cap, (long long)a.B * a.max_pages),
                                                   a.slots || a.positions ? a.T : 0);
   const long long blocks = std::min<long long>(num_sms, std::max<long long>(1, (items + 4 * kThreads - 1) / (4 * kThreads)));
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(page_tables_kernel, dim3((unsigned)blocks), dim3(kThreads), smem, st, a);
+  return launch_pdl(page_tables_kernel, dim3((unsigned)blocks), dim3(kThreads), smem_bytes(a.B), st, a);
 }
 
 }  // namespace pd

@@ -1,0 +1,48 @@
+"""build_page_tables: calls of several host threads, and slot maps without room."""
+import threading
+
+import pytest
+import torch
+
+import paged_kv_decode_19_gb300 as pd
+
+pytestmark = pytest.mark.gpu
+dev = "cuda"
+
+
+def _args(B, T):
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32, device=dev)  # noqa: E731
+    return dict(page_table=torch.arange(2 * B, dtype=torch.int32, device=dev).view(B, 2), lengths=i32(B) + 5,
+                new_tokens=i32(B) + 1, state=torch.zeros(4, dtype=torch.int64, device=dev), page_size=16,
+                page_table_indptr=i32(B + 1), page_table_values=i32(2 * B), length_info=i32(B),
+                slot_mapping=torch.zeros(T, dtype=torch.int64, device=dev), positions=i32(T))
+
+
+def test_host_threads_with_batches_of_different_size():
+    """Batches whose sums need different amounts of shared memory, from two threads at once."""
+    calls, failed = 3000, []
+
+    def work(B):
+        try:
+            a, s = _args(B, B), torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            a["new_tokens"].zero_()
+            torch.cuda.synchronize()
+            for _ in range(calls):
+                pd.build_page_tables(**a, stream=s)
+            a["new_tokens"].fill_(1)
+            torch.cuda.synchronize()
+            pd.build_page_tables(**a, stream=s)
+            torch.cuda.synchronize()
+            assert (a["lengths"] == 6).all() and (a["length_info"] == 6).all()
+            assert torch.equal(a["slot_mapping"], 32 * torch.arange(B, device=dev) + 5)
+        except Exception as e:  # noqa: BLE001 (shown by the assertion below)
+            failed.append((B, e))
+
+    threads = [threading.Thread(target=work, args=(B,)) for B in (3000, 8192, 2500, 5000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    assert pd.check_device_errors() == "PD_OK"
