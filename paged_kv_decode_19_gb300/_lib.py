@@ -759,14 +759,15 @@ def build_page_tables(page_table, lengths, new_tokens, state, page_size, page_ta
             raise ValueError("slot_mapping must be int64 [T]")
         if slot_mapping.get_device() != dev or not slot_mapping.is_contiguous():
             _refuse(dev, slot_mapping)
-        T, slots_at = slot_mapping.numel(), slot_mapping.data_ptr()
+        # (one of no entries has no address: any other stands for it, so that it still holds no token)
+        T, slots_at = slot_mapping.numel(), slot_mapping.data_ptr() or state.data_ptr()
     if positions is not None:
         n = positions.numel()
         if positions.dtype != i32 or positions.dim() != 1 or (slot_mapping is not None and n != T):
             raise ValueError("positions must be int32 [T]")
         if positions.get_device() != dev or not positions.is_contiguous():
             _refuse(dev, positions)
-        T, pos_at = n, positions.data_ptr()
+        T, pos_at = n, positions.data_ptr() or state.data_ptr()
     if free_pages is not None:
         n_free = free_pages.numel()
         if free_pages.dtype != i32 or free_pages.dim() != 1 or not n_free:

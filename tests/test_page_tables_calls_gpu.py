@@ -46,3 +46,18 @@ def test_host_threads_with_batches_of_different_size():
         t.join()
     assert not failed, failed
     assert pd.check_device_errors() == "PD_OK"
+
+
+@pytest.mark.parametrize("given", [("slot_mapping",), ("positions",), ("slot_mapping", "positions")])
+def test_slot_maps_without_room(given):
+    """A slot map (or positions) of no entries holds no new token: a step that brings some changes nothing."""
+    a = _args(3, 0)
+    for name in {"slot_mapping", "positions"} - set(given):
+        a[name] = None
+    pd.build_page_tables(**a)
+    assert pd.check_device_errors() == "PD_ERR_BAD_LENGTH"
+    assert a["lengths"].tolist() == [5, 5, 5] and a["page_table_indptr"].tolist() == [0, 0, 0, 0]
+    a["new_tokens"].copy_(torch.tensor([0, -5, -1]))
+    pd.build_page_tables(**a)
+    assert pd.check_device_errors() == "PD_OK"
+    assert a["lengths"].tolist() == [5, 0, 4] and a["page_table_indptr"].tolist() == [0, 1, 1, 2]
