@@ -41,8 +41,11 @@ DTYPE_CODES = {
 }
 # codes of a block-scaled cache (the _bs entry points)
 BS_DTYPE_CODES = {torch.float8_e4m3fn: 3, torch.int8: 4}
-# a 4-bit cache, by the type of its scales, and the dims that share one (the _mx entry points)
-MX_DTYPE_CODES = {torch.float8_e4m3fn: (5, 16), torch.float8_e8m0fnu: (6, 32)}
+# a 4-bit cache, by the type of its scales, and the dims that share one (the _mx entry points); power-of-two
+# scales want a torch that has their type
+MX_DTYPE_CODES = {torch.float8_e4m3fn: (5, 16)}
+if hasattr(torch, "float8_e8m0fnu"):
+    MX_DTYPE_CODES[torch.float8_e8m0fnu] = (6, 32)
 DTYPE_NAMES = {"f32": 0, "f16": 1, "bf16": 2, "e4m3": 3}
 
 # Every entry point declared in include/pageddecode.h.
