@@ -122,6 +122,14 @@ __device__ __forceinline__ uint32_t mul_hi(uint32_t a, uint32_t s) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __high2half2(*reinterpret_cast<const __half2*>(&s)));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// (x - m) c + w of two columns side by side, each step rounded as alone
+__device__ __forceinline__ float2 scaled_differences(float x0, float x1, float2 m, float2 c, float w) {
+  float2 r;
+  asm("{\n .reg .b64 x, m, c, w;\n mov.b64 x, {%2, %3};\n mov.b64 m, {%4, %5};\n mov.b64 c, {%6, %7};\n mov.b64 w, {%8, %8};\n"
+      " add.rn.f32x2 x, x, m;\n fma.rn.f32x2 x, x, c, w;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y) : "f"(x0), "f"(x1), "f"(-m.x), "f"(-m.y), "f"(c.x), "f"(c.y), "f"(w));
+  return r;
+}
 __device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* x, int from) {
   return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), from));
 }
@@ -470,8 +478,9 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     // 2^(14 - e) and its inverse, both normal: e is kept in [-100, 126]
     const int e = min(max((int)((__float_as_uint(amax) >> 23) & 255) - 127, -100), 126);
     const float up = copysignf(__uint_as_float((unsigned)(127 + 14 - e) << 23), p.score_scale);
-    // (at least the least normal float, so that the -inf of a row that does not count stays one)
-    const float cs = fmaxf(__uint_as_float((unsigned)(127 - 14 + e) << 23) * fabsf(p.score_scale), FLT_MIN);
+    // (at least the least normal float, so that the -inf of a row that does not count stays one, and finite, so
+    // that the maximum's difference of 0 does)
+    const float cs = fminf(fmaxf(__uint_as_float((unsigned)(127 - 14 + e) << 23) * fabsf(p.score_scale), FLT_MIN), FLT_MAX);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -485,8 +494,9 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   }
 
   // The running maxima m are of the products before the column's factor cs (> 0); weights are
-  // 2^(cs s + nm) with nm = kWeightUp - cs m.  They move when a product is above th
-  float st_m[2] = {-FLT_MAX, -FLT_MAX}, nm[2] = {0.f, 0.f}, st_d[2] = {0.f, 0.f};
+  // 2^(cs (s - m) + kWeightUp): by differences, which are finite and exact next to the maximum however large
+  // cs and m are.  They move when a product is above th.
+  float st_m[2] = {-FLT_MAX, -FLT_MAX}, st_d[2] = {0.f, 0.f};
   float th[2] = {-FLT_MAX, -FLT_MAX};
   float oacc[KT][4];
 #pragma unroll
@@ -624,10 +634,9 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       st_d[1] *= a1;
       st_m[0] = mn0;
       st_m[1] = mn1;
-      // (a column without a row so far keeps 0 and its threshold: cs FLT_MAX may be infinite, and the weight
-      // of a row that does not count would be NaN)
-      if (mn0 != -FLT_MAX) nm[0] = fmaf(-mn0, cs0, kWeightUp), th[0] = mn0 + kLazyMaxMx / cs0;
-      if (mn1 != -FLT_MAX) nm[1] = fmaf(-mn1, cs1, kWeightUp), th[1] = mn1 + kLazyMaxMx / cs1;
+      // (rounded down: never more than 2^kLazyMaxMx above the maximum; a column without a row so far keeps its own)
+      if (mn0 != -FLT_MAX) th[0] = __fadd_rd(mn0, kLazyMaxMx / cs0);
+      if (mn1 != -FLT_MAX) th[1] = __fadd_rd(mn1, kLazyMaxMx / cs1);
 #pragma unroll
       for (int mt = 0; mt < KT; ++mt) {
         oacc[mt][0] *= a0;
@@ -642,7 +651,11 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     for (int i = 0; i < NQ; ++i) {
       float pr[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) pr[e] = fast_exp2(fmaf(sc[i][e], e & 1 ? cs1 : cs0, nm[e & 1]));
+      for (int e = 0; e < 4; e += 2) {
+        const float2 x = scaled_differences(sc[i][e], sc[i][e + 1], make_float2(st_m[0], st_m[1]), make_float2(cs0, cs1), kWeightUp);
+        pr[e] = fast_exp2(x.x);
+        pr[e + 1] = fast_exp2(x.y);
+      }
       st_d[0] += pr[0] + pr[2];
       st_d[1] += pr[1] + pr[3];
       // P^T as a B fragment: rows 2 q4, 2 q4 + 1 (+ 8) of column g_id
@@ -734,7 +747,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const bool empty = st_d[h] == 0.f;
-    lse[h] = empty ? kEmptyM : log2f(st_d[h]) - nm[h];
+    lse[h] = empty ? kEmptyM : fmaf(st_m[h], h ? cs1 : cs0, log2f(st_d[h]) - kWeightUp);
     const float inv = empty ? 0.f : p.out_scale / st_d[h];
 #pragma unroll
     for (int mt = 0; mt < KT; ++mt) oacc[mt][h] *= inv, oacc[mt][h + 2] *= inv;
