@@ -109,19 +109,23 @@ __device__ __forceinline__ int col_head(const DecodeParams& p, int hk, int c) {
 // A learned sink logit of query head h joins the softmax as one more score with a zero
 // value row.  Given a final, sink-free output (o, lse = l; l = kEmptyM when no row was
 // attended), the result is o * scale with lse: the merge of (o, l) with (0, sink log2 e).
+// `empty`: whether no row was attended, where scores may lie below kEmptyM.
 struct SinkAdj {
   float scale, lse;
 };
-__device__ __forceinline__ SinkAdj apply_sink(const DecodeParams& p, int h, float l) {
+__device__ __forceinline__ SinkAdj apply_sink(const DecodeParams& p, int h, float l, bool empty) {
   if (!p.sink) return {1.f, l};
   const float ls = __ldg(p.sink + h) * 1.4426950408889634f;
   if (ls == -INFINITY) return {1.f, l};  // (a head without one)
   // no rows: the sink alone, however low it is (against kEmptyM as a maximum it would vanish too, 0 / 0)
-  if (l <= kEmptyM) return {ls == ls ? 0.f : ls, ls};
+  if (empty) return {ls == ls ? 0.f : ls, ls};
   const float m = fmaxf(l, ls);
   const float a = exp2f(l - m);  // weight of the attended rows (NaN: NaN)
   const float den = a + exp2f(ls - m);
   return {a / den, m + log2f(den)};
+}
+__device__ __forceinline__ SinkAdj apply_sink(const DecodeParams& p, int h, float l) {
+  return apply_sink(p, h, l, l <= kEmptyM);
 }
 
 // SeqInfo from a sequence's raw fields (page-table offsets i0, i1; last page length;

@@ -48,7 +48,7 @@
 namespace pd {
 
 constexpr float kLazyMaxMx = 8.f;   // the running maximum moves when exceeded by more than 2^8 ...
-constexpr float kWeightUp = 7.f;    // ... and a weight is held times 2^7: at most 2^15 in f16
+constexpr float kWeightUp = 7.f, kWeightDown = 0x1p-7f;  // ... and a weight is held times 2^7: at most 2^15 in f16
 // How many stages ahead of another warp of its scheduler a warp lets it catch up, and for how long (ns);
 // 3 to 12 stages and 200 to 1000 ns measure the same.
 constexpr int kLead = 6, kNap = 500;
@@ -122,12 +122,12 @@ __device__ __forceinline__ uint32_t mul_hi(uint32_t a, uint32_t s) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __high2half2(*reinterpret_cast<const __half2*>(&s)));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-// (x - m) c + w of two columns side by side, each step rounded as alone
-__device__ __forceinline__ float2 scaled_differences(float x0, float x1, float2 m, float2 c, float w) {
+// (x + n) c + w of two columns side by side, each step rounded as alone
+__device__ __forceinline__ float2 scaled_sums(float x0, float x1, float2 n, float2 c, float w) {
   float2 r;
-  asm("{\n .reg .b64 x, m, c, w;\n mov.b64 x, {%2, %3};\n mov.b64 m, {%4, %5};\n mov.b64 c, {%6, %7};\n mov.b64 w, {%8, %8};\n"
-      " add.rn.f32x2 x, x, m;\n fma.rn.f32x2 x, x, c, w;\n mov.b64 {%0, %1}, x;\n}"
-      : "=f"(r.x), "=f"(r.y) : "f"(x0), "f"(x1), "f"(-m.x), "f"(-m.y), "f"(c.x), "f"(c.y), "f"(w));
+  asm("{\n .reg .b64 x, n, c, w;\n mov.b64 x, {%2, %3};\n mov.b64 n, {%4, %5};\n mov.b64 c, {%6, %7};\n mov.b64 w, {%8, %8};\n"
+      " add.rn.f32x2 x, x, n;\n fma.rn.f32x2 x, x, c, w;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y) : "f"(x0), "f"(x1), "f"(n.x), "f"(n.y), "f"(c.x), "f"(c.y), "f"(w));
   return r;
 }
 __device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* x, int from) {
@@ -174,7 +174,9 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   constexpr int RB = T::RB, NB = T::NB, SR = T::SR;
   constexpr int KW = KB / 4;  // words
   extern __shared__ uint8_t s_raw[];
-  __shared__ float s_plse[NW][2][kMaxGroupPerCta]; // lse of each warp's partial states: first, last segment
+  // of each warp's partial states (first, last segment), by column: maximum and sum, factor
+  __shared__ float2 s_pmd[NW][2][kMaxGroupPerCta];
+  __shared__ float s_pcs[NW][2][kMaxGroupPerCta];
   __shared__ SegmentMerge s_merge[NW + 4];
   __shared__ int s_n_merge, s_done[NW];             // s_done: stages each warp has computed
   __shared__ WorkerStart s_start[NW];
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   // The running maxima m are of the products before the column's factor cs (> 0); weights are
   // 2^(cs (s - m) + kWeightUp): by differences, which are finite and exact next to the maximum however large
   // cs and m are.  They move when a product is above th.
-  float st_m[2] = {-FLT_MAX, -FLT_MAX}, st_d[2] = {0.f, 0.f};
+  float st_n[2] = {FLT_MAX, FLT_MAX}, st_d[2] = {0.f, 0.f};  // (st_n: -m)
   float th[2] = {-FLT_MAX, -FLT_MAX};
   float oacc[KT][4];
 #pragma unroll
@@ -628,12 +630,12 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       t1 = fmaxf(t1, fmaxf(sc[i][1], sc[i][3]));
     }
     if (__any_sync(0xffffffffu, t0 > th[0] || t1 > th[1])) {
-      const float mn0 = fmaxf(st_m[0], max_over_groups(t0)), mn1 = fmaxf(st_m[1], max_over_groups(t1));
-      const float a0 = fast_exp2((st_m[0] - mn0) * cs0), a1 = fast_exp2((st_m[1] - mn1) * cs1);
+      const float mn0 = fmaxf(-st_n[0], max_over_groups(t0)), mn1 = fmaxf(-st_n[1], max_over_groups(t1));
+      const float a0 = fast_exp2((-st_n[0] - mn0) * cs0), a1 = fast_exp2((-st_n[1] - mn1) * cs1);
       st_d[0] *= a0;
       st_d[1] *= a1;
-      st_m[0] = mn0;
-      st_m[1] = mn1;
+      st_n[0] = -mn0;
+      st_n[1] = -mn1;
       // (rounded down: never more than 2^kLazyMaxMx above the maximum; a column without a row so far keeps its own)
       if (mn0 != -FLT_MAX) th[0] = __fadd_rd(mn0, kLazyMaxMx / cs0);
       if (mn1 != -FLT_MAX) th[1] = __fadd_rd(mn1, kLazyMaxMx / cs1);
@@ -652,7 +654,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
       float pr[4];
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        const float2 x = scaled_differences(sc[i][e], sc[i][e + 1], make_float2(st_m[0], st_m[1]), make_float2(cs0, cs1), kWeightUp);
+        const float2 x = scaled_sums(sc[i][e], sc[i][e + 1], make_float2(st_n[0], st_n[1]), make_float2(cs0, cs1), kWeightUp);
         pr[e] = fast_exp2(x.x);
         pr[e + 1] = fast_exp2(x.y);
       }
@@ -742,13 +744,13 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   st_d[1] = sum_over_groups(st_d[1]);
 
   // ---------------------------------------------------------------- finish the segment
-  // This thread holds columns 2 q4 (o0, o2) and 2 q4 + 1 (o1, o3), dims RL g_id .. + RL - 1.
-  float lse[2];
+  int ln;  // (the lane's number, read here: nothing that follows is worked out before the loop)
+  asm volatile("mov.u32 %0, %%laneid;" : "=r"(ln)::"memory");
+  const int gf = ln >> 2, qf4 = ln & 3;
+  // This thread holds columns 2 qf4 (o0, o2) and 2 qf4 + 1 (o1, o3), dims RL gf .. + RL - 1.
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const bool empty = st_d[h] == 0.f;
-    lse[h] = empty ? kEmptyM : fmaf(st_m[h], h ? cs1 : cs0, log2f(st_d[h]) - kWeightUp);
-    const float inv = empty ? 0.f : p.out_scale / st_d[h];
+    const float inv = st_d[h] == 0.f ? 0.f : p.out_scale / st_d[h];
 #pragma unroll
     for (int mt = 0; mt < KT; ++mt) oacc[mt][h] *= inv, oacc[mt][h + 2] *= inv;
   }
@@ -760,13 +762,16 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
     float* const o = state_of(warp, side);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int j = 2 * q4 + h;
+      const int j = 2 * qf4 + h;
       if (j >= hcount) continue;
 #pragma unroll
       for (int x = 0; x < RL / 4; ++x)
-        reinterpret_cast<float4*>(o + j * D + RL * g_id)[x] =
+        reinterpret_cast<float4*>(o + j * D + RL * gf)[x] =
             make_float4(oacc[2 * x][h], oacc[2 * x][h + 2], oacc[2 * x + 1][h], oacc[2 * x + 1][h + 2]);
-      if (g_id == 0) s_plse[warp][side][j] = lse[h];
+      if (gf == 0) {
+        s_pmd[warp][side][j] = make_float2(-st_n[h], st_d[h] * kWeightDown);
+        s_pcs[warp][side][j] = h ? cs1 : cs0;
+      }
     }
     const int wi = lane < NW && lane % zg == warp % zg ? lane : -1;
     const long long w0 = wi >= 0 ? s_start[wi].x0 : 0, w1 = wi >= 0 ? s_start[wi].x1 : 0;
@@ -782,21 +787,22 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   if (mine) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int j = 2 * q4 + h;
+      const int j = 2 * qf4 + h;
       if (j >= hcount) continue;
       const size_t row = col_row<MQ>(p, sg.b, hk, c0 + j);
-      float inv = 1.f;
+      const bool empty = st_d[h] == 0.f;
+      float inv = 1.f, lse = empty ? kEmptyM : fmaf(-st_n[h], h ? cs1 : cs0, log2f(st_d[h]) - kWeightUp);
       if (p.sink) {
-        const SinkAdj sa = apply_sink(p, col_head<MQ>(p, hk, c0 + j), lse[h]);
+        const SinkAdj sa = apply_sink(p, col_head<MQ>(p, hk, c0 + j), lse, empty);
         inv = sa.scale;
-        lse[h] = sa.lse;
+        lse = sa.lse;
       }
 #pragma unroll
       for (int x = 0; x < RL / 4; ++x)
-        store_four(p, row * D + RL * g_id + 4 * x,
+        store_four(p, row * D + RL * gf + 4 * x,
                    make_float4(oacc[2 * x][h] * inv, oacc[2 * x][h + 2] * inv, oacc[2 * x + 1][h] * inv,
                                oacc[2 * x + 1][h + 2] * inv));
-      if (g_id == 0) p.lse[row] = lse[h];
+      if (gf == 0) p.lse[row] = lse;
     }
   }
   }  // ua < ub
@@ -804,7 +810,7 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
   }  // segments
   if (!waited) pdl_wait();  // (a worker without units: what the block merges may still follow it)
   if (lane == 0) *(volatile int*)&s_done[warp] = INT_MAX / 2;
-  merge_states<D, MQ, NW>(p, s_merge, s_n_merge, s_plse, state_of);
+  merge_states<D, MQ, NW>(p, s_merge, s_n_merge, s_pmd, s_pcs, state_of);
 }
 
 // ----------------------------------------------------------------------------- launch

@@ -3,6 +3,7 @@
 // workers of a block and the blocks of a segment leave.
 #pragma once
 
+#include <cfloat>
 #include <type_traits>
 
 #include "decode_common.cuh"
@@ -157,9 +158,11 @@ __device__ __forceinline__ void line_starts(const DecodeParams& p, WorkerStart* 
 }
 
 // ----------------------------------------------------------------------------- merges at the block's end
-// A warp leaves its part of a segment that it shares as a state (normalised outputs and lse) in shared
-// memory and goes on.  At its end the block merges its states of each such segment (lse = M + log2 sum
-// 2^(lse_s - M), out = sum 2^(lse_s - M) o_s / sum 2^(lse_s - M)), all segments at once.  If the block
+// A warp leaves its part of a segment that it shares as a state (per column normalised outputs, the maximum m of
+// the products before the column's factor cs, and d = sum 2^(cs (s - m))) in shared memory and goes on.  At its
+// end the block merges its states of each such segment (M = max m_s, w_s = d_s 2^(cs (m_s - M)), out = sum w_s
+// o_s / sum w_s), all segments at once.  Differences of maxima stand where a log-sum-exp would be rounded to
+// the size of the scores; a state without rows has d = 0 and m = -FLT_MAX.  If the block
 // holds all units of a segment that is the result; else it publishes the state and adds its units to the
 // segment's counter, and the block that completes the count merges the blocks' states.  Such code runs
 // once, from a cold instruction cache, and each dependent step costs its latency: it is kept short, and
@@ -209,24 +212,33 @@ struct SegmentMerge {
 template <int NW>
 struct MergeScratch {
   float weight[NW + 4][NW][kMaxGroupPerCta];  // of a segment's states, by column
-  float lse[NW + 4][kMaxGroupPerCta];
+  float2 md[NW + 4][kMaxGroupPerCta];         // of the block's state
+  float cs[NW + 4][kMaxGroupPerCta];
   bool all[NW + 4];  // the segment is complete, and its blocks' states are to be merged
 };
-// (s_merge, s_n: the segments; state_of(warp, side), s_plse: the states, of a warp's first and last segment.)
+// (s_merge, s_n: the segments; state_of(warp, side), s_pmd, s_pcs: the states, of a warp's first and last segment.
+// A published state's m and d lie in p.part_lse, a pair a column: two slots per block and slice side by side, where
+// the workspace has two per warp.)
 template <int D, bool MQ, int NW, typename StateOf>
 __device__ __forceinline__ void merge_states(const DecodeParams& p, const SegmentMerge (&s_merge)[NW + 4], const int& s_n,
-                                           const float (&s_plse)[NW][2][kMaxGroupPerCta], StateOf state_of) {
+                                           const float2 (&s_pmd)[NW][2][kMaxGroupPerCta],
+                                           const float (&s_pcs)[NW][2][kMaxGroupPerCta], StateOf state_of) {
   constexpr int NT = NW * 32, G8 = kMaxGroupPerCta, kItems = G8 * (D / 4);  // of a segment: a column and four dims each
+  static_assert(NW >= 8, "room for the published pairs: at most four slices side by side");
   __shared__ MergeScratch<NW> s;
   const int tid = threadIdx.x;
   __syncthreads();
   const int n = s_n;
   if (n == 0) return;
-  auto put = [&](int w, int j, int d, float4 o, float l, bool final) {
+  float2* const part_md = reinterpret_cast<float2*>(p.part_lse);
+  auto put = [&](int w, int j, int d, float4 o, float2 md, bool final) {
     const PartMerge& e = s_merge[w].e;
     if (final) {
+      const bool empty = md.y == 0.f;
+      float l = kEmptyM;
+      if ((p.sink || d == 0) && !empty) l = fmaf(md.x, s.cs[w][j], log2f(md.y));
       if (p.sink) {
-        const SinkAdj sa = apply_sink(p, col_head<MQ>(p, e.hk, e.c0 + j), l);
+        const SinkAdj sa = apply_sink(p, col_head<MQ>(p, e.hk, e.c0 + j), l, empty);
         o = make_float4(o.x * sa.scale, o.y * sa.scale, o.z * sa.scale, o.w * sa.scale);
         l = sa.lse;
       }
@@ -237,27 +249,32 @@ __device__ __forceinline__ void merge_states(const DecodeParams& p, const Segmen
       const SegmentBlocks& sb = s_merge[w].blocks;
       const long long at = slot_of(e, sb, (int)(blockIdx.x - sb.first)) + j;
       *reinterpret_cast<float4*>(p.part_o + at * D + d) = o;
-      if (d == 0) p.part_lse[at] = l;
+      if (d == 0) part_md[at] = md;
     }
   };
   // the block's own states: their weights, then the sums
   for (int x = tid; x < n * G8; x += NT) {
     const int w = x / G8, j = x % G8;
-    float l[NW], M = kEmptyM, den = 0.f;
+    const unsigned from = s_merge[w].from, late = s_merge[w].late;
+    const int one = __ffs(from) - 1;
+    const float cs = s_pcs[one][(late >> one) & 1][j];
+    float2 md[NW];
+    float M = -FLT_MAX, den = 0.f;
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
-      l[i] = (s_merge[w].from >> i) & 1 ? s_plse[i][(s_merge[w].late >> i) & 1][j] : kEmptyM;
-      M = fmaxf(M, l[i]);
+      md[i] = (from >> i) & 1 ? s_pmd[i][(late >> i) & 1][j] : make_float2(-FLT_MAX, 0.f);
+      M = fmaxf(M, md[i].x);
     }
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
-      l[i] = l[i] <= kEmptyM ? 0.f : fast_exp2(l[i] - M);  // (NaN counts)
-      den += l[i];
+      md[i].y *= fast_exp2((md[i].x - M) * cs);
+      den += md[i].y;
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
-    for (int i = 0; i < NW; ++i) s.weight[w][i][j] = l[i] * inv;
-    s.lse[w][j] = den == 0.f ? kEmptyM : M + log2f(den);
+    for (int i = 0; i < NW; ++i) s.weight[w][i][j] = md[i].y * inv;
+    s.md[w][j] = make_float2(M, den);
+    s.cs[w][j] = cs;
   }
   __syncthreads();
   for (int x = tid; x < n * kItems; x += NT) {
@@ -272,7 +289,7 @@ __device__ __forceinline__ void merge_states(const DecodeParams& p, const Segmen
       const float4 o = *reinterpret_cast<const float4*>(state_of(i, (late >> i) & 1) + j * D + d);
       acc = make_float4(fmaf(x_, o.x, acc.x), fmaf(x_, o.y, acc.y), fmaf(x_, o.z, acc.z), fmaf(x_, o.w, acc.w));
     }
-    put(w, j, d, acc, s.lse[w][j], s_merge[w].in_block == s_merge[w].e.n);
+    put(w, j, d, acc, s.md[w][j], s_merge[w].in_block == s_merge[w].e.n);
   }
   if (p.mode != kSchedBalanced) return;
   __syncthreads();
@@ -298,39 +315,40 @@ __device__ __forceinline__ void merge_states(const DecodeParams& p, const Segmen
     const PartMerge& e = s_merge[w].e;
     if (j >= e.hcount || !s.all[w]) continue;
     const SegmentBlocks sb = s_merge[w].blocks;
-    float M = kEmptyM, den = 0.f;
+    const float cs = s.cs[w][j];
+    float M = -FLT_MAX, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    // four states' sums and rows in flight together (eight, twice the cold code: 32 sequences 22.4 us for 21.7)
 #pragma unroll 1
-    for (int i0 = 0; i0 < sb.n; i0 += 8) {  // eight states' lse and rows in flight together
-      float l[8];
-      float4 o[8];
+    for (int i0 = 0; i0 < sb.n; i0 += 4) {
+      float2 md[4];
+      float4 o[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const long long at = slot_of(e, sb, min(i0 + i, sb.n - 1)) + j;
-        l[i] = __ldcg(p.part_lse + at);
+        md[i] = __ldcg(part_md + at);
         o[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
       }
       float m = M;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i0 + i >= sb.n || !holds_units(e, sb, i0 + i)) l[i] = kEmptyM;
-        m = fmaxf(m, l[i]);
+      for (int i = 0; i < 4; ++i) {
+        if (i0 + i >= sb.n || !holds_units(e, sb, i0 + i)) md[i] = make_float2(-FLT_MAX, 0.f);
+        m = fmaxf(m, md[i].x);
       }
-      const float f = fast_exp2(M - m);
+      const float f = fast_exp2((M - m) * cs);
       M = m;
       den *= f;
       acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (l[i] <= kEmptyM) continue;  // (NaN counts)
-        const float x_ = fast_exp2(l[i] - M);
+      for (int i = 0; i < 4; ++i) {
+        if (md[i].y == 0.f) continue;  // (of a block without units: not written)
+        const float x_ = md[i].y * fast_exp2((md[i].x - M) * cs);
         den += x_;
         acc = make_float4(fmaf(x_, o[i].x, acc.x), fmaf(x_, o[i].y, acc.y), fmaf(x_, o[i].z, acc.z), fmaf(x_, o[i].w, acc.w));
       }
     }
-    const bool empty = den == 0.f;
-    const float inv = empty ? 0.f : 1.f / den;
-    put(w, j, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), empty ? kEmptyM : M + log2f(den), true);
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    put(w, j, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), make_float2(M, den), true);
   }
 }
 

@@ -65,7 +65,9 @@ def _ref(c, sm, sink):
 def _check(c, sm=1.0, sink=None, out_dt=None, **kw):
     """A weight is exact but for f16 (half a step, 2^-11 of it; F32 Q: 22 bits), ex2 and its argument (2^-20 and
     18 2^-24 in log2 units); the sums of few rows as in _mx.check_decode.  lse: the column's factor, its product
-    with the maximum and the last sum, half a step of fp32 each."""
+    with the maximum and the last sum, half a step of fp32 each.  A sink times log2 e and the log-sum-exp that it
+    joins are fp32 numbers: the weight of the one against the other is off by ln 2 times their roundings, half a
+    step of the sink's and three of the lse's, all within 4 2^-24 of the larger."""
     out, lse = _run(c, out_dt, sm_scale=sm, sink=sink, **kw)
     assert pd.check_device_errors() == "PD_OK"
     o, l, A, vmax = _ref(c, sm, sink)
@@ -74,6 +76,9 @@ def _check(c, sm=1.0, sink=None, out_dt=None, **kw):
     split = c["Q"].dtype == torch.float32
     rows = max(c["lengths"])
     rel = 2.0 ** -17 + (2.0 ** -22 if split else 2.0 ** -11) + 2 * (17 * rows / 16 + 40) * 2.0 ** -24
+    if sink is not None:
+        low = torch.where(sink.isinf(), 0.0, sink.double()).abs() * LOG2E
+        rel = rel + math.log(2) * 4 * 2.0 ** -24 * torch.maximum(low, l.abs())[..., None]
     tol = A * rel + o.abs() * torch.finfo(out.dtype).eps / 2 + rows * 2.0 ** -32 * vmax[..., None]
     if out.dtype == torch.float16:
         tol = tol + 2.0 ** -25
@@ -93,7 +98,8 @@ def test_the_largest_scores_alone_count(dt, D, P, q_len, sign, e):
         top = torch.where((r * 7 // 5) % 29 == 3, 7, step)       # and 7 (6.0) here and there
         return torch.where(r > n // 3, top, step) if sign > 0 else 8 - top  # (negative: the smallest is largest)
     c = _case([700, 33, 1, 2100], D, P, dt, q_len, k, q=(sign * 2.0 ** e, 0.0), seed=e)
-    _check(c, num_splits=1)
+    for n in (0, 1, 9):
+        _check(c, num_splits=n)
     _check(c, num_splits=1, out_dt=torch.float32)
 
 
@@ -106,4 +112,21 @@ def test_small_differences_of_large_scores(q_len, sign, dt, e):
     def k(r, n):  # (under a scale of 2, codes 0.5 and 0, 3, 6)
         return 1 + 16 * torch.where(r >= n - 12, 7, torch.where(r >= n - 162, 5, 0))
     c = _case([1662, 1700, 3000], 128, 16, dt, q_len, k, scale=0x40, q=(sign * 2.0 ** e, 1.0), seed=e)
-    _check(c, num_splits=1, out_dt=torch.float32)
+    for n in (1, 0, 9):
+        _check(c, num_splits=n, out_dt=torch.float32)
+
+
+@pytest.mark.parametrize("dt,q0,D,P", [("bf16", -2.0 ** 17, 128, 16), ("f32", -2.0 ** 17, 64, 20), ("f32", -34660.0, 128, 16),
+                                       ("f16", -40000.0, 256, 16), ("f32", -34660.0, 128, 7)])
+@pytest.mark.parametrize("q_len", [1, 2])
+def test_scores_below_the_empty_mark(q_len, dt, q0, D, P):
+    """Every score, or some shares' all, below -5e4 in log2 units, the log-sum-exp of a sequence without
+    rows: the rows count, however they are split."""
+    def k(r, n):
+        return 1 + 16 * (r * 13 // 7 % 8)
+    c = _case([700, 33, 0, 1, 3000, 5000], D, P, dt, q_len, k, scale=0x40, q=(q0, 1.0), seed=1)
+    sink = torch.tensor([q0, q0 + 9, q0 - 3, 1.5 * q0, -math.inf, q0 + 12], device=dev)
+    for s in (None, sink):
+        for n in (1, 0, 5, 64):
+            _check(c, num_splits=n, sink=s)
+        _check(c, sink=s, host_meta=pd.host_meta_of(c["indptr"], c["li"]))
