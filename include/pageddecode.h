@@ -404,7 +404,9 @@ pd_status pd_append_paged_kv_mx(void* pages, void* scales, const void* k_new, co
  * Arithmetic: tensor cores; codes times scales are exact in f16.  F16 and BF16 Q enter exactly (scaled
  * per head by a power of two; elements under 2^-28 of the head's largest lose bits), and the weights
  * 2^(s - n) are rounded once to f16; F32 Q and its weights go as sums of two f16 parts (22 bits).  Sums
- * in fp32.  Fastest where page_size is a multiple of 16 and Q 16-bit.
+ * in fp32, rounded to nearest; of 16-bit Q within 4096 rows of a share in the tensor cores, which cut off (6e-6).
+ * Scores of any size: weights are taken from differences to the largest.  Fastest where page_size is a
+ * multiple of 16 and Q 16-bit.
  */
 pd_status pd_batch_decode_paged_kv_mx(const void* Q, const void* pages, const void* scales,
                                       const int32_t* page_table_indptr,

@@ -77,6 +77,11 @@ struct MxTile {
 template <int SB, int D, bool ROWS, int NW>
 constexpr int mx_smem_bytes() { return NW * (MxTile<SB, D, ROWS>::kRing + MxTile<SB, D, ROWS>::kState) + 128; }
 
+// 16-bit Q: tiles whose products are summed in the accumulators, which cut every sum off (by 5e-8 of it a tile, always
+// towards zero).  Such sums are added, rounded to nearest, in local memory: 6e-6 is what the cutting adds up to, however long
+// the share (32 tiles at a time would be 1e-6, but 64 already cost D 256 10 %: the local memory leaves L2 in between).
+constexpr int kSumTiles = 256;
+
 // Row of the tile that fragment row g (0..7; g + 8: the row + 8) holds, and byte offset of the 16-byte
 // chunk c of row r of a tile in shared memory.  Chosen so that the rows of K that one phase of lanes
 // reads (those of g = 2i, 2i + 1; D 64: of four g), and the rows of V that the quad lanes read (those
@@ -506,10 +511,19 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
 
   [[maybe_unused]] unsigned full_left = 0;  // `full` from tile k on
 
+  // this lane's accumulators' sums of the share so far, kSumTiles tiles at a time, against the maxima -sums_n
+  [[maybe_unused]] float4 sums_local[SPLIT ? 1 : KT];
+  [[maybe_unused]] float4* sums = sums_local;
+  if constexpr (!SPLIT) asm volatile("" : "+l"(sums));  // (kept out of the registers)
+  [[maybe_unused]] float sums_n[2] = {FLT_MAX, FLT_MAX};
+
+#pragma unroll 1
+  for (int k = 0; k < k_end;) {
   // NQ tiles from the ring: their chains of loads, products and exponentials are independent and
   // overlap in the warp, and share the vote and the rescale
+  const int k_next = SPLIT ? k_end : min(k + kSumTiles, k_end);
 #pragma unroll 1
-  for (int k = 0; k < k_end; k += NQ) {
+  for (; k < k_next; k += NQ) {
     cp_async_group_wait<NST - 1>();
     __syncwarp();  // every lane's copies, and what was written beside them
     const uint8_t* const stage = my_ring + cst * T::kStage;
@@ -739,6 +753,25 @@ __global__ void __launch_bounds__(NW * 32, BLOCKS) decode_mx_kernel(const __grid
         if (stages > least + kLead) __nanosleep(kNap);
       }
     }
+  }
+  if constexpr (!SPLIT) {
+    if (__builtin_expect(k_end > kSumTiles, 0)) {
+      const bool first = k <= kSumTiles;
+      const float a0 = fast_exp2((st_n[0] - sums_n[0]) * cs0), a1 = fast_exp2((st_n[1] - sums_n[1]) * cs1);
+      sums_n[0] = st_n[0];
+      sums_n[1] = st_n[1];
+#pragma unroll
+      for (int mt = 0; mt < KT; ++mt) {
+        float4 x = first ? make_float4(0.f, 0.f, 0.f, 0.f) : sums[mt];
+        x = make_float4(fmaf(x.x, a0, oacc[mt][0]), fmaf(x.y, a1, oacc[mt][1]), fmaf(x.z, a0, oacc[mt][2]), fmaf(x.w, a1, oacc[mt][3]));
+        if (k < k_end) {
+          sums[mt] = x;
+          x = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        oacc[mt][0] = x.x, oacc[mt][1] = x.y, oacc[mt][2] = x.z, oacc[mt][3] = x.w;
+      }
+    }
+  }
   }
   st_d[0] = sum_over_groups(st_d[0]);
   st_d[1] = sum_over_groups(st_d[1]);
