@@ -376,7 +376,7 @@ pd_status pd_batch_decode_paged_kv_bs(const void* Q, const void* pages, const fl
  * Arguments (device pointers): k_new, v_new [T, H_kv, D] of in_dtype, token t at element t * k_stride
  * (v_stride), heads contiguous; slot_mapping [T] int64 as in pd_append_paged_kv (negative: skipped; at
  * or beyond max_pages * P: skipped, PD_ERR_BAD_SLOT; two tokens of one call on one slot leave it
- * undefined).  The decode may follow with PD_DECODE_EARLY_INPUTS.
+ * undefined).  The decode may follow with PD_DECODE_EARLY_INPUTS if T > 0 (no kernel is enqueued for 0).
  */
 typedef struct {
   int32_t T;                  /* new tokens */

@@ -594,7 +594,9 @@ def batch_decode_paged_kv_mx(Q, pages, scales, page_table_indptr, page_table_val
                              workspace=None, early_inputs=False, sink=None, host_meta=None, stream=None):
     """pd_batch_decode_paged_kv_mx: decode over 4-bit pages [max_pages, 2, H_kv, P, D / 2] (uint8,
     two e2m1 codes a byte) with scales [max_pages, 2, H_kv, P, D / 16] float8_e4m3fn or
-    [..., D / 32] float8_e8m0fnu, times k_scale and v_scale.  Q [B, H_qo, D], or [B, q_len, H_qo, D]
+    [..., D / 32] float8_e8m0fnu, times k_scale and v_scale.  Power-of-two scales must lie in
+    [2^-14, 2^13], as append_paged_kv_mx writes them (a smaller one counts as 0, a larger one as NaN; the
+    cache's k_scale and v_scale move the range).  Q [B, H_qo, D], or [B, q_len, H_qo, D]
     for several query tokens per sequence (causal among them); output like Q, lse [B, H_qo] or
     [B, q_len, H_qo].  K is used as stored and Q as given: rotate both with qk_norm_rope."""
     shape, pshape, sshape = Q.shape, pages.shape, scales.shape

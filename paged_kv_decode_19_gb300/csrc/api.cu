@@ -33,9 +33,11 @@ constexpr int kSegCostTiles = PD_SEG_COST_TILES;
 #define PD_BS_SEG_COST_TILES 8
 #endif
 constexpr int kBsSegCostTiles = PD_BS_SEG_COST_TILES;
-// And of the 4-bit one, in tiles times head dim: 8 tiles at D 128, 16 at D 64.  Measured (us; 256 and 32
-// sequences at D 128, 24 with four queries at D 64): half of it 117.0, 23.4 and 20.9, as it is 116.7,
-// 22.3 and 19.2, twice 120.3, 23.4 and 20.7.
+// And of the 4-bit one, in tiles times head dim: 8 tiles at D 128, 16 at D 64, 4 at D 256.  Measured (us): half of
+// it / as it is / twice.  D 128, 256 and 32 sequences: 117.0 / 117.1 / 120.7, 22.9 / 21.8 / 23.0; F32 Q, the same:
+// 162.4 / 164.1 / 166.5, 27.6 / 28.5 / 29.1; D 64, 256 sequences and 24 with four queries: 69.8 / 70.3 / 75.5,
+// 20.5 / 18.7 / 20.0; D 256, 256, 32 and 24 with four: 223.9 / 217.5 / 216.2, 38.3 / 36.6 / 36.3, 50.6 / 49.3 /
+// 47.5.  (D 256 alone would take twice of it, by 1 to 4 %.)
 constexpr int kMxSegCostDims = 1024;
 constexpr size_t kWsAlign = 256;
 

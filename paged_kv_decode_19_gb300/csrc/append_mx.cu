@@ -12,9 +12,11 @@
 // step of the quotient (and a / 6 likewise of e4m3's borders).
 //
 // Bound by the bytes (2 D elements in, D (1 + 2 / block) bytes out per token and head), by the loads
-// under way and by the instructions: rows need nothing but their own values, so a thread takes 16 dims, which share a scale (two threads of 32), of a token's K and of its
-// V, with one slot and one address for both, and the stores alone wait for the slot.  No quotient is a
-// division.  Measured on one GB300: 8192 tokens of 8 heads of 128 from bf16 8.4 us (75 % of the copy rate
+// under way and by the instructions: rows need nothing but their own values, so a thread takes 16 dims, which share
+// a scale (two threads of 32), of a token's K and of its V, with one slot and one address for both, and the
+// stores alone wait for the slot.  Quotients are corrected products: without a cache scale there is no division;
+// with one a thread divides its largest magnitude, of K and of V, and every value only if the scale is outside
+// 2^-60 .. 2^60 or that quotient is 2^120 or more, or NaN.  Measured on one GB300: 8192 tokens of 8 heads of 128 from bf16 8.4 us (75 % of the copy rate
 // on 43 MB; with IEEE divisions 16.7, with K and V on threads of their own 9.8), with power-of-two scales
 // 7.9, from fp32 13.0 (87 %; K and V apart 12.4), under a cache scale of 0.37 10.4 (with divisions by it
 // 13.8); 256 tokens 1.5 us, 1777 of 4 heads of 64, a third of them skipped, 1.8 us (launches).

@@ -359,6 +359,8 @@ __device__ __forceinline__ void merge_states(const DecodeParams& p, const Segmen
 // the block that completes the count merges the blocks' states.  So a segment split over the
 // four warps of a block never leaves it, and one over several blocks costs a state per block.
 // Called by the whole block, after every warp has written its entries; s0: the block's first start.
+// (The 8-bit decode's: four warps and log-sum-exps, segment after segment.  merge_states above rounds in another
+// order, so this one stays, and with it that decode's results bit for bit.)
 template <int D, bool MQ, int NW, typename StateOf>
 __device__ __forceinline__ void merge_parts(const DecodeParams& p, PartEntry (&s_part)[NW][2],
                                             float (&s_plse)[NW][2][kMaxGroupPerCta], int (&s_last)[2 * NW],
