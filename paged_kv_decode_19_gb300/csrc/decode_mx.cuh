@@ -19,23 +19,26 @@
 // masks and rare paths out of the loop 128 / 137; one block of twelve warps an SM, in which the older
 // warps of a scheduler do not run ahead of the younger (three blocks of four: 128 / 137; sixteen warps of
 // 128 registers: 121 / 145) and merges by the whole block at the end 117 / 130; power-of-two scales two at
-// a time 117 / 127.  The copies alone take 97 us and 94 us.
+// a time 117 / 127; weights of two columns an instruction, nothing of a segment's end worked out before its loop
+// 117 / 123.  The copies alone take 97 us and 94 us.
 //   Measured on one GB300 (of the 6791 GB/s copy rate): 256 sequences, 64 heads, e4m3 scales 117 us (82 %),
-// eight long contexts, power-of-two scales 126 us (79 %), 32 sequences of 512 to 4096 rows 22.3 us (47 %),
-// 24 sequences with four queries, D 64 19.2 us (36 %), one of 300 rows 6.3 us (launch and latency); seven short
-// ones with F32 Q, D 256, in pages of 20 rows 17.1 us (13 %: bound by its start and its few warps).  256
-// sequences in other forms: bf16 D 256 219 us (87 %; its rows gathered one by one 257), F32 Q 162 us (60 %;
-// gathered 186; each product twice), pages of 20 rows 145 us.
+// eight long contexts, power-of-two scales 123 us (81 %), 32 sequences of 512 to 4096 rows 21.9 us (48 %),
+// 24 sequences with four queries, D 64 18.9 us (36 %), one of 300 rows 6.5 us (launch and latency); seven short
+// ones with F32 Q, D 256, in pages of 20 rows 17.2 us (13 %: bound by its start and its few warps).  256
+// sequences in other forms: bf16 D 256 217 us (88 %; its rows gathered one by one 257), F32 Q 164 us (59 %;
+// gathered 186; each product twice), pages of 20 rows 144 us.
 //
 // Arithmetic (mma.sync m16n8k16, fp32 accumulation: at most 8 query columns share a KV head's tile, an
 // eighth of the rows of a tcgen05 tile, whose 4-bit products would want Q in 4 bits too and cannot scale
 // single rows of V):
 //   - a code times its scale has at most 6 significant bits and is exact in f16.
 //   - Q is scaled per column by a power of two into the upper f16 range: a bf16 or f16 value keeps all
-//     its bits unless it is below 2^-28 of the column's largest.  F32 Q goes as hi + lo (22 bits), and a
-//     tile's outputs are added to the sum by rounded additions (the products' own cut off).
+//     its bits unless it is below 2^-28 of the column's largest.  F32 Q goes as hi + lo (22 bits).
 //   - the denominator is held in fp32; the weights of P.V go to f16 once, times 2^7 against a lazy running
-//     maximum (F32 Q: hi + lo): the largest lies between 2^7 and 2^15.
+//     maximum (F32 Q: hi + lo): the largest lies between 2^7 and 2^15.  They are taken from differences to the
+//     maximum, and partial states carry the maximum, so that only those differences matter, at any size.
+//   - the products' own sum is cut off towards zero: it holds at most kSumTiles tiles (F32 Q: one), and such
+//     sums are added by rounded additions.
 //   - rows that do not count get scores of -inf and zero scales of V; a NaN scale of a row that counts
 //     makes NaN what attends it.
 #pragma once
@@ -77,9 +80,9 @@ struct MxTile {
 template <int SB, int D, bool ROWS, int NW>
 constexpr int mx_smem_bytes() { return NW * (MxTile<SB, D, ROWS>::kRing + MxTile<SB, D, ROWS>::kState) + 128; }
 
-// 16-bit Q: tiles whose products are summed in the accumulators, which cut every sum off (by 5e-8 of it a tile, always
-// towards zero).  Such sums are added, rounded to nearest, in local memory: 6e-6 is what the cutting adds up to, however long
-// the share (32 tiles at a time would be 1e-6, but 64 already cost D 256 10 %: the local memory leaves L2 in between).
+// 16-bit Q: tiles whose products are summed in the accumulators, which cut every sum off (by 5e-8 of it a tile).
+// Such sums are added, rounded to nearest, in local memory: the cutting adds up to 6e-6, however long the share.
+// (64 tiles at a time would be 2e-6, but cost D 256 10 %: the local memory has left L2 when it is next touched.)
 constexpr int kSumTiles = 256;
 
 // Row of the tile that fragment row g (0..7; g + 8: the row + 8) holds, and byte offset of the 16-byte
