@@ -64,12 +64,21 @@ def _dist():
 
 
 # Sources the tensor-core decode's launches depend on (its kernel, the shared device code
-# and the host planner); the SIMT kernel, merge/append kernels, the workspace arenas and the
-# block-scaled cache's kernels do not change what it reads or writes.
+# and the host planner); the SIMT kernel, merge/append kernels, the workspace arenas, the
+# block-scaled and 4-bit caches' kernels and the page tables' do not change what it reads or writes.
 _TRAFFIC_EXCLUDE = ("decode_simt.cu", "merge_append.cu", "decode_noalloc.cu", "arena.h",
                     "decode_simt.cuh", "decode_simt_bs.cu", "decode_bs.cuh", "decode_bs_e4m3.cu",
                     "decode_bs_int.cu", "decode_bs_rows_e4m3.cu", "decode_bs_rows_int.cu",
-                    "append_bs.cu", "qk_norm_rope.cu", "bs_plan.h")
+                    "append_bs.cu", "qk_norm_rope.cu", "bs_plan.h", "decode_parts.cuh",
+                    "decode_mx.cuh", "decode_mx_e4m3.cu", "decode_mx_e8m0.cu", "decode_mx_f32_e4m3.cu",
+                    "decode_mx_f32_e8m0.cu", "decode_mx_rows_e4m3.cu", "decode_mx_rows_e8m0.cu",
+                    "decode_mx_rows_f32_e4m3.cu", "decode_mx_rows_f32_e8m0.cu", "append_mx.cu",
+                    "page_tables.cu")
+
+
+def _traffic_sources() -> list[str]:
+    d = os.path.join(ROOT, "paged_kv_decode_19_gb300", "csrc")
+    return [n for n in sorted(os.listdir(d)) if n.endswith((".cu", ".cuh", ".h")) and n not in _TRAFFIC_EXCLUDE]
 
 
 def _sources_digest() -> str:
@@ -78,10 +87,9 @@ def _sources_digest() -> str:
     import hashlib
     d = os.path.join(ROOT, "paged_kv_decode_19_gb300", "csrc")
     h = hashlib.sha256()
-    for name in sorted(os.listdir(d)):
-        if name.endswith((".cu", ".cuh", ".h")) and name not in _TRAFFIC_EXCLUDE:
-            h.update(name.encode())
-            h.update(open(os.path.join(d, name), "rb").read())
+    for name in _traffic_sources():
+        h.update(name.encode())
+        h.update(open(os.path.join(d, name), "rb").read())
     return h.hexdigest()
 
 
