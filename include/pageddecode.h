@@ -127,8 +127,9 @@ typedef struct {
  * The caller asserts that the kernel enqueued just before the decode writes none of
  * those inputs, and that everything enqueued before that kernel is complete once it
  * starts: both hold when it is pd_append_paged_kv (which writes only the pages and,
- * itself, waits for its predecessor before it lets the decode start).  The decode then
- * runs its start-up (work split scan, page-table and Q loads) under the append.
+ * itself, waits for its predecessor before it lets the decode start; of no tokens it
+ * enqueues nothing, and the kernel before it counts).  The decode then runs its start-up
+ * (work split scan, page-table and Q loads) under the append.
  */
 #define PD_DECODE_EARLY_INPUTS 1
 

@@ -1,4 +1,7 @@
-"""build_page_tables: calls of several host threads, and slot maps without room."""
+"""build_page_tables: calls of several host threads, a first call under capture, and slot maps without room."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -8,6 +11,7 @@ import paged_kv_decode_19_gb300 as pd
 
 pytestmark = pytest.mark.gpu
 dev = "cuda"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _args(B, T):
@@ -61,3 +65,28 @@ def test_slot_maps_without_room(given):
     pd.build_page_tables(**a)
     assert pd.check_device_errors() == "PD_OK"
     assert a["lengths"].tolist() == [5, 0, 4] and a["page_table_indptr"].tolist() == [0, 1, 1, 2]
+
+
+FIRST = """
+import sys
+import torch
+sys.path.insert(0, %r)
+import paged_kv_decode_19_gb300 as pd
+from tests.test_page_tables_calls_gpu import _args
+a = _args(%d, %d)
+s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph, stream=s):
+    pd.build_page_tables(**a)
+assert (a["lengths"] == 5).all()
+for n in (6, 7):
+    graph.replay()
+    torch.cuda.synchronize()
+    assert pd.check_device_errors() == "PD_OK" and (a["lengths"] == n).all() and (a["length_info"] == n).all()
+"""
+
+
+@pytest.mark.parametrize("B", [3, 8192])
+def test_the_first_call_of_a_process_is_captured(B):
+    r = subprocess.run([sys.executable, "-c", FIRST % (ROOT, B, B)], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
